@@ -250,6 +250,7 @@ def _label_grad(logits, e, S, at, coef, scale):
 def _plain_logp(case, s):
     scale = case["scale"]
     logp, lse, e, S, at = _label_logp(s["logits"], s["labels"], scale)
+    lse = torch.where(s["labels"] >= 0, lse, 0.0)      # a row that is not scored has neither
     if not case["backward"]:
         return logp.float(), lse.float()
     coef = torch.where(s["labels"] >= 0, s["grad"], 0.0)
@@ -400,6 +401,7 @@ def exact(case, seed):
         lse = torch.logsumexp(z.detach() * case["scale"], 1)
         labels = s["labels"].long()
         keep = labels >= 0
+        lse = torch.where(keep, lse, 0.0)
         logp = torch.where(keep, logq[torch.arange(T, device=z.device), labels.clamp(min=0)], 0.0)
         if not case["backward"]:
             return logp.detach(), lse
