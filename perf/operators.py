@@ -201,7 +201,7 @@ def _own(case, s):
         logp, lse = sk.token_logprobs(s["logits"], s["labels"], scale=case["scale"])
         if not case["backward"]:
             return logp, lse
-        return logp, lse, sk.token_logprobs_backward(s["logits"], s["labels"], lse, s["grad"],
+        return logp, lse, sk.token_logprobs_backward(s["logits"], s["labels"], s["grad"],
                                                      scale=case["scale"])
     if case["op"] == "policy":
         return sk.policy_loss(s["logits"], s["labels"], s["offsets"], s["old"], s["adv"],
