@@ -10,6 +10,9 @@ Entry points (same names as the C ABI):
   potentials(X, Y, a, b, eps, iters, ...)   -> f, g, cost
   plan_coo(X, Y, a, b, f, g, eps, ...)      -> rows, cols, vals, pair_offsets
   loss_grad(X, Y, rows, cols, vals, pair_offsets, ...) -> loss, dX
+Losses over rows of logits (include/sinkhorn_losses.h, module ``losses``):
+  token_logprobs, token_logprobs_backward, policy_loss, preference_loss,
+  distill_loss, balance_loss
 """
 from __future__ import annotations
 
@@ -20,6 +23,8 @@ import torch
 
 __all__ = ["SinkhornError", "potentials", "potentials_noalloc", "plan_coo", "loss_grad",
            "workspace_bytes",
+           "token_logprobs", "token_logprobs_backward", "policy_loss", "preference_loss",
+           "distill_loss", "balance_loss", "losses_workspace_bytes",
            "library_path", "load_library"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -95,6 +100,7 @@ def load_library():
     lib.sinkhorn_status_string.restype = ctypes.c_char_p
     lib.sinkhorn_last_error.argtypes = []
     lib.sinkhorn_last_error.restype = ctypes.c_char_p
+    losses.declare(lib)
     _lib = lib
     return lib
 
@@ -506,3 +512,9 @@ def hvp(X, Y, a, b, f, g, eps: float, V, cg_iters: int = 100, workspace=None, ou
                           ws.numel(), _stream())
     _check(rc)
     return HV, res
+
+
+# the losses over logits build on the names above
+from . import losses  # noqa: E402
+from .losses import (LOSS_EXPORTS, balance_loss, distill_loss, losses_workspace_bytes,  # noqa: E402
+                     policy_loss, preference_loss, token_logprobs, token_logprobs_backward)

@@ -1,5 +1,6 @@
 // abi.hip -- the C ABI declared in include/sinkhorn.h: argument checks,
 // workspace carve-up, the eps-annealing driver and kernel launches.
+#include "abi.h"
 #include "common.h"
 #include "hvp.h"
 #include "sinkhorn.h"
@@ -16,6 +17,10 @@ namespace {
 
 thread_local char g_err[512] = "";
 
+}  // namespace
+
+void clear_error() { g_err[0] = '\0'; }
+
 int fail(int code, const char *fmt, ...)
 {
     va_list ap;
@@ -30,26 +35,12 @@ int hip_fail(hipError_t e, const char *where)
     return fail(SK_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
 
+namespace {
+
 constexpr int kPad = 64;
 constexpr int kMaxPoints = 1 << 24;
 constexpr int kMaxPairs = 65535;     // pairs index a grid dimension (y or z), at most 65535
 constexpr int kMaxNormDim = 4096;   // dimensions accepted by the normalisation
-
-// Bump allocator over the caller's workspace (256-byte aligned pieces).
-// Pieces of the caller's workspace, each at a 256-byte aligned address (the
-// sizes add 256 bytes of slack for a workspace that starts unaligned).
-struct Carve {
-    char *base;
-    size_t off = 0;
-    template <typename T> T *take(size_t count)
-    {
-        const uintptr_t at = (uintptr_t)base + off;
-        off += (((at + 255) & ~(uintptr_t)255) - at);
-        T *p = base ? reinterpret_cast<T *>(base + off) : nullptr;
-        off += count * sizeof(T);
-        return p;
-    }
-};
 
 bool shape_ok(int B, int n, int m, int d)
 {

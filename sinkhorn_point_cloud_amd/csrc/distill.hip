@@ -1,0 +1,333 @@
+// distill.hip -- distillation from a teacher's top logits: the divergence of a
+// student's softmax from a teacher's distribution on K tokens, and its gradient.
+//
+// Per row, at temperature tau, with the teacher's logits u_k at tokens i_k, the
+// student's softmax q over the whole row and a row weight w:
+//     p_k  = exp(u_k / tau - U),    U = LSE_k(u_k / tau), or the teacher's own
+//                                   log-sum-exp over its whole vocabulary,
+//     loss = w tau^2 sum_k p_k (log p_k - log q_{i_k}),
+//     dloss/dz_v = w tau (C q_v - sum_{k: i_k = v} p_k),   C = sum_k p_k.
+// A token may stand in the list twice; its terms add.  The gradient is a
+// multiple of the row's exponentials with K elements written again, so the
+// plan of the row kernels holds: one read of the row, one write of its
+// gradient.  The teacher's side (K values, fp64) is worked out by one wave
+// while the row's loads are in flight.
+//
+// What bounds it: HBM.
+#include "rows.h"
+#include "token_loss.h"
+
+namespace sk {
+namespace {
+
+using namespace rows;
+
+constexpr int kSplit = 256;
+
+struct Args {
+    LogitRows r;
+    DistillArgs d;
+    TokenWs w;
+    int parts;
+    float c;
+};
+
+// The list of a row in shared memory: entry k's token, probability and the
+// student's logit there, and the entries of each owner thread as a linked list.
+struct List {
+    int *head;   // [NT] first entry whose element the thread owns, or -1
+    int *next;   // [K]
+    int *token;  // [K]
+    float *p;    // [K]
+    float *z;    // [K]
+    __device__ __forceinline__ List(int *room, int NT, int K)
+        : head(room), next(room + NT), token(next + K), p((float *)(token + K)), z(p + K)
+    {
+    }
+};
+size_t list_bytes(int NT, int K) { return (size_t)(NT + 4 * K) * 4; }
+
+struct Teacher {
+    double C, plogp;   // sum of p and sum of p log p
+    bool any, bad;
+};
+
+// One wave: the teacher's probabilities into the list.
+__device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const List &l)
+{
+    const int K = a.d.K, V = a.r.V, lane = lane_id();
+    const double inv = a.r.scale;   // 1 / tau
+    const int32_t *token = a.d.index + t * K;
+    const float *u = a.d.teacher + t * K;
+    float top = -kInf;
+    int bad = 0;
+    for (int k = lane; k < K; k += kWave) {
+        const int v = token[k];
+        l.token[k] = v;
+        if (v >= 0) {
+            bad |= v >= V;
+            top = fmaxf(top, u[k]);
+            bad |= u[k] != u[k];
+        }
+    }
+    top = wave_max(top);
+    Teacher r;
+    r.bad = __any(bad);
+    r.any = top != -kInf;
+    double U;
+    if (a.d.teacher_lse) {
+        U = (double)a.d.teacher_lse[t];
+    } else {
+        double s = 0.0;
+        if (r.any)
+            for (int k = lane; k < K; k += kWave)
+                if (token[k] >= 0)
+                    s += exp(((double)u[k] - (double)top) * inv);
+        U = (double)top * inv + log(wave_sum(s));
+    }
+    double C = 0.0, H = 0.0;
+    for (int k = lane; k < K; k += kWave) {
+        const double lp = (double)u[k] * inv - U;
+        // rounded once, to what the gradient subtracts; loss and gradient then
+        // belong to the same distribution
+        const float pf = r.any && token[k] >= 0 ? (float)exp(lp) : 0.f;
+        const double p = (double)pf;
+        l.p[k] = pf;
+        if (p != 0.0) {
+            C += p;
+            H += p * lp;
+        }
+    }
+    r.C = wave_sum(C);
+    r.plogp = wave_sum(H);
+    return r;
+}
+
+struct RowScalars {
+    float A, M, sub;   // out_v = A 2^((z_v - M) c) - sub sum_{k: i_k = v} p_k
+    int zero;
+};
+
+// One wave, once the row's (M, S) and the list are there: loss and coefficients.
+__device__ __forceinline__ RowScalars student_side(const Args &a, long t, const List &l,
+                                                   const Teacher &r, float M, float S, bool writes)
+{
+    const int K = a.d.K, lane = lane_id();
+    const double inv = a.r.scale, tau = 1.0 / inv;
+    const double w = a.d.weights ? (double)a.d.weights[t] : 1.0;
+    const double lnS = log((double)S);
+    double cross = 0.0;   // sum of p log q
+    for (int k = lane; k < K; k += kWave) {
+        const double p = (double)l.p[k];
+        if (p != 0.0)
+            cross += p * (((double)l.z[k] - (double)M) * inv - lnS);
+    }
+    cross = wave_sum(cross);
+    const bool none = S == 0.f || (!r.any && !r.bad);
+    const double nan = __builtin_nan("");
+    if (writes && lane == 0)
+        a.d.loss[t] = none ? 0.f : (float)(r.bad ? nan : w * tau * tau * (r.plogp - cross));
+    const double add = w * tau;
+    return RowScalars{(float)(r.bad ? nan : add * r.C / (double)S), M, (float)add, none};
+}
+
+// The elements of the list that this thread owns, written over its dense values.
+template <typename T>
+__device__ __forceinline__ void write_list(const List &l, T *out, int K, const Dense &d, float sub)
+{
+    for (int k = l.head[threadIdx.x]; k >= 0; k = l.next[k]) {
+        const int v = l.token[k];
+        float p = l.p[k];
+        // the same token again?  Then every one of its entries writes the sum, in list order
+        bool twice = false;
+        for (int j = l.head[threadIdx.x]; j >= 0; j = l.next[j])
+            twice |= j != k && l.token[j] == v;
+        if (twice) {
+            p = 0.f;
+            for (int j = 0; j < K; ++j)
+                p += l.token[j] == v ? l.p[j] : 0.f;
+        }
+        Pack<T>::put(out + v, d.at(l.z[k]) - sub * p);
+    }
+}
+
+template <typename T, typename Src>
+__device__ __forceinline__ void link(const List &l, const Src &src, int K)
+{
+    for (int k = lane_id(); k < K; k += kWave) {
+        const int v = l.token[k];
+        const int who = src.owner(v);
+        if (who >= 0)
+            l.next[k] = atomicExch(&l.head[who], k);
+    }
+}
+
+__device__ __forceinline__ bool dropped(const Args &a, long t)
+{
+    return a.d.weights && a.d.weights[t] == 0.f;
+}
+
+template <typename T, int NT, typename Src>
+__global__ __launch_bounds__(NT) void distill_kernel(Args a)
+{
+    extern __shared__ int dyn[];
+    __shared__ float2 room[NT / kWave];
+    __shared__ RowScalars scal;
+    const long t = group_index();
+    if (t >= a.r.T)
+        return;
+    const int V = a.r.V, K = a.d.K;
+    T *out = (T *)a.r.dlogits + t * a.r.dld;
+    const bool grad = a.r.dlogits;
+    if (dropped(a, t)) {
+        if (threadIdx.x == 0)
+            a.d.loss[t] = 0.f;
+        if (grad)
+            zero_row<T, NT>(out, V, 0, 1);
+        return;
+    }
+    const List l(dyn, NT, K);
+    l.head[threadIdx.x] = -1;
+    __syncthreads();
+    const T *row = (const T *)a.r.logits + t * a.r.ld;
+    Src src(row, V, 0, 1);
+    Teacher r{};
+    src.load();
+    if (threadIdx.x < kWave) {
+        r = teacher_side(a, t, l);
+        for (int k = lane_id(); k < K; k += kWave) {
+            const int v = l.token[k];
+            l.z[k] = v >= 0 && v < V ? Pack<T>::get(row + v) : 0.f;
+        }
+        if (grad)
+            link<T>(l, src, K);
+    }
+    float M = -kInf, S = 0.f;
+    src.stats(a.c, M, S);
+    merge_group<NT>(M, S, a.c, room);
+    if (threadIdx.x < kWave) {
+        const RowScalars k = student_side(a, t, l, r, M, S, true);
+        if (threadIdx.x == 0)
+            scal = k;
+    }
+    if (!grad)
+        return;
+    __syncthreads();
+    const RowScalars k = scal;
+    if (k.zero) {
+        zero_row<T, NT>(out, V, 0, 1);
+        return;
+    }
+    const Dense d{k.A, k.M, a.c};
+    src.dense(out, d);
+    write_list<T>(l, out, K, d, k.sub);
+}
+
+// Few rows: partial statistics, and the student's logits at the list's tokens
+// (the second launch may write its gradient over the logits).
+template <typename T> __global__ __launch_bounds__(kSplit) void distill_part_kernel(Args a)
+{
+    __shared__ float2 room[kSplit / kWave];
+    const long t = group_index() / a.parts;
+    const int part = (int)(group_index() % a.parts), K = a.d.K, V = a.r.V;
+    if (t >= a.r.T || dropped(a, t))
+        return;
+    const T *row = (const T *)a.r.logits + t * a.r.ld;
+    if (part == a.parts - 1)
+        for (int k = threadIdx.x; k < K; k += kSplit) {
+            const int v = a.d.index[t * K + k];
+            a.d.zk[t * K + k] = v >= 0 && v < V ? Pack<T>::get(row + v) : 0.f;
+        }
+    Streamed<T, kSplit> src(row, V, part, a.parts);
+    float m = -kInf, s = 0.f;
+    src.stats(a.c, m, s);
+    merge_group<kSplit>(m, s, a.c, room);
+    if (threadIdx.x == 0)
+        a.w.part[t * a.parts + part] = make_float2(m, s);
+}
+
+template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_kernel(Args a, int run)
+{
+    extern __shared__ int dyn[];
+    __shared__ RowScalars scal;
+    const long t = group_index() / run;
+    const int part = (int)(group_index() % run), V = a.r.V, K = a.d.K;
+    if (t >= a.r.T)
+        return;
+    T *out = (T *)a.r.dlogits + t * a.r.dld;
+    const bool grad = a.r.dlogits;
+    if (dropped(a, t)) {
+        if (threadIdx.x == 0 && part == 0)
+            a.d.loss[t] = 0.f;
+        if (grad)
+            zero_row<T, kSplit>(out, V, part, run);
+        return;
+    }
+    const List l(dyn, kSplit, K);
+    l.head[threadIdx.x] = -1;
+    __syncthreads();
+    const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, run);
+    if (threadIdx.x < kWave) {
+        const Teacher r = teacher_side(a, t, l);
+        for (int k = lane_id(); k < K; k += kWave)
+            l.z[k] = a.d.zk[t * K + k];
+        if (grad)
+            link<T>(l, src, K);
+        float M = -kInf, S = 0.f;
+        const float2 *p = a.w.part + t * a.parts;
+        for (int i = lane_id(); i < a.parts; i += kWave) {
+            const float mn = fmaxf(M, p[i].x), at = shift_of(mn);
+            S = S * ex2((M - at) * a.c) + p[i].y * ex2((p[i].x - at) * a.c);
+            M = mn;
+        }
+        merge_wave(M, S, a.c);
+        const RowScalars k = student_side(a, t, l, r, M, S, part == 0);
+        if (threadIdx.x == 0)
+            scal = k;
+    }
+    if (!grad)
+        return;
+    __syncthreads();
+    const RowScalars k = scal;
+    if (k.zero) {
+        zero_row<T, kSplit>(out, V, part, run);
+        return;
+    }
+    const Dense d{k.A, k.M, a.c};
+    src.dense(out, d);
+    write_list<T>(l, out, K, d, k.sub);
+}
+
+template <typename T, int NT, typename Src> void run_rows(const Args &a, hipStream_t st)
+{
+    hipLaunchKernelGGL((distill_kernel<T, NT, Src>), grid_of(a.r.T), dim3(NT),
+                       list_bytes(NT, a.d.K), st, a);
+}
+
+template <typename T> void launch_rows(const Args &a, hipStream_t st)
+{
+    if (a.parts > 1) {
+        hipLaunchKernelGGL((distill_part_kernel<T>), grid_of((long)a.r.T * a.parts), dim3(kSplit),
+                           0, st, a);
+        const int run = a.r.dlogits ? a.parts : 1;
+        hipLaunchKernelGGL((distill_join_kernel<T>), grid_of((long)a.r.T * run), dim3(kSplit),
+                           list_bytes(kSplit, a.d.K), st, a, run);
+        return;
+    }
+    run_rows<T, 1024, Streamed<T, 1024>>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_distill(const LogitRows &r, const DistillArgs &d, const TokenWs &w,
+                          hipStream_t st)
+{
+    Args a{r, d, w, token_parts(r.T, r.V, r.dtype), (float)(r.scale * kLog2eD)};
+    if (r.dtype == 1)
+        launch_rows<uint16_t>(a, st);
+    else
+        launch_rows<float>(a, st);
+    return hipGetLastError();
+}
+
+}  // namespace sk

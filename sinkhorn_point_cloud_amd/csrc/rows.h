@@ -1,0 +1,356 @@
+// rows.h -- one row of logits as a work-group sees it: 16-byte chunks dealt to
+// the threads, the running (maximum, sum) of its exponentials, and the pass
+// that writes coefficient x exponential.
+//
+// A row starts at any address that suits its type.  It is cut into 16-byte
+// aligned chunks (4 fp32 or 8 bf16 values) and the fewer than one chunk's
+// worth of values before the first and behind the last of them, the edge; the
+// edge values are dealt one to a thread.  Chunk c0 + i * threads + t belongs to
+// thread t, so that a wave's loads are 1 KB in a run and the thread that owns
+// an element is known from its index alone: an element with a sparse term is
+// written again by the thread that wrote its chunk, in that thread's own
+// program order, and needs no barrier.
+//
+// The exponentials are taken in base 2: with c = scale log2(e) and the row
+// maximum M, e_v = 2^((x_v - M) c).  The difference is formed first, so a row
+// of the type's lowest finite values is an ordinary row.  Values of -inf take
+// no part; a row of nothing else has the sum 0.  NaN and +inf give a NaN sum.
+#pragma once
+
+#include "common.h"
+
+#include <algorithm>
+
+namespace sk {
+namespace rows {
+
+// Four 32-bit words: a chunk as it is loaded and stored.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kInf = __builtin_inff();
+
+// A grid of `count` work-groups in two dimensions: threads along one dimension
+// of a launch have to stay below 2^32, and rows x threads may not.
+inline dim3 grid_of(long count)
+{
+    const long x = std::min(count, 1l << 20);
+    return dim3((unsigned)x, (unsigned)((count + x - 1) / x));
+}
+__device__ __forceinline__ long group_index() { return (long)blockIdx.y * gridDim.x + blockIdx.x; }
+
+template <typename T> struct Pack;
+template <> struct Pack<float> {
+    static constexpr int n = 4;
+    static constexpr uint32_t kNone = 0xFF800000u;   // -inf
+    __device__ __forceinline__ static void open(u32x4 v, float (&x)[n])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = __uint_as_float(v[i]);
+    }
+    __device__ __forceinline__ static u32x4 close(const float (&x)[n])
+    {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __float_as_uint(x[i]);
+        return v;
+    }
+    __device__ __forceinline__ static float get(const float *p) { return *p; }
+    __device__ __forceinline__ static void put(float *p, float x) { *p = x; }
+};
+template <> struct Pack<uint16_t> {
+    static constexpr int n = 8;
+    static constexpr uint32_t kNone = 0xFF80FF80u;
+    __device__ __forceinline__ static void open(u32x4 v, float (&x)[n])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(v[i] << 16);
+            x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+        }
+    }
+    // fp32 to bf16, round to nearest even: the gradient's one rounding
+    __device__ __forceinline__ static u32x4 close(const float (&x)[n])
+    {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x2 two = {x[2 * i], x[2 * i + 1]};
+            v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2));
+        }
+        return v;
+    }
+    __device__ __forceinline__ static float get(const uint16_t *p) { return bf16_to_float(*p); }
+    __device__ __forceinline__ static void put(uint16_t *p, float x)
+    {
+        *p = __builtin_bit_cast(uint16_t, (__bf16)x);
+    }
+};
+
+// How one row is cut: `head` values, `chunks` aligned chunks, then the rest;
+// `edge` = values before and behind.
+struct Cut {
+    int head, chunks, edge;
+};
+
+template <typename T> __device__ __forceinline__ Cut cut_of(const T *p, int len)
+{
+    constexpr int n = Pack<T>::n;
+    const int off = (int)(((uintptr_t)p & 15) / sizeof(T));
+    Cut c;
+    c.head = off ? min(len, n - off) : 0;
+    c.chunks = (len - c.head) / n;
+    c.edge = len - c.chunks * n;
+    return c;
+}
+
+// The part of a row that one work-group of NT threads handles: chunks
+// [c0, c1), and the edge if it is the first part.
+template <typename T, int NT> struct Slice {
+    static constexpr int n = Pack<T>::n;
+    const T *row;
+    Cut cut;
+    int c0, c1;
+    bool edges;
+
+    __device__ __forceinline__ Slice(const T *p, int len, int part, int parts) : row(p)
+    {
+        cut = cut_of(p, len);
+        const int per = (cut.chunks + parts - 1) / parts;
+        c0 = min(part * per, cut.chunks);
+        c1 = min(c0 + per, cut.chunks);
+        edges = part == 0;
+    }
+    __device__ __forceinline__ bool has_edge(int t) const { return edges && t < cut.edge; }
+    // element of edge value t
+    __device__ __forceinline__ int edge_at(int t) const
+    {
+        return t < cut.head ? t : t + cut.chunks * n;
+    }
+    __device__ __forceinline__ const u32x4 *chunk(int c) const
+    {
+        return reinterpret_cast<const u32x4 *>(row + cut.head) + c;
+    }
+    // thread that owns element v, or -1 where another part does or the row has no such element
+    __device__ __forceinline__ int owner(int v) const
+    {
+        const int behind = cut.head + cut.chunks * n;
+        if (v < 0 || v >= behind + cut.edge - cut.head)
+            return -1;
+        if (v < cut.head)
+            return edges ? v : -1;
+        if (v >= behind)
+            return edges ? v - cut.chunks * n : -1;
+        const int c = (v - cut.head) / n;
+        return c >= c0 && c < c1 ? (c - c0) % NT : -1;
+    }
+};
+
+// Running maximum and sum of exponentials.  The shift of an empty state is 0,
+// so that no difference of two infinities is formed.
+__device__ __forceinline__ float shift_of(float m) { return m == -kInf ? 0.f : m; }
+
+template <int K>
+__device__ __forceinline__ void absorb(const float (&x)[K], float c, float &m, float &s)
+{
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < K; ++i)
+        top = fmaxf(top, x[i]);
+    const float mn = fmaxf(m, top), at = shift_of(mn);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+        sum += ex2((x[i] - at) * c);
+    s = fmaf(s, ex2((m - at) * c), sum);
+    m = mn;
+}
+
+__device__ __forceinline__ void merge_wave(float &m, float &s, float c)
+{
+    const float top = wave_max(m), at = shift_of(top);
+    s = wave_sum(s * ex2((m - at) * c));
+    m = top;
+}
+
+// (M, S) of the whole work-group in every thread.  `room`: one entry per wave.
+// One barrier; `room` may be written again only behind another one.
+template <int NT>
+__device__ __forceinline__ void merge_group(float &m, float &s, float c, float2 *room)
+{
+    merge_wave(m, s, c);
+    if constexpr (NT > kWave) {
+        constexpr int waves = NT / kWave;
+        if (lane_id() == 0)
+            room[threadIdx.x / kWave] = make_float2(m, s);
+        __syncthreads();
+        const float2 r = lane_id() < waves ? room[lane_id()] : make_float2(-kInf, 0.f);
+        m = r.x;
+        s = r.y;
+        merge_wave(m, s, c);
+    }
+}
+
+// coefficient x exponential of one row: out_v = A 2^((x_v - M) c), or zeros.
+struct Dense {
+    float A, M, c;
+    __device__ __forceinline__ float at(float x) const { return A * ex2((x - M) * c); }
+};
+
+template <typename T>
+__device__ __forceinline__ void store_chunk(T *out, const float (&y)[Pack<T>::n], bool aligned)
+{
+    if (aligned) {
+        *reinterpret_cast<u32x4 *>(out) = Pack<T>::close(y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Pack<T>::n; ++i)
+            Pack<T>::put(out + i, y[i]);
+    }
+}
+
+// The row read from memory in each pass.
+template <typename T, int NT> struct Streamed : Slice<T, NT> {
+    using S = Slice<T, NT>;
+    static constexpr int n = S::n;
+    static constexpr int kUnroll = 4;
+    using S::S;
+
+    __device__ __forceinline__ void load() {}
+
+    __device__ __forceinline__ void stats(float c, float &m, float &s) const
+    {
+        const int t = threadIdx.x;
+        if (S::has_edge(t)) {
+            const float x[1] = {Pack<T>::get(S::row + S::edge_at(t))};
+            absorb<1>(x, c, m, s);
+        }
+        int i = S::c0 + t;
+        for (; i + (kUnroll - 1) * NT < S::c1; i += kUnroll * NT) {
+            u32x4 v[kUnroll];
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j)
+                v[j] = *S::chunk(i + j * NT);
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j) {
+                float x[n];
+                Pack<T>::open(v[j], x);
+                absorb<n>(x, c, m, s);
+            }
+        }
+        for (; i < S::c1; i += NT) {
+            float x[n];
+            Pack<T>::open(*S::chunk(i), x);
+            absorb<n>(x, c, m, s);
+        }
+    }
+
+    __device__ __forceinline__ void dense(T *out, const Dense &d) const
+    {
+        const int t = threadIdx.x;
+        const bool aligned = (((uintptr_t)(out + S::cut.head)) & 15) == 0;
+        if (S::has_edge(t)) {
+            const int v = S::edge_at(t);
+            Pack<T>::put(out + v, d.at(Pack<T>::get(S::row + v)));
+        }
+        T *base = out + S::cut.head;
+        int i = S::c0 + t;
+        for (; i + (kUnroll - 1) * NT < S::c1; i += kUnroll * NT) {
+            u32x4 v[kUnroll];
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j)
+                v[j] = *S::chunk(i + j * NT);
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j) {
+                float x[n];
+                Pack<T>::open(v[j], x);
+#pragma unroll
+                for (int k = 0; k < n; ++k)
+                    x[k] = d.at(x[k]);
+                store_chunk<T>(base + (size_t)(i + j * NT) * n, x, aligned);
+            }
+        }
+        for (; i < S::c1; i += NT) {
+            float x[n];
+            Pack<T>::open(*S::chunk(i), x);
+#pragma unroll
+            for (int k = 0; k < n; ++k)
+                x[k] = d.at(x[k]);
+            store_chunk<T>(base + (size_t)i * n, x, aligned);
+        }
+    }
+};
+
+// The row read once and kept in registers between the passes: N chunks a
+// thread, N * NT at least the chunks of the slice.
+template <typename T, int NT, int N> struct Held : Slice<T, NT> {
+    using S = Slice<T, NT>;
+    static constexpr int n = S::n;
+    using S::S;
+    u32x4 v[N];
+    float e;
+
+    __device__ __forceinline__ void load()
+    {
+        const int t = threadIdx.x;
+        e = S::has_edge(t) ? Pack<T>::get(S::row + S::edge_at(t)) : -kInf;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = u32x4{Pack<T>::kNone, Pack<T>::kNone, Pack<T>::kNone, Pack<T>::kNone};
+            const int at = S::c0 + i * NT + t;
+            if (at < S::c1)
+                v[i] = *S::chunk(at);
+        }
+    }
+    __device__ __forceinline__ void stats(float c, float &m, float &s) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (S::c0 + i * NT < S::c1) {
+                float x[n];
+                Pack<T>::open(v[i], x);
+                absorb<n>(x, c, m, s);
+            }
+        const float x[1] = {e};
+        absorb<1>(x, c, m, s);
+    }
+    __device__ __forceinline__ void dense(T *out, const Dense &d) const
+    {
+        const int t = threadIdx.x;
+        const bool aligned = (((uintptr_t)(out + S::cut.head)) & 15) == 0;
+        if (S::has_edge(t))
+            Pack<T>::put(out + S::edge_at(t), d.at(e));
+        T *base = out + S::cut.head;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = S::c0 + i * NT + t;
+            if (at < S::c1) {
+                float x[n];
+                Pack<T>::open(v[i], x);
+#pragma unroll
+                for (int k = 0; k < n; ++k)
+                    x[k] = d.at(x[k]);
+                store_chunk<T>(base + (size_t)at * n, x, aligned);
+            }
+        }
+    }
+};
+
+// Zeros over the slice's elements of an output row (cut by the output's own
+// alignment: nothing is read).
+template <typename T, int NT> __device__ __forceinline__ void zero_row(T *out, int len, int part, int parts)
+{
+    const Slice<T, NT> z(out, len, part, parts);
+    const int t = threadIdx.x;
+    if (z.has_edge(t))
+        Pack<T>::put(out + z.edge_at(t), 0.f);
+    u32x4 *base = reinterpret_cast<u32x4 *>(out + z.cut.head);
+    for (int i = z.c0 + t; i < z.c1; i += NT)
+        base[i] = u32x4{0u, 0u, 0u, 0u};
+}
+
+}  // namespace rows
+}  // namespace sk
