@@ -17,7 +17,8 @@ size_t elem(int dtype) { return dtype == SK_BF16 ? 2 : 4; }
 
 struct Ws {
     TokenWs token{};
-    float2 *info = nullptr, *term = nullptr, *stat = nullptr;
+    float2 *info = nullptr, *term = nullptr;
+    RowStat *stat = nullptr;
     float *coef = nullptr, *zk = nullptr;
     BalanceWs balance{};
 };
@@ -45,7 +46,7 @@ Ws carve(Carve &c, int op, int T, int V, int k, int dtype)
         w.info = c.take<float2>(rows);
         w.term = c.take<float2>(rows);
     } else if (op == SK_OP_PREFERENCE_LOSS) {
-        w.stat = c.take<float2>(rows);
+        w.stat = c.take<RowStat>(rows);
         w.coef = c.take<float>(rows);
     }
     return w;
@@ -234,6 +235,8 @@ int sinkhorn_policy_loss(const void *logits, int dtype, int64_t ld, const int32_
     a.mean = (flags & SK_LOSS_MEAN) != 0;
     a.lo = 1.0 - clip_lo;
     a.hi = 1.0 + clip_hi;
+    a.log_lo = log1p(-clip_lo);
+    a.log_hi = log1p(clip_hi);
     a.kl = kl_coef;
     a.info = w.info;
     a.term = w.term;

@@ -10,8 +10,8 @@
 // A token may stand in the list twice; its terms add.  The gradient is a
 // multiple of the row's exponentials with K elements written again, so the
 // plan of the row kernels holds: one read of the row, one write of its
-// gradient.  The teacher's side (K values, fp64) is worked out by one wave
-// while the row's loads are in flight.
+// gradient.  The teacher's side (K values) is worked out by one wave while the
+// row's loads are in flight.
 //
 // What bounds it: HBM.
 #include "rows.h"
@@ -29,7 +29,7 @@ struct Args {
     DistillArgs d;
     TokenWs w;
     int parts;
-    float c;
+    Scale c;
 };
 
 // The list of a row in shared memory: entry k's token, probability and the
@@ -48,58 +48,86 @@ struct List {
 size_t list_bytes(int NT, int K) { return (size_t)(NT + 4 * K) * 4; }
 
 struct Teacher {
-    double C, plogp;   // sum of p and sum of p log p
+    double C, U;   // sum of p, log-sum-exp
     bool any, bad;
 };
 
-// One wave: the teacher's probabilities into the list.
-__device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const List &l)
-{
-    const int K = a.d.K, V = a.r.V, lane = lane_id();
-    const double inv = a.r.scale;   // 1 / tau
-    const int32_t *token = a.d.index + t * K;
-    const float *u = a.d.teacher + t * K;
-    float top = -kInf;
-    int bad = 0;
-    for (int k = lane; k < K; k += kWave) {
-        const int v = token[k];
-        l.token[k] = v;
-        if (v >= 0) {
-            bad |= v >= V;
-            top = fmaxf(top, u[k]);
-            bad |= u[k] != u[k];
+// The first entries of a row's list, asked for ahead of the row itself: loads
+// return in order, so the list's work can begin while the row is on its way.
+struct Ahead {
+    static constexpr int n = 4;   // 256 entries
+    int v[n];
+    float u[n];
+    __device__ __forceinline__ void load(const Args &a, long t)
+    {
+        const int K = a.d.K;
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            const int k = lane_id() + j * kWave;
+            v[j] = k < K ? a.d.index[t * K + k] : -1;
+            u[j] = k < K ? a.d.teacher[t * K + k] : 0.f;
         }
     }
-    top = wave_max(top);
+    // f(k, token, logit) for every entry of this lane
+    template <typename F> __device__ __forceinline__ void each(const Args &a, long t, F &&f) const
+    {
+        const int K = a.d.K;
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            const int k = lane_id() + j * kWave;
+            if (k < K)
+                f(k, v[j], u[j]);
+        }
+        for (int k = lane_id() + n * kWave; k < K; k += kWave)
+            f(k, a.d.index[t * K + k], a.d.teacher[t * K + k]);
+    }
+};
+
+// One wave: the teacher's probabilities into the list.  The exponents are formed
+// in fp64, the exponentials and their sum are fp32.
+__device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const Ahead &in,
+                                                const List &l)
+{
+    const int V = a.r.V;
+    const double c = a.r.scale * kLog2eD;   // log2(e) / tau
+    float top = -kInf;
+    int bad = 0;
+    in.each(a, t, [&](int k, int v, float u) {
+        l.token[k] = v;
+        if (v >= 0) {
+            bad |= v >= V || u != u;
+            top = fmaxf(top, u);
+        }
+    });
+    top = max_wave(top);
     Teacher r;
     r.bad = __any(bad);
     r.any = top != -kInf;
-    double U;
+    // p_k = 2^((u_k - at) c - less) / sum
+    double at = (double)top, less = 0.0;
+    float sum = 1.f;
     if (a.d.teacher_lse) {
-        U = (double)a.d.teacher_lse[t];
+        r.U = (double)a.d.teacher_lse[t];
+        at = 0.0;
+        less = r.U * kLog2eD;
     } else {
-        double s = 0.0;
-        if (r.any)
-            for (int k = lane; k < K; k += kWave)
-                if (token[k] >= 0)
-                    s += exp(((double)u[k] - (double)top) * inv);
-        U = (double)top * inv + log(wave_sum(s));
+        float s = 0.f;
+        in.each(a, t, [&](int, int v, float u) {
+            if (r.any && v >= 0)
+                s += ex2((float)(((double)u - at) * c));
+        });
+        sum = sum_wave(s);
+        r.U = at * a.r.scale + ln_of(sum);
     }
-    double C = 0.0, H = 0.0;
-    for (int k = lane; k < K; k += kWave) {
-        const double lp = (double)u[k] * inv - U;
+    double C = 0.0;
+    in.each(a, t, [&](int k, int v, float u) {
         // rounded once, to what the gradient subtracts; loss and gradient then
         // belong to the same distribution
-        const float pf = r.any && token[k] >= 0 ? (float)exp(lp) : 0.f;
-        const double p = (double)pf;
-        l.p[k] = pf;
-        if (p != 0.0) {
-            C += p;
-            H += p * lp;
-        }
-    }
-    r.C = wave_sum(C);
-    r.plogp = wave_sum(H);
+        const float p = r.any && v >= 0 ? ex2((float)(((double)u - at) * c - less)) / sum : 0.f;
+        l.p[k] = p;
+        C += (double)p;
+    });
+    r.C = sum_wave(C);
     return r;
 }
 
@@ -109,24 +137,25 @@ struct RowScalars {
 };
 
 // One wave, once the row's (M, S) and the list are there: loss and coefficients.
-__device__ __forceinline__ RowScalars student_side(const Args &a, long t, const List &l,
-                                                   const Teacher &r, float M, float S, bool writes)
+__device__ __forceinline__ RowScalars student_side(const Args &a, long t, const Ahead &in,
+                                                   const List &l, const Teacher &r, float M,
+                                                   float S, bool writes)
 {
-    const int K = a.d.K, lane = lane_id();
+    const int lane = lane_id();
     const double inv = a.r.scale, tau = 1.0 / inv;
     const double w = a.d.weights ? (double)a.d.weights[t] : 1.0;
-    const double lnS = log((double)S);
-    double cross = 0.0;   // sum of p log q
-    for (int k = lane; k < K; k += kWave) {
+    // log p_k - log q_k = (u_k - (z_k - M)) / tau - (U - ln S)
+    double apart = 0.0;
+    in.each(a, t, [&](int k, int, float u) {
         const double p = (double)l.p[k];
         if (p != 0.0)
-            cross += p * (((double)l.z[k] - (double)M) * inv - lnS);
-    }
-    cross = wave_sum(cross);
+            apart += p * ((double)u - ((double)l.z[k] - (double)M));
+    });
+    apart = sum_wave(apart) * inv - r.C * (r.U - ln_of(S));
     const bool none = S == 0.f || (!r.any && !r.bad);
     const double nan = __builtin_nan("");
     if (writes && lane == 0)
-        a.d.loss[t] = none ? 0.f : (float)(r.bad ? nan : w * tau * tau * (r.plogp - cross));
+        a.d.loss[t] = none ? 0.f : (float)(r.bad ? nan : w * tau * tau * apart);
     const double add = w * tau;
     return RowScalars{(float)(r.bad ? nan : add * r.C / (double)S), M, (float)add, none};
 }
@@ -170,12 +199,13 @@ __device__ __forceinline__ bool dropped(const Args &a, long t)
 template <typename T, int NT, typename Src>
 __global__ __launch_bounds__(NT) void distill_kernel(Args a)
 {
-    extern __shared__ int dyn[];
+    extern __shared__ u32x4 chunks[];   // [Src::lds_chunks], then the list
     __shared__ float2 room[NT / kWave];
     __shared__ RowScalars scal;
     const long t = group_index();
     if (t >= a.r.T)
         return;
+    int *dyn = (int *)(chunks + Src::lds_chunks);
     const int V = a.r.V, K = a.d.K;
     T *out = (T *)a.r.dlogits + t * a.r.dld;
     const bool grad = a.r.dlogits;
@@ -190,15 +220,17 @@ __global__ __launch_bounds__(NT) void distill_kernel(Args a)
     l.head[threadIdx.x] = -1;
     __syncthreads();
     const T *row = (const T *)a.r.logits + t * a.r.ld;
-    Src src(row, V, 0, 1);
+    Src src(row, V, 0, 1, chunks);
     Teacher r{};
+    Ahead ahead;
+    if (threadIdx.x < kWave)
+        ahead.load(a, t);
     src.load();
     if (threadIdx.x < kWave) {
-        r = teacher_side(a, t, l);
-        for (int k = lane_id(); k < K; k += kWave) {
-            const int v = l.token[k];
+        ahead.each(a, t, [&](int k, int v, float) {
             l.z[k] = v >= 0 && v < V ? Pack<T>::get(row + v) : 0.f;
-        }
+        });
+        r = teacher_side(a, t, ahead, l);
         if (grad)
             link<T>(l, src, K);
     }
@@ -206,7 +238,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Args a)
     src.stats(a.c, M, S);
     merge_group<NT>(M, S, a.c, room);
     if (threadIdx.x < kWave) {
-        const RowScalars k = student_side(a, t, l, r, M, S, true);
+        const RowScalars k = student_side(a, t, ahead, l, r, M, S, true);
         if (threadIdx.x == 0)
             scal = k;
     }
@@ -218,7 +250,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Args a)
         zero_row<T, NT>(out, V, 0, 1);
         return;
     }
-    const Dense d{k.A, k.M, a.c};
+    const Dense d{k.A, k.M, a.c.hi};
     src.dense(out, d);
     write_list<T>(l, out, K, d, k.sub);
 }
@@ -268,7 +300,9 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
     __syncthreads();
     const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, run);
     if (threadIdx.x < kWave) {
-        const Teacher r = teacher_side(a, t, l);
+        Ahead ahead;
+        ahead.load(a, t);
+        const Teacher r = teacher_side(a, t, ahead, l);
         for (int k = lane_id(); k < K; k += kWave)
             l.z[k] = a.d.zk[t * K + k];
         if (grad)
@@ -277,11 +311,11 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
         const float2 *p = a.w.part + t * a.parts;
         for (int i = lane_id(); i < a.parts; i += kWave) {
             const float mn = fmaxf(M, p[i].x), at = shift_of(mn);
-            S = S * ex2((M - at) * a.c) + p[i].y * ex2((p[i].x - at) * a.c);
+            S = S * a.c.pow(M - at) + p[i].y * a.c.pow(p[i].x - at);
             M = mn;
         }
         merge_wave(M, S, a.c);
-        const RowScalars k = student_side(a, t, l, r, M, S, part == 0);
+        const RowScalars k = student_side(a, t, ahead, l, r, M, S, part == 0);
         if (threadIdx.x == 0)
             scal = k;
     }
@@ -293,16 +327,20 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
         zero_row<T, kSplit>(out, V, part, run);
         return;
     }
-    const Dense d{k.A, k.M, a.c};
+    const Dense d{k.A, k.M, a.c.hi};
     src.dense(out, d);
     write_list<T>(l, out, K, d, k.sub);
 }
 
-template <typename T, int NT, typename Src> void run_rows(const Args &a, hipStream_t st)
-{
-    hipLaunchKernelGGL((distill_kernel<T, NT, Src>), grid_of(a.r.T), dim3(NT),
-                       list_bytes(NT, a.d.K), st, a);
-}
+template <typename T> struct RunRows {
+    const Args &a;
+    hipStream_t st;
+    template <int NT, typename Src> void operator()() const
+    {
+        hipLaunchKernelGGL((distill_kernel<T, NT, Src>), grid_of(a.r.T), dim3(NT),
+                           (size_t)Src::lds_chunks * 16 + list_bytes(NT, a.d.K), st, a);
+    }
+};
 
 template <typename T> void launch_rows(const Args &a, hipStream_t st)
 {
@@ -314,7 +352,9 @@ template <typename T> void launch_rows(const Args &a, hipStream_t st)
                            list_bytes(kSplit, a.d.K), st, a, run);
         return;
     }
-    run_rows<T, 1024, Streamed<T, 1024>>(a, st);
+    const RunRows<T> run{a, st};
+    // without a gradient too: the loss is then the same to the bit
+    with_source<T>(a.r.V, list_bytes(1024, a.d.K), run);
 }
 
 }  // namespace
@@ -322,7 +362,7 @@ template <typename T> void launch_rows(const Args &a, hipStream_t st)
 hipError_t launch_distill(const LogitRows &r, const DistillArgs &d, const TokenWs &w,
                           hipStream_t st)
 {
-    Args a{r, d, w, token_parts(r.T, r.V, r.dtype), (float)(r.scale * kLog2eD)};
+    Args a{r, d, w, token_parts(r.T, r.V, r.dtype), scale_of_row(r.scale)};
     if (r.dtype == 1)
         launch_rows<uint16_t>(a, st);
     else

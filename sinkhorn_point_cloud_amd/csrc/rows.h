@@ -20,6 +20,7 @@
 #include "common.h"
 
 #include <algorithm>
+#include <math.h>
 
 namespace sk {
 namespace rows {
@@ -149,12 +150,78 @@ template <typename T, int NT> struct Slice {
     }
 };
 
+// Reductions over a wave without LDS: over each row of 16 lanes by lane moves,
+// then the four rows through scalar registers, in a fixed order.  All lanes
+// active; every lane gets the result.
+__device__ __forceinline__ float read_lane(float v, int lane)
+{
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ float sum_wave(float v)
+{
+    v = row16_sum(v);
+    return (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
+}
+__device__ __forceinline__ float max_wave(float v)
+{
+    v = fmaxf(v, dpp_move<kDppXor1>(v));
+    v = fmaxf(v, dpp_move<kDppXor2>(v));
+    v = fmaxf(v, dpp_move<kDppHalfMirror>(v));
+    v = fmaxf(v, dpp_move<kDppMirror>(v));
+    return fmaxf(fmaxf(read_lane(v, 0), read_lane(v, 16)),
+                 fmaxf(read_lane(v, 32), read_lane(v, 48)));
+}
+template <int Ctrl> __device__ __forceinline__ double dpp_move(double v)
+{
+    return __hiloint2double(
+        __builtin_amdgcn_mov_dpp(__double2hiint(v), Ctrl, 0xF, 0xF, true),
+        __builtin_amdgcn_mov_dpp(__double2loint(v), Ctrl, 0xF, 0xF, true));
+}
+__device__ __forceinline__ double read_lane(double v, int lane)
+{
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), lane),
+                            __builtin_amdgcn_readlane(__double2loint(v), lane));
+}
+__device__ __forceinline__ double sum_wave(double v)
+{
+    v += dpp_move<kDppXor1>(v);
+    v += dpp_move<kDppXor2>(v);
+    v += dpp_move<kDppHalfMirror>(v);
+    v += dpp_move<kDppMirror>(v);
+    return (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
+}
+
+// ln of a positive sum in fp64, off by about 2^-24: the exponent is exact, the
+// logarithm of the mantissa is the hardware's, between -1 and 0.
+__device__ __forceinline__ double ln_of(float s)
+{
+    const int e = __builtin_amdgcn_frexp_expf(s);
+    return ((double)e + (double)lg2(__builtin_amdgcn_frexp_mantf(s))) * kLn2D;
+}
+
+// c = scale log2(e) in two pieces.  With one, every exponent of a row's sum would
+// be off by the same relative 2^-25: an error of one sign, about 1e-7 in each
+// log-probability, which adds up over a sequence.  hi lies below c, so that lo is
+// positive and a difference of -inf gives -inf in both terms.
+struct Scale {
+    float hi, lo;
+    __device__ __forceinline__ float pow(float d) const { return ex2(fmaf(d, hi, d * lo)); }
+};
+inline Scale scale_of_row(double scale)
+{
+    const double c = scale * kLog2eD;
+    float hi = (float)c;
+    if ((double)hi >= c)
+        hi = nextafterf(hi, 0.f);
+    return Scale{hi, (float)(c - (double)hi)};
+}
+
 // Running maximum and sum of exponentials.  The shift of an empty state is 0,
 // so that no difference of two infinities is formed.
 __device__ __forceinline__ float shift_of(float m) { return m == -kInf ? 0.f : m; }
 
 template <int K>
-__device__ __forceinline__ void absorb(const float (&x)[K], float c, float &m, float &s)
+__device__ __forceinline__ void absorb(const float (&x)[K], const Scale &k, float &m, float &s)
 {
     float top = x[0];
 #pragma unroll
@@ -164,22 +231,22 @@ __device__ __forceinline__ void absorb(const float (&x)[K], float c, float &m, f
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < K; ++i)
-        sum += ex2((x[i] - at) * c);
-    s = fmaf(s, ex2((m - at) * c), sum);
+        sum += k.pow(x[i] - at);
+    s = fmaf(s, k.pow(m - at), sum);
     m = mn;
 }
 
-__device__ __forceinline__ void merge_wave(float &m, float &s, float c)
+__device__ __forceinline__ void merge_wave(float &m, float &s, const Scale &c)
 {
-    const float top = wave_max(m), at = shift_of(top);
-    s = wave_sum(s * ex2((m - at) * c));
+    const float top = max_wave(m), at = shift_of(top);
+    s = sum_wave(s * c.pow(m - at));
     m = top;
 }
 
 // (M, S) of the whole work-group in every thread.  `room`: one entry per wave.
 // One barrier; `room` may be written again only behind another one.
 template <int NT>
-__device__ __forceinline__ void merge_group(float &m, float &s, float c, float2 *room)
+__device__ __forceinline__ void merge_group(float &m, float &s, const Scale &c, float2 *room)
 {
     merge_wave(m, s, c);
     if constexpr (NT > kWave) {
@@ -204,7 +271,8 @@ template <typename T>
 __device__ __forceinline__ void store_chunk(T *out, const float (&y)[Pack<T>::n], bool aligned)
 {
     if (aligned) {
-        *reinterpret_cast<u32x4 *>(out) = Pack<T>::close(y);
+        // not read again here: kept out of the way of what other rows read
+        __builtin_nontemporal_store(Pack<T>::close(y), reinterpret_cast<u32x4 *>(out));
     } else {
 #pragma unroll
         for (int i = 0; i < Pack<T>::n; ++i)
@@ -216,12 +284,17 @@ __device__ __forceinline__ void store_chunk(T *out, const float (&y)[Pack<T>::n]
 template <typename T, int NT> struct Streamed : Slice<T, NT> {
     using S = Slice<T, NT>;
     static constexpr int n = S::n;
+    static constexpr int lds_chunks = 0;
     static constexpr int kUnroll = 4;
-    using S::S;
+    __device__ __forceinline__ Streamed(const T *p, int len, int part, int parts,
+                                        u32x4 * = nullptr)
+        : S(p, len, part, parts)
+    {
+    }
 
     __device__ __forceinline__ void load() {}
 
-    __device__ __forceinline__ void stats(float c, float &m, float &s) const
+    __device__ __forceinline__ void stats(const Scale &c, float &m, float &s) const
     {
         const int t = threadIdx.x;
         if (S::has_edge(t)) {
@@ -284,15 +357,32 @@ template <typename T, int NT> struct Streamed : Slice<T, NT> {
     }
 };
 
-// The row read once and kept in registers between the passes: N chunks a
-// thread, N * NT at least the chunks of the slice.
-template <typename T, int NT, int N> struct Held : Slice<T, NT> {
+// Chunks on their way into shared memory: 16 bytes a lane, a wave's chunk in a
+// run from `to` on (the same in all its lanes).
+__device__ __forceinline__ void load_to_lds(const u32x4 *from, u32x4 *to)
+{
+    __builtin_amdgcn_global_load_lds(
+        (const __attribute__((address_space(1))) void *)from,
+        (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+}
+
+// The row read once and kept between the passes: N chunks a thread in
+// registers, L more in shared memory; what is beyond (N + L) * NT chunks is
+// read in both passes.  Every thread reads its own chunks only, so the shared
+// memory needs a wait for its loads and no barrier.
+template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
     using S = Slice<T, NT>;
     static constexpr int n = S::n;
-    using S::S;
+    static constexpr int lds_chunks = L * NT;
+    static constexpr int kUnroll = 2;   // registers are taken
     u32x4 v[N];
     float e;
+    u32x4 *lds;   // [L][NT]
 
+    __device__ __forceinline__ Held(const T *p, int len, int part, int parts, u32x4 *room)
+        : S(p, len, part, parts), lds(room)
+    {
+    }
     __device__ __forceinline__ void load()
     {
         const int t = threadIdx.x;
@@ -304,16 +394,63 @@ template <typename T, int NT, int N> struct Held : Slice<T, NT> {
             if (at < S::c1)
                 v[i] = *S::chunk(at);
         }
+        if constexpr (L > 0) {
+            u32x4 *wave = lds + wave_id_uniform() * kWave;
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int at = S::c0 + (N + i) * NT + t;
+                if (at < S::c1)
+                    load_to_lds(S::chunk(at), wave + i * NT);
+            }
+        }
     }
-    __device__ __forceinline__ void stats(float c, float &m, float &s) const
+    // f(chunk, values) for each held chunk, then for those beyond
+    template <bool First, typename F> __device__ __forceinline__ void each(F &&f) const
     {
+        const int t = threadIdx.x;
 #pragma unroll
         for (int i = 0; i < N; ++i)
             if (S::c0 + i * NT < S::c1) {
                 float x[n];
                 Pack<T>::open(v[i], x);
-                absorb<n>(x, c, m, s);
+                f(S::c0 + i * NT + t, x);
             }
+        if constexpr (L > 0) {
+            // the loads into shared memory are this wave's own; the first pass waits for them
+            if constexpr (First)
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int at = S::c0 + (N + i) * NT + t;
+                if (at < S::c1) {
+                    float x[n];
+                    Pack<T>::open(lds[i * NT + t], x);
+                    f(at, x);
+                }
+            }
+            int i = S::c0 + (N + L) * NT + t;
+            for (; i + (kUnroll - 1) * NT < S::c1; i += kUnroll * NT) {
+                u32x4 w[kUnroll];
+#pragma unroll
+                for (int j = 0; j < kUnroll; ++j)
+                    w[j] = *S::chunk(i + j * NT);
+#pragma unroll
+                for (int j = 0; j < kUnroll; ++j) {
+                    float x[n];
+                    Pack<T>::open(w[j], x);
+                    f(i + j * NT, x);
+                }
+            }
+            for (; i < S::c1; i += NT) {
+                float x[n];
+                Pack<T>::open(*S::chunk(i), x);
+                f(i, x);
+            }
+        }
+    }
+    __device__ __forceinline__ void stats(const Scale &c, float &m, float &s) const
+    {
+        each<true>([&](int, const float (&x)[n]) { absorb<n>(x, c, m, s); });
         const float x[1] = {e};
         absorb<1>(x, c, m, s);
     }
@@ -324,20 +461,58 @@ template <typename T, int NT, int N> struct Held : Slice<T, NT> {
         if (S::has_edge(t))
             Pack<T>::put(out + S::edge_at(t), d.at(e));
         T *base = out + S::cut.head;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = S::c0 + i * NT + t;
+        each<false>([&](int at, float (&x)[n]) {
             if (at < S::c1) {
-                float x[n];
-                Pack<T>::open(v[i], x);
 #pragma unroll
                 for (int k = 0; k < n; ++k)
                     x[k] = d.at(x[k]);
                 store_chunk<T>(base + (size_t)at * n, x, aligned);
             }
-        }
+        });
     }
 };
+
+// Calls f with the row source that fits rows of `len` values.  A work-group of
+// 1024 threads has 128 registers a thread and 160 KB of shared memory: it holds
+// 16 chunks a thread (256 KB) in registers, up to 400 KB with 9 chunks in shared
+// memory, and 464 KB with 20 and 9; longer rows are read twice beyond that.
+// `taken`: bytes of shared memory that the caller needs itself; where they leave
+// no room for chunks, a long row is read twice as a whole.
+template <typename T, typename F> void with_source(int len, size_t taken, F &&f)
+{
+    const long chunks = (long)len * (long)sizeof(T) / 16;
+    const bool room = taken + 9 * 1024 * 16 <= (160u << 10) - 512;
+    if (chunks <= 256)
+        f.template operator()<64, Held<T, 64, 4>>();
+    else if (chunks <= 1024)
+        f.template operator()<256, Held<T, 256, 4>>();
+    else if (chunks <= 2048)
+        f.template operator()<256, Held<T, 256, 8>>();
+    else if (chunks <= 4096)
+        f.template operator()<512, Held<T, 512, 8>>();
+    else if (chunks <= 8192)
+        f.template operator()<1024, Held<T, 1024, 8>>();
+    else if (chunks <= 16384)
+        f.template operator()<1024, Held<T, 1024, 16>>();
+    else if (!room)
+        f.template operator()<1024, Streamed<T, 1024>>();
+    else if (chunks <= 25600)
+        f.template operator()<1024, Held<T, 1024, 16, 9>>();
+    else
+        f.template operator()<1024, Held<T, 1024, 20, 9>>();
+}
+
+// The same for a pass that reads the row once.
+template <typename T, typename F> void with_stream(int len, F &&f)
+{
+    const long chunks = (long)len * (long)sizeof(T) / 16;
+    if (chunks <= 512)
+        f.template operator()<64, Streamed<T, 64>>();
+    else if (chunks <= 4096)
+        f.template operator()<256, Streamed<T, 256>>();
+    else
+        f.template operator()<1024, Streamed<T, 1024>>();
+}
 
 // Zeros over the slice's elements of an output row (cut by the output's own
 // alignment: nothing is read).

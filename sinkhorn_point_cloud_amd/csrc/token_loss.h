@@ -34,11 +34,17 @@ struct TokenWs {
     float *zlab;    // [T] label's logit; parts > 1 only
 };
 
-// Per row: logp and lse (either may be NULL), and (maximum, sum) for a later
-// gradient pass (may be NULL).
+// What a row's statistics leave for a later pass: its maximum, sum and the
+// label's log-probability before it is rounded.
+struct RowStat {
+    float M, S;
+    double logp;
+};
+
+// Per row, each may be NULL.
 struct LogpOut {
     float *logp, *lse;
-    float2 *stat;
+    RowStat *stat;
 };
 hipError_t launch_logp(const LogitRows &r, const int32_t *labels, const Packed &p,
                        const TokenWs &w, const LogpOut &out, hipStream_t st);
@@ -46,15 +52,15 @@ hipError_t launch_logp(const LogitRows &r, const int32_t *labels, const Packed &
 // dlogits = G_t scale (1[v = label] - softmax), the softmax found on the way
 hipError_t launch_logp_backward(const LogitRows &r, const int32_t *labels, const float *G,
                                 const TokenWs &w, hipStream_t st);
-// the same with the rows' (maximum, sum) given
+// the same with the rows' statistics given
 hipError_t launch_label_grad(const LogitRows &r, const int32_t *labels, const Packed &p,
-                             const float2 *stat, const float *G, hipStream_t st);
+                             const RowStat *stat, const float *G, hipStream_t st);
 
 struct PolicyArgs {
     const float *old, *ref, *adv, *weights;
     int adv_per_token, mean;
-    double lo, hi, kl;
-    float2 *info;   // [T] scratch: row weight and advantage
+    double lo, hi, log_lo, log_hi, kl;
+    float2 *info;   // [T] scratch: row weight and advantage, where they are found beforehand
     float2 *term;   // [T] scratch: weighted loss and KL of a row
     float *loss, *kl_out, *logp;
 };
@@ -66,7 +72,7 @@ struct PreferenceArgs {
     int kind, mean;
     double beta, smoothing;
     float *coef;    // [T] scratch: dloss/dlogp of a row
-    float2 *stat;   // [T] scratch
+    RowStat *stat;  // [T] scratch
     float *loss, *reward, *logp;
 };
 hipError_t launch_preference(const LogitRows &r, const int32_t *labels, const Packed &p,

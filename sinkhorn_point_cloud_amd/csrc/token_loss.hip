@@ -5,10 +5,12 @@
 // sum of 2^((z_v - M) c), c = s log2(e):
 //     logp = s (z_y - M) - ln S,        lse = s M + ln S,
 //     d logp / d z_v = s (1[v = y] - q_v),   q_v = 2^((z_v - M) c) / S.
-// Sums and maxima are fp32 over non-negative terms; the logarithm and every
-// per-row scalar behind it (ratios, clipping decisions, KL terms) are fp64 in
-// one wave, so a ratio is clipped by the same decision as in 64 bits unless it
-// is within a few 1e-7 of the border.
+// Sums and maxima are fp32 over non-negative terms.  The log-probability is put
+// together in fp64 (off by about 1e-7) and so are its differences to given ones:
+// a ratio is clipped by the same decision as in 64 bits unless it is that near
+// the border.  Ratio and KL term are fp32 functions of those differences; a
+// double-precision exponential and logarithm, several hundred instructions in
+// one wave with the others waiting, cost 2 us a row.
 //
 // What bounds it: HBM.  A row is read once and its gradient written once.
 #include "rows.h"
@@ -47,11 +49,23 @@ struct LabelArgs {
     Packed p;
     TokenWs w;
     int parts;
-    float c;
+    Scale c;
     LogpOut out;
     PolicyArgs pol;
     const float *G;   // dL/dlogp of a row; a row of 0 is not read
+    int fold;         // the policy loss finds a row's weight in the row's own work-group
 };
+
+struct SeqRange {
+    long first, last;
+};
+__device__ __forceinline__ SeqRange seq_range(const Packed &p, int i, long T)
+{
+    SeqRange r;
+    r.first = min(max((long)p.offsets[i], 0l), T);
+    r.last = min(max((long)p.offsets[i + 1], r.first), T);
+    return r;
+}
 
 __device__ __forceinline__ RowState row_state(const LabelArgs &a, long t, int label)
 {
@@ -63,10 +77,16 @@ __device__ __forceinline__ RowState row_state(const LabelArgs &a, long t, int la
 
 struct LogpMode {
     static constexpr bool kGradient = false;
-    __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, float M, float S,
-                                                     float zy, bool writes)
+    struct Row {};
+    template <int NT>
+    __device__ __forceinline__ static Row begin(const LabelArgs &, long, int *)
     {
-        const double lnS = log((double)S), s = a.r.scale;
+        return Row{};
+    }
+    __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &,
+                                                     float M, float S, float zy, bool writes)
+    {
+        const double lnS = ln_of(S), s = a.r.scale;
         const bool none = S == 0.f;
         if (writes && lane_id() == 0) {
             if (a.out.logp)
@@ -74,7 +94,7 @@ struct LogpMode {
             if (a.out.lse)
                 a.out.lse[t] = none ? -kInf : (float)((double)M * s + lnS);
             if (a.out.stat)
-                a.out.stat[t] = make_float2(M, S);
+                a.out.stat[t] = RowStat{M, S, none ? 0.0 : ((double)zy - (double)M) * s - lnS};
         }
         return RowScalars{0.f, 0.f, 0.f, 1};
     }
@@ -85,15 +105,21 @@ struct LogpMode {
         if (a.out.lse)
             a.out.lse[t] = 0.f;
         if (a.out.stat)
-            a.out.stat[t] = make_float2(0.f, 0.f);
+            a.out.stat[t] = RowStat{0.f, 0.f, 0.0};
     }
 };
 
 // The gradient alone, of given dL/dlogp.
 struct BackwardMode {
     static constexpr bool kGradient = true;
-    __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, float M, float S,
-                                                     float zy, bool)
+    struct Row {};
+    template <int NT>
+    __device__ __forceinline__ static Row begin(const LabelArgs &, long, int *)
+    {
+        return Row{};
+    }
+    __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &,
+                                                     float M, float S, float zy, bool)
     {
         const double add = (double)a.G[t] * a.r.scale;
         const bool none = S == 0.f;
@@ -104,26 +130,83 @@ struct BackwardMode {
     __device__ __forceinline__ static void unused(const LabelArgs &, long) {}
 };
 
+// e^g - 1 - g to fp32 precision: the series where the difference would cancel
+// (|g| < 1: the first term left out, g^12/12!, is below 2^-27 of the value)
+__device__ __forceinline__ float exp_over(float g)
+{
+    if (!(fabsf(g) < 1.f)) {
+        const float e = ex2(g * kLog2e);
+        return e == kInf ? e : e - 1.f - g;   // a label of probability 0: infinite
+    }
+    float r = 1.f / 39916800.f;
+    r = fmaf(r, g, 1.f / 3628800.f);
+    r = fmaf(r, g, 1.f / 362880.f);
+    r = fmaf(r, g, 1.f / 40320.f);
+    r = fmaf(r, g, 1.f / 5040.f);
+    r = fmaf(r, g, 1.f / 720.f);
+    r = fmaf(r, g, 1.f / 120.f);
+    r = fmaf(r, g, 1.f / 24.f);
+    r = fmaf(r, g, 1.f / 6.f);
+    r = fmaf(r, g, 0.5f);
+    return r * g * g;
+}
+
 struct PolicyMode {
     static constexpr bool kGradient = true;
-    __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, float M, float S,
-                                                     float zy, bool writes)
+    struct Row {
+        float w, adv;   // row weight and advantage
+    };
+    // Every thread of the work-group, while the row's loads are in flight.
+    template <int NT>
+    __device__ __forceinline__ static Row begin(const LabelArgs &a, long t, int *room)
     {
         const PolicyArgs &q = a.pol;
-        const float2 info = q.info[t];
+        if (!a.fold) {
+            const float2 info = q.info[t];
+            return Row{info.x, info.y};
+        }
+        // the sequence is the number of sequences that end at or before t
+        const int lane = lane_id();
+        const bool ends = lane < a.p.n && (long)a.p.offsets[lane + 1] <= t;
+        const int i = min((int)__popcll(__ballot(ends)), a.p.n - 1);
+        double w = q.weights ? (double)q.weights[i] : 1.0;
+        if (q.mean) {
+            const SeqRange r = seq_range(a.p, i, a.r.T);
+            int n = 0;
+            for (long k = r.first + threadIdx.x; k < r.last; k += NT)
+                n += a.labels[k] >= 0;
+            n = wave_sum(n);
+            if constexpr (NT > kWave) {
+                if (lane == 0)
+                    room[threadIdx.x / kWave] = n;
+                __syncthreads();
+                n = wave_sum(lane < NT / kWave ? room[lane] : 0);
+            }
+            w = n ? w / (double)n : 0.0;
+        }
+        return Row{(float)w, q.adv[q.adv_per_token ? t : i]};
+    }
+    __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &info,
+                                                     float M, float S, float zy, bool writes)
+    {
+        const PolicyArgs &q = a.pol;
         const bool none = S == 0.f;
-        const double s = a.r.scale, w = info.x, adv = info.y;
-        const double logp = ((double)zy - (double)M) * s - log((double)S);
-        const double ratio = exp(logp - (double)q.old[t]);
-        const bool above = adv > 0.0 && ratio > q.hi;
-        const bool below = adv < 0.0 && ratio < q.lo;
-        const double gain = (above ? q.hi : below ? q.lo : ratio) * adv;
-        double slope = above || below ? 0.0 : -ratio * adv;   // d(-gain)/d logp
+        const double s = a.r.scale, w = (double)info.w;
+        const float adv = info.adv;
+        const double logp = ((double)zy - (double)M) * s - ln_of(S);
+        // the clipping decision is taken on the log-ratio, in fp64
+        const double change = logp - (double)q.old[t];
+        const float ratio = ex2((float)(change * kLog2eD));
+        const bool above = adv > 0.f && change > q.log_hi;
+        const bool below = adv < 0.f && change < q.log_lo;
+        const double gain = (above ? q.hi : below ? q.lo : (double)ratio) * (double)adv;
+        double slope = above || below ? 0.0 : -(double)ratio * (double)adv;   // d(-gain)/d logp
         double kl = 0.0;
         if (q.ref) {
-            const double gap = (double)q.ref[t] - logp, em = expm1(gap);
-            kl = isinf(em) ? em : em - gap;   // a label of probability 0: infinite
-            slope -= q.kl * em;
+            const float gap = (float)((double)q.ref[t] - logp);
+            const float over = exp_over(gap);   // e^gap - 1 - gap
+            kl = (double)over;
+            slope -= q.kl * ((double)over + (double)gap);
         }
         if (writes && lane_id() == 0) {
             if (q.logp)
@@ -146,9 +229,9 @@ struct PolicyMode {
 // The row's gradient from its scalars; `zy` is the label's logit.
 template <typename T, typename Src>
 __device__ __forceinline__ void write_gradient(const Src &src, T *out, int label, float zy,
-                                               const RowScalars &k, float c)
+                                               const RowScalars &k, const Scale &c)
 {
-    const Dense d{k.A, k.M, c};
+    const Dense d{k.A, k.M, c.hi};
     src.dense(out, d);
     if (src.owner(label) == (int)threadIdx.x)
         Pack<T>::put(out + label, d.at(zy) + k.add);
@@ -158,7 +241,9 @@ __device__ __forceinline__ void write_gradient(const Src &src, T *out, int label
 template <typename T, int NT, typename Src, typename Mode>
 __global__ __launch_bounds__(NT) void row_kernel(LabelArgs a)
 {
+    extern __shared__ u32x4 chunks[];   // [Src::lds_chunks]
     __shared__ float2 room[NT / kWave];
+    __shared__ int count[NT / kWave];
     __shared__ RowScalars scal;
     const long t = group_index();
     if (t >= a.r.T)
@@ -178,14 +263,15 @@ __global__ __launch_bounds__(NT) void row_kernel(LabelArgs a)
         return;
     }
     const T *row = (const T *)a.r.logits + t * a.r.ld;
-    Src src(row, V, 0, 1);
+    Src src(row, V, 0, 1, chunks);
     const float zy = label < V ? Pack<T>::get(row + label) : __builtin_nanf("");
     src.load();
+    const typename Mode::Row info = Mode::template begin<NT>(a, t, count);
     float M = -kInf, S = 0.f;
     src.stats(a.c, M, S);
     merge_group<NT>(M, S, a.c, room);
     if (threadIdx.x < kWave) {
-        const RowScalars k = Mode::row(a, t, M, S, zy, true);
+        const RowScalars k = Mode::row(a, t, info, M, S, zy, true);
         if (threadIdx.x == 0)
             scal = k;
     }
@@ -223,7 +309,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void part_kernel(Labe
 }
 
 // (M, S) of a row from its partial ones, in every lane of the calling wave.
-__device__ __forceinline__ void merge_parts(const float2 *part, int parts, float c, float &M,
+__device__ __forceinline__ void merge_parts(const float2 *part, int parts, const Scale &c, float &M,
                                             float &S)
 {
     M = -kInf;
@@ -231,7 +317,7 @@ __device__ __forceinline__ void merge_parts(const float2 *part, int parts, float
     for (int i = lane_id(); i < parts; i += kWave) {
         const float2 p = part[i];
         const float mn = fmaxf(M, p.x), at = shift_of(mn);
-        S = S * ex2((M - at) * c) + p.y * ex2((p.x - at) * c);
+        S = S * c.pow(M - at) + p.y * c.pow(p.x - at);
         M = mn;
     }
     merge_wave(M, S, c);
@@ -242,6 +328,7 @@ __device__ __forceinline__ void merge_parts(const float2 *part, int parts, float
 template <typename T, typename Mode>
 __global__ __launch_bounds__(kSplit) void join_kernel(LabelArgs a, int run)
 {
+    __shared__ int count[kSplit / kWave];
     __shared__ RowScalars scal;
     const long t = group_index() / run;
     const int part = (int)(group_index() % run), V = a.r.V;
@@ -261,10 +348,11 @@ __global__ __launch_bounds__(kSplit) void join_kernel(LabelArgs a, int run)
         return;
     }
     const float zy = a.w.zlab[t];
+    const typename Mode::Row info = Mode::template begin<kSplit>(a, t, count);
     if (threadIdx.x < kWave) {
         float M, S;
         merge_parts(a.w.part + t * a.parts, a.parts, a.c, M, S);
-        const RowScalars k = Mode::row(a, t, M, S, zy, part == 0);
+        const RowScalars k = Mode::row(a, t, info, M, S, zy, part == 0);
         if (threadIdx.x == 0)
             scal = k;
     }
@@ -284,10 +372,10 @@ struct GradArgs {
     LogitRows r;
     const int32_t *labels;
     Packed p;
-    const float2 *stat;
+    const RowStat *stat;
     const float *G;
     int parts;
-    float c;
+    Scale c;
 };
 
 // The gradient of rows whose statistics are known.
@@ -302,10 +390,10 @@ template <typename T> __global__ __launch_bounds__(kSplit) void label_grad_kerne
     const RowState state = row_state(a.p, t, a.r.T, label);
     if (state == kOutside)
         return;
-    const float2 k0 = state == kUsed ? a.stat[t] : make_float2(0.f, 0.f);
-    const float M = k0.x;
-    const double shrink = 1.0 / (double)k0.y;   // softmax = 2^((z - M) c) * shrink
-    const bool none = k0.y == 0.f;
+    const RowStat k0 = state == kUsed ? a.stat[t] : RowStat{0.f, 0.f, 0.0};
+    const float M = k0.M;
+    const double shrink = 1.0 / (double)k0.S;   // softmax = 2^((z - M) c) * shrink
+    const bool none = k0.S == 0.f;
     const double add = (state == kUsed ? (double)a.G[t] : 0.0) * a.r.scale;
     if (state == kZeroRow || none) {
         zero_row<T, kSplit>(out, V, part, a.parts);
@@ -317,7 +405,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void label_grad_kerne
     const float zy = mine ? Pack<T>::get(row + label) : 0.f;
     // a label beyond the row has no log-probability: NaN, like its loss
     const RowScalars k{label < V ? (float)(-add * shrink) : __builtin_nanf(""), M, (float)add, 0};
-    const Dense d{k.A, k.M, a.c};
+    const Dense d{k.A, k.M, a.c.hi};
     src.dense(out, d);
     if (mine)
         Pack<T>::put(out + label, d.at(zy) + k.add);
@@ -327,31 +415,20 @@ template <typename T> __global__ __launch_bounds__(kSplit) void label_grad_kerne
 
 constexpr int kSeqThreads = 1024;
 
-struct SeqRange {
-    long first, last;
-};
-__device__ __forceinline__ SeqRange seq_range(const Packed &p, int i, long T)
-{
-    SeqRange r;
-    r.first = min(max((long)p.offsets[i], 0l), T);
-    r.last = min(max((long)p.offsets[i + 1], r.first), T);
-    return r;
-}
-
 // Sums of up to three fp64 values over the work-group, in a fixed order.
 template <int K> __device__ __forceinline__ void group_sum(double (&v)[K], double *room)
 {
     constexpr int waves = kSeqThreads / kWave;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const double w = wave_sum(v[k]);
+        const double w = sum_wave(v[k]);
         if (lane_id() == 0)
             room[k * waves + threadIdx.x / kWave] = w;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        v[k] = wave_sum(lane_id() < waves ? room[k * waves + lane_id()] : 0.0);
+        v[k] = sum_wave(lane_id() < waves ? room[k * waves + lane_id()] : 0.0);
     __syncthreads();
 }
 
@@ -392,53 +469,67 @@ __global__ __launch_bounds__(kSeqThreads) void policy_sum_kernel(Packed p, long 
     }
 }
 
-// One pair: the two sequences' summed log-ratios, the loss and its slope.
+// One pair: the two sequences' summed log-ratios (half of the threads each),
+// the loss and its slope.
 __global__ __launch_bounds__(kSeqThreads) void preference_kernel(const int32_t *labels, Packed p,
                                                                  long T, PreferenceArgs a)
 {
-    __shared__ double room[2 * kSeqThreads / kWave];
-    const int i = blockIdx.x;
-    double ratio[2], share[2];
-    for (int h = 0; h < 2; ++h) {
-        const SeqRange r = seq_range(p, 2 * i + h, T);
-        double v[2] = {0.0, 0.0};
-        for (long t = r.first + threadIdx.x; t < r.last; t += kSeqThreads)
-            // a row without any finite logit drops out like one without a label
-            if (labels[t] >= 0 && a.stat[t].y != 0.f) {
-                v[0] += (double)a.logp[t] - (a.ref ? (double)a.ref[t] : 0.0);
-                v[1] += 1.0;
-            }
-        group_sum<2>(v, room);
-        share[h] = a.mean ? (v[1] > 0.0 ? 1.0 / v[1] : 0.0) : 1.0;
-        ratio[h] = v[0] * share[h];
+    constexpr int half = kSeqThreads / 2, waves = half / kWave;
+    __shared__ double room[2][2][waves];
+    __shared__ float slopes[2];
+    const int i = blockIdx.x, h = threadIdx.x / half;
+    const SeqRange r = seq_range(p, 2 * i + h, T);
+    const long first = r.first + threadIdx.x % half;
+    double sum = 0.0;
+    int n = 0;
+    for (long t = first; t < r.last; t += half)
+        // a row without any finite logit drops out like one without a label
+        if (labels[t] >= 0 && a.stat[t].S != 0.f) {
+            sum += a.stat[t].logp - (a.ref ? (double)a.ref[t] : 0.0);
+            ++n;
+        }
+    sum = sum_wave(sum);
+    n = wave_sum(n);
+    if (lane_id() == 0) {
+        room[h][0][threadIdx.x % half / kWave] = sum;
+        room[h][1][threadIdx.x % half / kWave] = (double)n;
     }
-    const double beta = a.beta, gap = ratio[0] - ratio[1];
-    const double w = a.weights ? (double)a.weights[i] : 1.0;
-    double loss, slope;
-    if (a.kind == 0) {
-        // -(1 - eps) log sigma(h) - eps log sigma(-h), h = beta gap
-        const double h = beta * gap, eps = a.smoothing;
-        const double far = log1p(exp(-fabs(h)));
-        loss = (1.0 - eps) * (far + fmax(-h, 0.0)) + eps * (far + fmax(h, 0.0));
-        if (h != h)
-            loss = h;
-        slope = beta * (eps - 1.0 / (1.0 + exp(h)));
-    } else {
-        const double d = gap - 0.5 / beta;
-        loss = d * d;
-        slope = 2.0 * d;
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+        double ratio[2], share[2];
+        for (int k = 0; k < 2; ++k) {
+            const double v = sum_wave(lane_id() < waves ? room[k][0][lane_id()] : 0.0);
+            const double c = sum_wave(lane_id() < waves ? room[k][1][lane_id()] : 0.0);
+            share[k] = a.mean ? (c > 0.0 ? 1.0 / c : 0.0) : 1.0;
+            ratio[k] = v * share[k];
+        }
+        const double beta = a.beta, gap = ratio[0] - ratio[1];
+        const double w = a.weights ? (double)a.weights[i] : 1.0;
+        double loss, slope;
+        if (a.kind == 0) {
+            // -(1 - eps) log sigma(h) - eps log sigma(-h), h = beta gap
+            const double x = beta * gap, eps = a.smoothing;
+            const double e = exp(-fabs(x)), far = log1p(e);
+            loss = x != x ? x : (1.0 - eps) * (far + fmax(-x, 0.0)) + eps * (far + fmax(x, 0.0));
+            // sigma(-x)
+            slope = beta * (eps - (x > 0.0 ? e : 1.0) / (1.0 + e));
+        } else {
+            const double d = gap - 0.5 / beta;
+            loss = d * d;
+            slope = 2.0 * d;
+        }
+        if (threadIdx.x == 0) {
+            a.loss[i] = (float)(w * loss);
+            a.reward[2 * i] = (float)(beta * ratio[0]);
+            a.reward[2 * i + 1] = (float)(beta * ratio[1]);
+            slopes[0] = (float)(slope * w * share[0]);
+            slopes[1] = (float)(-slope * w * share[1]);
+        }
     }
-    if (threadIdx.x == 0) {
-        a.loss[i] = (float)(w * loss);
-        a.reward[2 * i] = (float)(beta * ratio[0]);
-        a.reward[2 * i + 1] = (float)(beta * ratio[1]);
-    }
-    for (int h = 0; h < 2; ++h) {
-        const SeqRange r = seq_range(p, 2 * i + h, T);
-        const float k = (float)((h ? -slope : slope) * w * share[h]);
-        for (long t = r.first + threadIdx.x; t < r.last; t += kSeqThreads)
-            a.coef[t] = labels[t] >= 0 ? k : 0.f;
-    }
+    __syncthreads();
+    const float k = slopes[h];
+    for (long t = first; t < r.last; t += half)
+        a.coef[t] = labels[t] >= 0 ? k : 0.f;
 }
 
 }  // namespace
@@ -447,13 +538,15 @@ __global__ __launch_bounds__(kSeqThreads) void preference_kernel(const int32_t *
 
 namespace {
 
-float scale2(double scale) { return (float)(scale * kLog2eD); }
-
-template <typename T, int NT, typename Src, typename Mode>
-void run_rows(const LabelArgs &a, hipStream_t st)
-{
-    hipLaunchKernelGGL((row_kernel<T, NT, Src, Mode>), grid_of(a.r.T), dim3(NT), 0, st, a);
-}
+template <typename T, typename Mode> struct RunRows {
+    const LabelArgs &a;
+    hipStream_t st;
+    template <int NT, typename Src> void operator()() const
+    {
+        hipLaunchKernelGGL((row_kernel<T, NT, Src, Mode>), grid_of(a.r.T), dim3(NT),
+                           (size_t)Src::lds_chunks * 16, st, a);
+    }
+};
 
 template <typename T, typename Mode> void launch_rows(const LabelArgs &a, hipStream_t st)
 {
@@ -463,7 +556,12 @@ template <typename T, typename Mode> void launch_rows(const LabelArgs &a, hipStr
         hipLaunchKernelGGL((join_kernel<T, Mode>), grid_of((long)a.r.T * run), dim3(kSplit), 0, st, a, run);
         return;
     }
-    run_rows<T, 1024, Streamed<T, 1024>, Mode>(a, st);
+    const RunRows<T, Mode> run{a, st};
+    // a loss keeps its launch shape without a gradient: the same to the bit
+    if constexpr (Mode::kGradient)
+        with_source<T>(a.r.V, 0, run);
+    else
+        with_stream<T>(a.r.V, run);
 }
 
 template <typename Mode> hipError_t dispatch_rows(const LabelArgs &a, hipStream_t st)
@@ -477,12 +575,24 @@ template <typename Mode> hipError_t dispatch_rows(const LabelArgs &a, hipStream_
 
 }  // namespace
 
+// A row's weight is found in its own work-group where that is cheap: the
+// sequences are one to a lane, and a sequence's labels a few to a thread.  It
+// saves a launch.
+static int fold_rows(int T, int n) { return n <= kWave && T <= 2048; }
+
+// Work-groups per row.  A row of up to 128 KB is one work-group's (one launch):
+// with few such rows the split saves at most 4 us of the kernels' time (1 row of
+// 128 KB: 10.7 against 6.9 us) and costs another launch.  Longer rows are split
+// while there are too few to keep the compute units loading (1 row of 256 KB:
+// 17.8 against 6.9 us, 64 rows 20.8 against 13.0, 128 rows 23.2 against 20.3, 200
+// rows 25.3 against 30.2), into about 1024 work-groups of at least two chunks a
+// thread.
 int token_parts(int T, int V, int dtype)
 {
-    const long chunks = (long)V * (dtype == 1 ? 2 : 4) / 16;
-    // enough work-groups to fill the device, none with less than two chunks a thread
-    const long want = T > 0 ? (512 + T - 1) / T : 1, most = chunks / (2 * kSplit);
-    return (int)std::max(1l, std::min({want, most, 64l}));
+    const long bytes = (long)V * (dtype == 1 ? 2 : 4), chunks = bytes / 16;
+    if (T < 1 || T > 128 || bytes <= 128 << 10)
+        return 1;
+    return (int)std::min({1024l / T, chunks / (2 * kSplit), 64l});
 }
 
 int grad_parts(int T, int V, int dtype)
@@ -501,15 +611,15 @@ hipError_t launch_logp(const LogitRows &r, const int32_t *labels, const Packed &
     a.p = p;
     a.w = w;
     a.parts = token_parts(r.T, r.V, r.dtype);
-    a.c = scale2(r.scale);
+    a.c = scale_of_row(r.scale);
     a.out = out;
     return dispatch_rows<LogpMode>(a, st);
 }
 
 hipError_t launch_label_grad(const LogitRows &r, const int32_t *labels, const Packed &p,
-                             const float2 *stat, const float *G, hipStream_t st)
+                             const RowStat *stat, const float *G, hipStream_t st)
 {
-    GradArgs a{r, labels, p, stat, G, grad_parts(r.T, r.V, r.dtype), scale2(r.scale)};
+    GradArgs a{r, labels, p, stat, G, grad_parts(r.T, r.V, r.dtype), scale_of_row(r.scale)};
     const dim3 grid = grid_of((long)r.T * a.parts);
     if (r.dtype == 1)
         hipLaunchKernelGGL((label_grad_kernel<uint16_t>), grid, dim3(kSplit), 0, st, a);
@@ -526,7 +636,7 @@ hipError_t launch_logp_backward(const LogitRows &r, const int32_t *labels, const
     a.labels = labels;
     a.w = w;
     a.parts = token_parts(r.T, r.V, r.dtype);
-    a.c = scale2(r.scale);
+    a.c = scale_of_row(r.scale);
     a.G = G;
     return dispatch_rows<BackwardMode>(a, st);
 }
@@ -535,15 +645,17 @@ hipError_t launch_policy(const LogitRows &r, const int32_t *labels, const Packed
                          const PolicyArgs &q, const TokenWs &w, hipStream_t st)
 {
     if (r.T > 0) {
-        hipLaunchKernelGGL(policy_rows_kernel, dim3(p.n), dim3(kSeqThreads), 0, st, labels, p,
-                           (long)r.T, q);
         LabelArgs a{};
+        a.fold = fold_rows(r.T, p.n);
+        if (!a.fold)
+            hipLaunchKernelGGL(policy_rows_kernel, dim3(p.n), dim3(kSeqThreads), 0, st, labels, p,
+                               (long)r.T, q);
         a.r = r;
         a.labels = labels;
         a.p = p;
         a.w = w;
         a.parts = token_parts(r.T, r.V, r.dtype);
-        a.c = scale2(r.scale);
+        a.c = scale_of_row(r.scale);
         a.pol = q;
         const hipError_t e = dispatch_rows<PolicyMode>(a, st);
         if (e)

@@ -16,16 +16,17 @@ that overlap, and graphs that are replayed, need one each.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
-from . import SK_BF16, SK_F32, _check, _check_out, _ptr, load_library
+from . import SK_BF16, SK_F32, _check, _check_out, load_library
 
 SK_OP_TOKEN_LOGPROBS, SK_OP_POLICY_LOSS, SK_OP_PREFERENCE_LOSS, SK_OP_DISTILL_LOSS, \
     SK_OP_BALANCE_LOSS = range(5)
 SK_LOSS_MEAN, SK_LOSS_FILL, SK_LOSS_ROW_ADVANTAGE = 1, 2, 4
+_TYPES = {torch.float32: SK_F32, torch.bfloat16: SK_BF16}
 PREFERENCE_KINDS = {"sigmoid": 0, "square": 1}
 
 LOSS_EXPORTS = ("sinkhorn_losses_workspace_bytes", "sinkhorn_token_logprobs",
@@ -57,20 +58,25 @@ def losses_workspace_bytes(op: int, T: int, V: int, k: int, dtype: int) -> int:
     return int(load_library().sinkhorn_losses_workspace_bytes(op, T, V, k, dtype))
 
 
+# a pure function of its arguments: training loops ask for the same sizes again and again
+_space_bytes = functools.lru_cache(maxsize=4096)(losses_workspace_bytes)
+
+
 def _rows(logits):
     """(logits, dtype code, rows, columns, row distance); copies a layout the kernels do not take."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a [T, V] tensor")
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+    dt = _TYPES.get(logits.dtype)
+    if dt is None:
         raise TypeError("logits must be float32 or bfloat16")
     if not logits.is_cuda:
         raise ValueError("logits must be a GPU tensor")
     T, V = logits.shape
-    if V > 0 and T > 0 and ((V > 1 and logits.stride(1) != 1)
-                            or (T > 1 and logits.stride(0) < V)):
-        logits = logits.contiguous()
-    ld = logits.stride(0) if T > 1 else V
-    return logits, SK_F32 if logits.dtype == torch.float32 else SK_BF16, T, V, max(ld, V)
+    if logits.is_contiguous():
+        return logits, dt, T, V, V
+    if (V > 1 and logits.stride(1) != 1) or (T > 1 and logits.stride(0) < V):
+        return logits.contiguous(), dt, T, V, V
+    return logits, dt, T, V, logits.stride(0) if T > 1 else V
 
 
 def _row_array(x, shape, dtype, device, what, optional=False):
@@ -81,10 +87,10 @@ def _row_array(x, shape, dtype, device, what, optional=False):
         raise TypeError(f"{what} must be a tensor")
     if x.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {x.dtype}")
-    if tuple(x.shape) != tuple(shape) or x.device != device:
+    if x.shape != shape or x.device != device:
         raise ValueError(f"{what} must be {tuple(shape)} on {device}, got {tuple(x.shape)} "
                          f"on {x.device}")
-    return x.contiguous()
+    return x if x.is_contiguous() else x.contiguous()
 
 
 def _offsets(offsets, device):
@@ -93,15 +99,20 @@ def _offsets(offsets, device):
     return _row_array(offsets, offsets.shape, torch.int64, device, "offsets")
 
 
+def _at(x):
+    """Address of a tensor for the C ABI (None: NULL)."""
+    return None if x is None else x.data_ptr()
+
+
 def _new_gradient(logits, ld):
     T, V = logits.shape
     if V < ld <= 2 * V:   # padded rows: the same distance keeps both at the same alignment
-        return torch.empty(T, ld, dtype=logits.dtype, device=logits.device)[:, :V]
-    return torch.empty(T, V, dtype=logits.dtype, device=logits.device)
+        return torch.empty((T, ld), dtype=logits.dtype, device=logits.device)[:, :V], ld
+    return torch.empty((T, V), dtype=logits.dtype, device=logits.device), V
 
 
 def _check_gradient(d, logits):
-    """(row distance) of a caller's gradient buffer."""
+    """Row distance of a caller's gradient buffer."""
     if d is None:
         return 0
     if not isinstance(d, torch.Tensor):
@@ -115,26 +126,24 @@ def _check_gradient(d, logits):
 
 
 def _space(op, T, V, k, dt, device, workspace):
-    need = losses_workspace_bytes(op, T, V, k, dt)
-    if workspace is not None:
-        if workspace.device != device or workspace.dtype != torch.uint8 \
-                or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-        if workspace.numel() < need:
-            raise ValueError(f"workspace of {need} bytes needed, {workspace.numel()} given")
-        return workspace
-    return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    need = _space_bytes(op, T, V, k, dt)
+    if workspace is None:
+        return torch.empty(need or 1, dtype=torch.uint8, device=device)
+    if workspace.device != device or workspace.dtype != torch.uint8 \
+            or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    if workspace.numel() < need:
+        raise ValueError(f"workspace of {need} bytes needed, {workspace.numel()} given")
+    return workspace
 
 
-def _device(device):
-    """The device of the tensors as the current one, for the launch."""
+def _run(entry, device, *args):
+    """Calls an entry point on the current stream of the tensors' device."""
     if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
-def _stream_of(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        _check(entry(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(entry(*args, torch.cuda.current_stream(device).cuda_stream))
 
 
 def token_logprobs(logits, labels, scale: float = 1.0, out=None, workspace=None):
@@ -152,10 +161,8 @@ def token_logprobs(logits, labels, scale: float = 1.0, out=None, workspace=None)
         logp = torch.empty(T, dtype=torch.float32, device=dev)
         lse = torch.empty(T, dtype=torch.float32, device=dev)
     ws = _space(SK_OP_TOKEN_LOGPROBS, T, V, 0, dt, dev, workspace)
-    with _device(dev):
-        _check(lib.sinkhorn_token_logprobs(_ptr(logits), dt, ld, _ptr(labels), T, V, scale,
-                                           _ptr(logp), _ptr(lse), _ptr(ws), ws.numel(),
-                                           _stream_of(dev)))
+    _run(lib.sinkhorn_token_logprobs, dev, _at(logits), dt, ld, _at(labels), T, V, scale,
+         _at(logp), _at(lse), _at(ws), ws.numel())
     return logp, lse
 
 
@@ -166,13 +173,13 @@ def token_logprobs_backward(logits, labels, grad, scale: float = 1.0, out=None, 
     dev = logits.device
     labels = _row_array(labels, (T,), torch.int32, dev, "labels")
     grad = _row_array(grad, (T,), torch.float32, dev, "grad")
-    d = out if out is not None else _new_gradient(logits, ld)
-    dld = _check_gradient(d, logits)
+    if out is None:
+        d, dld = _new_gradient(logits, ld)
+    else:
+        d, dld = out, _check_gradient(out, logits)
     ws = _space(SK_OP_TOKEN_LOGPROBS, T, V, 0, dt, dev, workspace)
-    with _device(dev):
-        _check(lib.sinkhorn_token_logprobs_backward(_ptr(logits), dt, ld, _ptr(labels), _ptr(grad),
-                                                    T, V, scale, _ptr(d), dld, _ptr(ws),
-                                                    ws.numel(), _stream_of(dev)))
+    _run(lib.sinkhorn_token_logprobs_backward, dev, _at(logits), dt, ld, _at(labels), _at(grad), T,
+         V, scale, _at(d), dld, _at(ws), ws.numel())
     return d
 
 
@@ -201,6 +208,7 @@ def policy_loss(logits, labels, offsets, old, adv, ref=None, clip=(0.2, 0.2), kl
     flags = (SK_LOSS_MEAN if mean else 0) | (SK_LOSS_ROW_ADVANTAGE if per_row else 0)
     if out is not None:
         loss, kls, logp, d = out
+        dld = _check_gradient(d, logits)
         if loss is None or kls is None:
             raise ValueError("out needs loss and kl tensors")
         _check_out(((loss, (n,)), (kls, (n,)), (logp, (T,))), torch.float32, dev, "out")
@@ -209,15 +217,11 @@ def policy_loss(logits, labels, offsets, old, adv, ref=None, clip=(0.2, 0.2), kl
         loss = torch.empty(n, dtype=torch.float32, device=dev)
         kls = torch.empty(n, dtype=torch.float32, device=dev)
         logp = torch.empty(T, dtype=torch.float32, device=dev)
-        d = _new_gradient(logits, ld) if grad else None
-    dld = _check_gradient(d, logits)
+        d, dld = _new_gradient(logits, ld) if grad else (None, 0)
     ws = _space(SK_OP_POLICY_LOSS, T, V, 0, dt, dev, workspace)
-    with _device(dev):
-        _check(lib.sinkhorn_policy_loss(_ptr(logits), dt, ld, _ptr(labels), T, V, _ptr(offsets), n,
-                                        _ptr(old), _ptr(adv), _ptr(ref), _ptr(weights), scale,
-                                        clip[0], clip[1], kl, flags, _ptr(loss), _ptr(kls),
-                                        _ptr(logp), _ptr(d), dld, _ptr(ws), ws.numel(),
-                                        _stream_of(dev)))
+    _run(lib.sinkhorn_policy_loss, dev, _at(logits), dt, ld, _at(labels), T, V, _at(offsets), n,
+         _at(old), _at(adv), _at(ref), _at(weights), scale, clip[0], clip[1], kl, flags, _at(loss),
+         _at(kls), _at(logp), _at(d), dld, _at(ws), ws.numel())
     return loss, kls, logp, d
 
 
@@ -246,6 +250,7 @@ def preference_loss(logits, labels, offsets, ref=None, beta: float = 0.1, smooth
     flags = SK_LOSS_MEAN if mean else 0
     if out is not None:
         loss, reward, logp, d = out
+        dld = _check_gradient(d, logits)
         if loss is None or reward is None or logp is None:
             raise ValueError("out needs loss, reward and logp tensors")
         _check_out(((loss, (n // 2,)), (reward, (n,)), (logp, (T,))), torch.float32, dev, "out")
@@ -254,15 +259,11 @@ def preference_loss(logits, labels, offsets, ref=None, beta: float = 0.1, smooth
         loss = torch.empty(n // 2, dtype=torch.float32, device=dev)
         reward = torch.empty(n, dtype=torch.float32, device=dev)
         logp = torch.empty(T, dtype=torch.float32, device=dev)
-        d = _new_gradient(logits, ld) if grad else None
-    dld = _check_gradient(d, logits)
+        d, dld = _new_gradient(logits, ld) if grad else (None, 0)
     ws = _space(SK_OP_PREFERENCE_LOSS, T, V, 0, dt, dev, workspace)
-    with _device(dev):
-        _check(lib.sinkhorn_preference_loss(_ptr(logits), dt, ld, _ptr(labels), T, V,
-                                            _ptr(offsets), n // 2, _ptr(ref), _ptr(weights), scale,
-                                            PREFERENCE_KINDS[kind], beta, smoothing, flags,
-                                            _ptr(loss), _ptr(reward), _ptr(logp), _ptr(d), dld,
-                                            _ptr(ws), ws.numel(), _stream_of(dev)))
+    _run(lib.sinkhorn_preference_loss, dev, _at(logits), dt, ld, _at(labels), T, V, _at(offsets), n
+         // 2, _at(ref), _at(weights), scale, PREFERENCE_KINDS[kind], beta, smoothing, flags,
+         _at(loss), _at(reward), _at(logp), _at(d), dld, _at(ws), ws.numel())
     return loss, reward, logp, d
 
 
@@ -288,18 +289,16 @@ def distill_loss(logits, index, teacher, teacher_lse=None, temperature: float = 
         raise ValueError(f"temperature must be positive, got {temperature}")
     if out is not None:
         loss, d = out
+        dld = _check_gradient(d, logits)
         if loss is None:
             raise ValueError("out needs a loss tensor")
         _check_out(((loss, (T,)),), torch.float32, dev, "out")
     else:
         loss = torch.empty(T, dtype=torch.float32, device=dev)
-        d = _new_gradient(logits, ld) if grad else None
-    dld = _check_gradient(d, logits)
+        d, dld = _new_gradient(logits, ld) if grad else (None, 0)
     ws = _space(SK_OP_DISTILL_LOSS, T, V, K, dt, dev, workspace)
-    with _device(dev):
-        _check(lib.sinkhorn_distill_loss(_ptr(logits), dt, ld, T, V, _ptr(index), _ptr(teacher), K,
-                                         _ptr(teacher_lse), _ptr(weights), temperature, _ptr(loss),
-                                         _ptr(d), dld, _ptr(ws), ws.numel(), _stream_of(dev)))
+    _run(lib.sinkhorn_distill_loss, dev, _at(logits), dt, ld, T, V, _at(index), _at(teacher), K,
+         _at(teacher_lse), _at(weights), temperature, _at(loss), _at(d), dld, _at(ws), ws.numel())
     return loss, d
 
 
@@ -325,6 +324,7 @@ def balance_loss(logits, index, offsets=None, balance: float = 1.0, z: float = 0
     flags = 0
     if out is not None:
         loss, zloss, counts, d = out
+        dld = _check_gradient(d, logits)
         if loss is None or zloss is None or counts is None:
             raise ValueError("out needs loss, zloss and counts tensors")
         _check_out(((loss, (G,)), (zloss, (G,))), torch.float32, dev, "out")
@@ -334,12 +334,8 @@ def balance_loss(logits, index, offsets=None, balance: float = 1.0, z: float = 0
         loss = torch.empty(G, dtype=torch.float32, device=dev)
         zloss = torch.empty(G, dtype=torch.float32, device=dev)
         counts = torch.empty(G, E, dtype=torch.int32, device=dev)
-        d = _new_gradient(logits, ld) if grad else None
-    dld = _check_gradient(d, logits)
+        d, dld = _new_gradient(logits, ld) if grad else (None, 0)
     ws = _space(SK_OP_BALANCE_LOSS, T, E, G, dt, dev, workspace)
-    with _device(dev):
-        _check(lib.sinkhorn_balance_loss(_ptr(logits), dt, ld, T, E, _ptr(index), K,
-                                         _ptr(offsets), G, balance, z, flags, _ptr(loss),
-                                         _ptr(zloss), _ptr(counts), _ptr(d), dld, _ptr(ws),
-                                         ws.numel(), _stream_of(dev)))
+    _run(lib.sinkhorn_balance_loss, dev, _at(logits), dt, ld, T, E, _at(index), K, _at(offsets), G,
+         balance, z, flags, _at(loss), _at(zloss), _at(counts), _at(d), dld, _at(ws), ws.numel())
     return loss, zloss, counts, d

@@ -9,6 +9,13 @@ joins add 30 more, each rounding by 2^-24.  So the sum S is off, relative, by at
     eps_S = 2^-24 (2 + 2.1 log2 V + V/512 + 100),
 lse and logp by eps_S and their own rounding (2^-24 relative), and an element q_v of the softmax,
 relative, by eps_S + 2^-23 + 3 ln 2 2^-24 |argument| + 4 roundings.
+
+The logarithm of S, taken as its exponent and the logarithm of its mantissa, is off by 2^-24,
+which the 30 above leave room for (at most 10 joins take place).
+
+A teacher's probability p_k is an fp32 exponential of an argument formed in fp64 and rounded once
+(2^-24 |argument|), over the fp32 sum of K of them (K/64 + 10 additions), divided and stored: off,
+relative, by at most 2^-24 (14 + K/64 + |argument|).
 """
 import math
 
@@ -192,13 +199,17 @@ def distill(logits, index, teacher, teacher_lse=None, temperature=1.0, weights=N
         terms = p * (v - U0 - lq)
         loss[t] = w * tau * tau * torch.where(p > 0, terms, 0.0).sum()
         C = float(p.sum())
-        # p is rounded once (U each); log q is off by eps_S
-        loss_tol[t] = abs(w) * tau * tau * (C * eps_sum(V) + U * float(terms.abs().sum())) \
+        base = v.max() if teacher_lse is None else U0
+        p_off = U * (14 + idx.shape[1] / 64 + (v - base).abs())
+        # the terms follow p; log q and the teacher's own logarithm are off by eps_S at most
+        loss_tol[t] = abs(w) * tau * tau * (2 * C * eps_sum(V) + float((p_off * terms.abs()).sum())) \
             + 2 * U * abs(loss[t])
         sparse = torch.zeros(V, dtype=torch.float64).index_add_(0, at, p)
         grad[t] = w * tau * (C * R.q[t] - sparse)
         entries = int(keep.sum())
-        tol[t] = abs(w) * tau * (C * (R.q_tol[t] + 5 * U * R.q[t]) + (5 + entries) * U * sparse)
+        off = torch.zeros(V, dtype=torch.float64).index_add_(0, at, p * p_off)
+        tol[t] = abs(w) * tau * (C * (R.q_tol[t] + 5 * U * R.q[t]) + (5 + entries) * U * sparse
+                                 + off + float(off.sum()) * R.q[t])
     tol = tol + HALF[R.dtype] * (grad.abs() + tol) * 1.01 + 1e-38
     return (loss, loss_tol), (grad, tol)
 
