@@ -22,7 +22,8 @@
  *     gradient row is 0.  A label of V or more gives NaN where it enters,
  *     nothing is read out of range.
  *   - Packed sequences: offsets [n + 1] int64, non-decreasing; sequence i is
- *     rows offsets[i] <= t < offsets[i + 1] (empty ones are allowed).  Rows
+ *     rows offsets[i] <= t < offsets[i + 1] (empty ones are allowed; at most
+ *     2^20 sequences, pairs or groups).  Rows
  *     before the first and behind the last sequence are left as they are in
  *     every row output, or get zeros with SK_LOSS_FILL.
  *   - A logit of -inf has no probability (masked vocabulary, disabled expert).

@@ -11,6 +11,7 @@ namespace sk {
 namespace {
 
 constexpr int kMaxRows = 1 << 24;
+constexpr int kMaxSequences = 1 << 20;   // a work-group of 1024 threads each: 2^30 in a launch
 constexpr int64_t kMaxStride = 1ll << 38;   // rows x stride x 4 bytes stays below 2^64
 
 size_t elem(int dtype) { return dtype == SK_BF16 ? 2 : 4; }
@@ -29,9 +30,10 @@ Ws carve(Carve &c, int op, int T, int V, int k, int dtype)
     const size_t rows = (size_t)T;
     if (op == SK_OP_BALANCE_LOSS) {
         w.balance.count_chunks = balance_count_chunks(T, k);
-        w.balance.grad_chunks = balance_grad_chunks(T, V, k);
+        w.balance.grad_chunks = balance_grad_chunks(T, k);
         w.balance.count_part = c.take<int32_t>((size_t)w.balance.count_chunks * (V + 2));
         w.balance.sum_part = c.take<double>((size_t)w.balance.grad_chunks * 2);
+        w.balance.rows = c.take<int32_t>(k);
         return w;
     }
     const int parts = token_parts(T, V, dtype);
@@ -57,7 +59,7 @@ bool sizes_ok(int op, int T, int V, int k)
     if (T < 0 || T > kMaxRows || V < 1)
         return false;
     if (op == SK_OP_BALANCE_LOSS)
-        return V <= kMaxExperts && k >= 1 && k <= kMaxRows;
+        return V <= kMaxExperts && k >= 1 && k <= kMaxSequences;
     return V <= kMaxRows && (op != SK_OP_DISTILL_LOSS || (k >= 1 && k <= kMaxTopK));
 }
 
@@ -123,9 +125,9 @@ int check_scale(double scale, const char *what)
 
 int check_packed(const int64_t *offsets, int n, unsigned flags, unsigned known)
 {
-    if (!offsets || n < 1 || n > kMaxRows)
+    if (!offsets || n < 1 || n > kMaxSequences)
         return fail(SK_ERR_INVALID_ARG, "%d sequences need 1 <= n <= %d and device offsets", n,
-                    kMaxRows);
+                    kMaxSequences);
     if (flags & ~known)
         return fail(SK_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
     return SK_OK;
@@ -323,9 +325,9 @@ int sinkhorn_balance_loss(const void *logits, int dtype, int64_t ld, int T, int 
         return rc;
     if (K < 1 || K > kMaxChosen)
         return fail(SK_ERR_INVALID_ARG, "K=%d must be in [1, %d]", K, kMaxChosen);
-    if (G < 1 || G > kMaxRows || (!offsets && G != 1))
+    if (G < 1 || G > kMaxSequences || (!offsets && G != 1))
         return fail(SK_ERR_INVALID_ARG, "%d groups need 1 <= G <= %d, and offsets unless G is 1",
-                    G, kMaxRows);
+                    G, kMaxSequences);
     if (flags & ~SK_LOSS_FILL)
         return fail(SK_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
     if (!loss || !zloss || !counts || (T > 0 && !index))

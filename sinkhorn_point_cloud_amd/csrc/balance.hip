@@ -13,10 +13,15 @@
 // gradient needs anyway, is also all that the loss needs.  Since sum_e p = 1,
 // f - 1 stands for f in those differences: near balance nothing cancels.
 //
-// Three launches: counts per chunk of rows; gradient, each work-group summing
-// its group's counts first; sums per group.  Chunks lie within one group and
-// the sums are taken in a fixed order: no atomics in memory, the same result
-// every time.
+// Large batches take three launches: counts per chunk of rows; gradient, each
+// work-group summing its group's counts first; sums per group.  Small ones take
+// one, a work-group per group doing all of it: 512 rows of 8 experts in 7 us
+// against 12 for the three, and two launches fewer for the host.  Chunks lie within one
+// group and the sums are taken in a fixed order: no atomics in memory, the same
+// result every time.
+//
+// A row is 16 lanes' (reductions are lane moves within a row of the wave), four
+// rows to a wave, the next row loaded while one is worked on.
 //
 // What bounds it: HBM for large batches, the launches for small ones.
 #include "rows.h"
@@ -31,7 +36,10 @@ using rows::shift_of;
 using rows::grid_of;
 using rows::group_index;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;    // a chunk's work-group
+constexpr int kCounters = 1024;  // a counting work-group, and a small group's
+constexpr int kLanes = 16;       // lanes of a row
+constexpr int kFillers = 64;     // work-groups that zero the rows outside every group
 
 // Where a chunk of `size` rows lies: its group, its rows, and the group's chunks.
 struct Place {
@@ -86,28 +94,26 @@ __device__ Place place_of(const BalanceArgs &a, long chunk, long size)
     return r;
 }
 
-// Tokens per expert, rows with a choice and bad indices of one chunk of rows.
-__global__ __launch_bounds__(kThreads) void count_kernel(BalanceArgs a, BalanceWs w, long size)
+// Adds the choices of rows [first, last) to hist [E + 2]: tokens per expert,
+// rows with a choice, indices out of range.
+template <int NT>
+__device__ __forceinline__ void count_rows(const BalanceArgs &a, long first, long last, int *hist)
 {
-    extern __shared__ int hist[];   // [E + 2]
-    const long chunk = group_index();
-    const Place at = place_of(a, chunk, size);
-    if (at.group < 0)
-        return;
-    for (int e = threadIdx.x; e < a.E + 2; e += kThreads)
-        hist[e] = 0;
-    __syncthreads();
     int rows = 0, bad = 0;
-    for (long t = at.first + threadIdx.x; t < at.last; t += kThreads) {
+    for (long t = first + threadIdx.x; t < last; t += NT) {
         const int32_t *idx = a.index + t * a.K;
         bool any = false;
-        for (int k = 0; k < a.K; ++k) {
-            const int e = idx[k];
-            if (e >= a.E)
-                ++bad;
-            else if (e >= 0) {
-                any = true;
-                atomicAdd(&hist[e], 1);
+        for (int k = 0; k < a.K; k += 8) {
+            int e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                e[j] = k + j < a.K ? idx[k + j] : -1;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                any |= e[j] >= 0 && e[j] < a.E;
+                bad += e[j] >= a.E;
+                if (e[j] >= 0 && e[j] < a.E)
+                    atomicAdd(&hist[e[j]], 1);
             }
         }
         rows += any;
@@ -118,45 +124,211 @@ __global__ __launch_bounds__(kThreads) void count_kernel(BalanceArgs a, BalanceW
         atomicAdd(&hist[a.E], rows);
         atomicAdd(&hist[a.E + 1], bad);
     }
+}
+
+__global__ __launch_bounds__(kCounters) void count_kernel(BalanceArgs a, BalanceWs w, long size)
+{
+    extern __shared__ int hist[];   // [E + 2]
+    const long chunk = group_index();
+    if (chunk >= w.count_chunks)
+        return;
+    const Place at = place_of(a, chunk, size);
+    if (at.group < 0)
+        return;
+    for (int e = threadIdx.x; e < a.E + 2; e += kCounters)
+        hist[e] = 0;
+    __syncthreads();
+    count_rows<kCounters>(a, at.first, at.last, hist);
     __syncthreads();
     int32_t *out = w.count_part + chunk * (a.E + 2);
-    for (int e = threadIdx.x; e < a.E + 2; e += kThreads)
+    for (int e = threadIdx.x; e < a.E + 2; e += kCounters)
         out[e] = hist[e];
 }
 
-// Reductions over the L lanes of a row.
-template <int L> __device__ __forceinline__ float lanes_sum(float v)
+__device__ __forceinline__ float lanes_max(float v)
 {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1)
-        v += __shfl_xor(v, o, kWave);
-    return v;
+    v = fmaxf(v, dpp_move<kDppXor1>(v));
+    v = fmaxf(v, dpp_move<kDppXor2>(v));
+    v = fmaxf(v, dpp_move<kDppHalfMirror>(v));
+    return fmaxf(v, dpp_move<kDppMirror>(v));
 }
-template <int L> __device__ __forceinline__ float lanes_max(float v)
-{
+
+// R values a lane, W of them side by side; Wide: in one load or store, where
+// every row starts on such a boundary and E is a multiple of W.  A lane's columns
+// are the same either way, and with them the order of every sum.
+template <typename T, int R, bool Wide> struct Values {
+    static constexpr int W = R < 4 ? R : 4;
+    struct alignas(W * sizeof(T)) Word {
+        T v[W];
+    };
+    Word w[R / W];
+    int first;   // the row's first index
+
+    __device__ __forceinline__ static int column(int r, int lane)
+    {
+        return (r / W * kLanes + lane) * W + r % W;
+    }
+    __device__ __forceinline__ void load(const BalanceArgs &a, long t, int lane)
+    {
+        const T *row = (const T *)a.logits + t * a.ld;
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1)
-        v = fmaxf(v, __shfl_xor(v, o, kWave));
+        for (int i = 0; i < R / W; ++i) {
+            const int c = column(i * W, lane);
+            if constexpr (Wide) {
+                if (c < a.E)
+                    w[i] = *reinterpret_cast<const Word *>(row + c);
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    if (c + j < a.E)
+                        w[i].v[j] = row[c + j];
+            }
+        }
+        int any = -1;
+        for (int k = lane; k < a.K; k += kLanes)
+            any = max(any, a.index[t * a.K + k]);
+        first = any;
+    }
+};
+
+// The rows [first, last) of one group, NT threads: gradients, and this thread's
+// part of the sums.  f1 [E]: f - 1.
+template <typename T, int NT, int R, bool Wide>
+__device__ __forceinline__ void group_rows(const BalanceArgs &a, long first, long last,
+                                           const float *f1, int n, double &dots, double &squares)
+{
+    using V = Values<T, R, Wide>;
+    constexpr int W = V::W;
+    const int E = a.E, lane = threadIdx.x % kLanes, slots = NT / kLanes;
+    float f[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int c = V::column(r, lane);
+        f[r] = c < E ? f1[c] : 0.f;
+    }
+    const float over = n ? 1.f / (float)n : 0.f;
+    const float alpha = (float)a.balance * over, zeta = (float)(2.0 * a.z) * over;
+    V next;
+    const long t0 = first + threadIdx.x / kLanes;
+    if (t0 < last)
+        next.load(a, t0, lane);
+    // all lanes of a wave stay together: the lane moves need them
+    const long rounds = (last - first + slots - 1) / slots;
+    for (long i = 0; i < rounds; ++i) {
+        const long t = t0 + i * slots;
+        const V now = next;
+        if (t + slots < last)
+            next.load(a, t + slots, lane);
+        const bool row = t < last;
+        float x[R], m = -kInf, s = 0.f, dot = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            x[r] = row && V::column(r, lane) < E ? Pack<T>::get(&now.w[r / W].v[r % W]) : -kInf;
+            m = fmaxf(m, x[r]);
+        }
+        const bool chose = lanes_max(row && now.first >= 0 ? 1.f : 0.f) > 0.f;
+        m = lanes_max(m);
+        const float shift = shift_of(m);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            x[r] = ex2((x[r] - shift) * kLog2e);
+            s += x[r];
+            dot = fmaf(x[r], f[r], dot);
+        }
+        s = row16_sum(s);
+        dot = row16_sum(dot);
+        const bool used = chose && s != 0.f;
+        const float inv = used ? 1.f / s : 0.f, lse = used ? m + (float)rows::ln_of(s) : 0.f;
+        dot *= inv;
+        if (used && lane == 0) {
+            dots += 1.0 + (double)dot;
+            squares += (double)lse * (double)lse;
+        }
+        if (a.dlogits && row) {
+            T *out = (T *)a.dlogits + t * a.dld;
+            const float base = fmaf(zeta, lse, -alpha * dot);
+#pragma unroll
+            for (int i = 0; i < R / W; ++i) {
+                const int c = V::column(i * W, lane);
+                typename V::Word y;
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    Pack<T>::put(&y.v[j], used ? x[i * W + j] * inv *
+                                                     fmaf(alpha, f[i * W + j], base)
+                                               : 0.f);
+                if constexpr (Wide) {
+                    if (c < E)
+                        *reinterpret_cast<typename V::Word *>(out + c) = y;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < W; ++j)
+                        if (c + j < E)
+                            out[c + j] = y.v[j];
+                }
+            }
+        }
+    }
+}
+
+// The two sums over the work-group, in a fixed order; thread 0 and 1 get them.
+template <int NT>
+__device__ __forceinline__ double group_sums(double dots, double squares, double *room)
+{
+    constexpr int waves = NT / kWave;
+    dots = rows::sum_wave(dots);
+    squares = rows::sum_wave(squares);
+    if (lane_id() == 0) {
+        room[threadIdx.x / kWave] = dots;
+        room[waves + threadIdx.x / kWave] = squares;
+    }
+    __syncthreads();
+    double v = 0.0;
+    if (threadIdx.x < 2)
+        for (int i = 0; i < waves; ++i)
+            v += room[threadIdx.x * waves + i];
     return v;
 }
 
-// One chunk of rows, L lanes to a row and R values to a lane.
-template <typename T, int L, int R>
+// Zeros over the rows outside every group, one of kFillers work-groups.
+template <typename T, int NT> __device__ void fill_rows(const BalanceArgs &a, int filler)
+{
+    const long first = clamp_row(a.offsets[0], a.T);
+    const long last = max(clamp_row(a.offsets[a.G], a.T), first);
+    const long count = first + a.T - last;
+    for (long i = filler * (NT / kWave) + threadIdx.x / kWave; i < count;
+         i += (long)kFillers * (NT / kWave)) {
+        T *out = (T *)a.dlogits + (i < first ? i : last + i - first) * a.dld;
+        for (int e = lane_id(); e < a.E; e += kWave)
+            Pack<T>::put(out + e, 0.f);
+    }
+}
+
+// One chunk of rows.
+template <typename T, int R, bool Wide>
 __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a, BalanceWs w, long size,
                                                            long count_size)
 {
-    extern __shared__ float f1[];   // [E]: f - 1
+    extern __shared__ int dyn[];   // [E + 2] counts, [E] f - 1
     __shared__ double room[2 * kThreads / kWave];
     const long chunk = group_index();
+    if (chunk >= w.grad_chunks) {
+        if (a.fill && a.offsets && a.dlogits && chunk < w.grad_chunks + kFillers)
+            fill_rows<T, kThreads>(a, (int)(chunk - w.grad_chunks));
+        return;
+    }
     const Place at = place_of(a, chunk, size);
     if (at.group < 0)
         return;
     const int E = a.E, K = a.K;
+    int *count = dyn;
+    float *f1 = (float *)(dyn + E + 2);
+    for (int e = threadIdx.x; e < E + 2; e += kThreads)
+        count[e] = 0;
     // the group's counts, from its chunks of the first pass
     long c0 = 0, cn = (a.T + count_size - 1) / count_size;
     if (a.offsets) {
         // chunks of the groups before this one
-        for (int g = threadIdx.x % kWave; g < at.group; g += kWave) {
+        for (int g = lane_id(); g < at.group; g += kWave) {
             const long b = clamp_row(a.offsets[g], a.T);
             c0 += (max(clamp_row(a.offsets[g + 1], a.T), b) - b + count_size - 1) / count_size;
         }
@@ -165,220 +337,175 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a, Balanc
         cn = (max(clamp_row(a.offsets[at.group + 1], a.T), b) - b + count_size - 1) / count_size;
         cn = min(cn, w.count_chunks - c0);
     }
+    __syncthreads();
     const int32_t *part = w.count_part + c0 * (E + 2);
-    int n = 0, bad = 0;
-    for (long i = lane_id(); i < cn; i += kWave) {
-        n += part[i * (E + 2) + E];
-        bad += part[i * (E + 2) + E + 1];
+    for (int e = lane_id(); e < E + 2; e += kWave) {
+        int c = 0;
+#pragma unroll 8
+        for (long i = threadIdx.x / kWave; i < cn; i += kThreads / kWave)
+            c += part[i * (E + 2) + e];
+        atomicAdd(&count[e], c);
     }
-    n = wave_sum(n);
-    bad = wave_sum(bad);
+    __syncthreads();
+    const int n = count[E], bad = count[E + 1];
     const double per = n ? (double)E / ((double)K * (double)n) : 0.0;
     for (int e = threadIdx.x; e < E; e += kThreads) {
-        int c = 0;
-        for (long i = 0; i < cn; ++i)
-            c += part[i * (E + 2) + e];
-        f1[e] = bad ? __builtin_nanf("") : (float)((double)c * per - 1.0);
+        f1[e] = bad ? __builtin_nanf("") : (float)((double)count[e] * per - 1.0);
         if (chunk == at.chunk0)
-            a.counts[(long)at.group * E + e] = c;
+            a.counts[(long)at.group * E + e] = count[e];
     }
+    if (chunk == at.chunk0 && threadIdx.x == 0)
+        w.rows[at.group] = n;
     __syncthreads();
-
-    const int lane = threadIdx.x % L, slot = threadIdx.x / L;
-    float f[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-        f[r] = lane + r * L < E ? f1[lane + r * L] : 0.f;
-    const float over = n ? 1.f / (float)n : 0.f;
-    const float alpha = (float)a.balance * over, zeta = (float)(2.0 * a.z) * over;
     double dots = 0.0, squares = 0.0;
-    for (long t = at.first + slot; t < at.last; t += kThreads / L) {
-        const T *row = (const T *)a.logits + t * a.ld;
-        T *out = a.dlogits ? (T *)a.dlogits + t * a.dld : nullptr;
-        int chose = 0;
-        for (int k = lane; k < K; k += L) {
-            const int e = a.index[t * K + k];
-            chose |= e >= 0;
-        }
-        float x[R], m = -kInf, s = 0.f, dot = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            x[r] = lane + r * L < E ? Pack<T>::get(row + lane + r * L) : -kInf;
-            m = fmaxf(m, x[r]);
-        }
-        chose = lanes_max<L>((float)chose) > 0.f;
-        m = lanes_max<L>(m);
-        const float shift = shift_of(m);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            x[r] = ex2((x[r] - shift) * kLog2e);
-            s += x[r];
-            dot = fmaf(x[r], f[r], dot);
-        }
-        s = lanes_sum<L>(s);
-        dot = lanes_sum<L>(dot);
-        const bool used = chose && s != 0.f;
-        const float inv = used ? 1.f / s : 0.f, lse = used ? m + logf(s) : 0.f;
-        dot *= inv;
-        if (used && lane == 0) {
-            dots += 1.0 + (double)dot;
-            squares += (double)lse * (double)lse;
-        }
-        if (out) {
-            const float base = fmaf(zeta, lse, -alpha * dot);
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (lane + r * L < E)
-                    Pack<T>::put(out + lane + r * L,
-                                 used ? x[r] * inv * fmaf(alpha, f[r], base) : 0.f);
-        }
-    }
-    dots = wave_sum(dots);
-    squares = wave_sum(squares);
-    if (lane_id() == 0) {
-        room[threadIdx.x / kWave] = dots;
-        room[kThreads / kWave + threadIdx.x / kWave] = squares;
-    }
-    __syncthreads();
-    if (threadIdx.x < 2) {
-        double v = 0.0;
-        for (int i = 0; i < kThreads / kWave; ++i)
-            v += room[threadIdx.x * (kThreads / kWave) + i];
+    group_rows<T, kThreads, R, Wide>(a, at.first, at.last, f1, n, dots, squares);
+    const double v = group_sums<kThreads>(dots, squares, room);
+    if (threadIdx.x < 2)
         w.sum_part[2 * chunk + threadIdx.x] = v;
-    }
 }
 
-// The losses of one group; the counts of a group without rows; with `fill`,
-// zeros over the rows outside every group (by the groups before and behind).
+// The losses of one group; the counts of a group without rows.
 __global__ __launch_bounds__(kThreads) void balance_sum_kernel(BalanceArgs a, BalanceWs w,
-                                                               long size, long count_size)
+                                                               long size)
 {
-    __shared__ double room[kThreads / kWave][2];
-    __shared__ long seen[kThreads / kWave][2];
+    __shared__ double room[2 * kThreads / kWave];
     const int g = blockIdx.x, E = a.E;
     const long T = a.T;
-    long b = 0, e = T, c0 = 0, k0 = 0;
+    long b = 0, e = T, c0 = 0;
     if (a.offsets) {
-        for (int i = threadIdx.x; i < g; i += kThreads) {
+        for (int i = lane_id(); i < g; i += kWave) {
             const long bi = clamp_row(a.offsets[i], T);
-            const long len = max(clamp_row(a.offsets[i + 1], T), bi) - bi;
-            c0 += (len + size - 1) / size;
-            k0 += (len + count_size - 1) / count_size;
+            c0 += (max(clamp_row(a.offsets[i + 1], T), bi) - bi + size - 1) / size;
         }
         c0 = wave_sum(c0);
-        k0 = wave_sum(k0);
-        if (lane_id() == 0) {
-            seen[threadIdx.x / kWave][0] = c0;
-            seen[threadIdx.x / kWave][1] = k0;
-        }
-        __syncthreads();
-        c0 = k0 = 0;
-        for (int i = 0; i < kThreads / kWave; ++i) {
-            c0 += seen[i][0];
-            k0 += seen[i][1];
-        }
         b = clamp_row(a.offsets[g], T);
         e = max(clamp_row(a.offsets[g + 1], T), b);
     }
-    // the caps hold for offsets in order; out of order they keep the reads in bounds
+    // the cap holds for offsets in order; out of order it keeps the reads in bounds
     const long cn = min((e - b + size - 1) / size, w.grad_chunks - c0);
-    const long kn = min((e - b + count_size - 1) / count_size, w.count_chunks - k0);
-    double v[2] = {0.0, 0.0};
+    double dots = 0.0, squares = 0.0;
     for (long i = threadIdx.x; i < cn; i += kThreads) {
-        v[0] += w.sum_part[2 * (c0 + i)];
-        v[1] += w.sum_part[2 * (c0 + i) + 1];
+        dots += w.sum_part[2 * (c0 + i)];
+        squares += w.sum_part[2 * (c0 + i) + 1];
     }
-    int n = 0;
-    for (long i = 0; i < kn; ++i)
-        n += w.count_part[(k0 + i) * (E + 2) + E];
-    v[0] = wave_sum(v[0]);
-    v[1] = wave_sum(v[1]);
-    if (lane_id() == 0) {
-        room[threadIdx.x / kWave][0] = v[0];
-        room[threadIdx.x / kWave][1] = v[1];
-    }
-    __syncthreads();
+    const double v = group_sums<kThreads>(dots, squares, room);
     if (threadIdx.x < 2) {
-        double s = 0.0;
-        for (int i = 0; i < kThreads / kWave; ++i)
-            s += room[i][threadIdx.x];
-        (threadIdx.x ? a.zloss : a.loss)[g] = n ? (float)(s / (double)n) : 0.f;
+        const int n = cn > 0 ? w.rows[g] : 0;
+        (threadIdx.x ? a.zloss : a.loss)[g] = n ? (float)(v / (double)n) : 0.f;
     }
     if (cn <= 0)
         for (int i = threadIdx.x; i < E; i += kThreads)
             a.counts[(long)g * E + i] = 0;
 }
 
-template <typename T> __global__ void fill_kernel(BalanceArgs a)
+// A small group as a whole.
+template <typename T, int R, bool Wide>
+__global__ __launch_bounds__(kCounters) void balance_small_kernel(BalanceArgs a)
 {
-    const long t = group_index();
-    if (t >= a.T)
+    extern __shared__ int dyn[];   // [E + 2] counts, [E] f - 1
+    __shared__ double room[2 * kCounters / kWave];
+    const int g = blockIdx.x, E = a.E;
+    if (g >= a.G) {
+        fill_rows<T, kCounters>(a, g - a.G);
         return;
-    const long first = clamp_row(a.offsets[0], a.T), last = clamp_row(a.offsets[a.G], a.T);
-    if (t >= first && t < last)
-        return;
-    T *out = (T *)a.dlogits + t * a.dld;
-    for (int e = threadIdx.x; e < a.E; e += kWave)
-        Pack<T>::put(out + e, 0.f);
+    }
+    const long first = a.offsets ? clamp_row(a.offsets[g], a.T) : 0;
+    const long last = a.offsets ? max(clamp_row(a.offsets[g + 1], a.T), first) : a.T;
+    int *count = dyn;
+    float *f1 = (float *)(dyn + E + 2);
+    for (int e = threadIdx.x; e < E + 2; e += kCounters)
+        count[e] = 0;
+    __syncthreads();
+    count_rows<kCounters>(a, first, last, count);
+    __syncthreads();
+    const int n = count[E], bad = count[E + 1];
+    const double per = n ? (double)E / ((double)a.K * (double)n) : 0.0;
+    for (int e = threadIdx.x; e < E; e += kCounters) {
+        f1[e] = bad ? __builtin_nanf("") : (float)((double)count[e] * per - 1.0);
+        a.counts[(long)g * E + e] = count[e];
+    }
+    __syncthreads();
+    double dots = 0.0, squares = 0.0;
+    group_rows<T, kCounters, R, Wide>(a, first, last, f1, n, dots, squares);
+    const double v = group_sums<kCounters>(dots, squares, room);
+    if (threadIdx.x < 2)
+        (threadIdx.x ? a.zloss : a.loss)[g] = n ? (float)(v / (double)n) : 0.f;
 }
 
-// Rows of a chunk: about 64 chunks to count, about 1024 work-groups for the rest.
+// Rows of a chunk: 64 chunks or more to count, about 1024 work-groups for the rest.
 long count_size(int T) { return std::max(256l, ((long)T + 63) / 64); }
-int lanes_of(int E) { return E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64; }
-long grad_size(int T, int E)
+long grad_size(int T)
 {
-    const long pass = kThreads / lanes_of(E);   // rows a work-group takes at once
+    const long pass = kThreads / kLanes;   // rows a work-group takes at once
     const long want = ((long)T + 1023) / 1024;
-    return (want + pass - 1) / pass * pass;
+    return std::max(1l, (want + pass - 1) / pass) * pass;
 }
 
-template <typename T, int L, int R>
+// One work-group per group where that is little work even if a single group
+// holds every row.
+bool small(int T, int E) { return T <= 1024 && (long)T * E <= 65536; }
+
+template <typename T, int R, bool Wide>
 void run(const BalanceArgs &a, const BalanceWs &w, hipStream_t st)
 {
-    hipLaunchKernelGGL((balance_kernel<T, L, R>), grid_of(balance_grad_chunks(a.T, a.E, a.G)),
-                       dim3(kThreads), (size_t)a.E * 4, st, a, w, grad_size(a.T, a.E),
-                       count_size(a.T));
+    const int fillers = a.fill && a.offsets && a.dlogits ? kFillers : 0;
+    const size_t room = (size_t)(2 * a.E + 2) * 4;
+    if (small(a.T, a.E))
+        hipLaunchKernelGGL((balance_small_kernel<T, R, Wide>), dim3(a.G + fillers), dim3(kCounters),
+                           room, st, a);
+    else
+        hipLaunchKernelGGL((balance_kernel<T, R, Wide>), grid_of(w.grad_chunks + fillers),
+                           dim3(kThreads), room, st, a, w, grad_size(a.T), count_size(a.T));
+}
+
+template <typename T, int R>
+void run_width(const BalanceArgs &a, const BalanceWs &w, hipStream_t st)
+{
+    constexpr int W = Values<T, R, true>::W;
+    const bool wide = a.E % W == 0 && a.ld % W == 0 && (!a.dlogits || a.dld % W == 0) &&
+                      ((uintptr_t)a.logits | (uintptr_t)a.dlogits) % (W * sizeof(T)) == 0;
+    if (wide)
+        run<T, R, true>(a, w, st);
+    else
+        run<T, R, false>(a, w, st);
 }
 
 template <typename T> void run_rows(const BalanceArgs &a, const BalanceWs &w, hipStream_t st)
 {
-    if (a.E <= 8)
-        run<T, 8, 1>(a, w, st);
-    else if (a.E <= 16)
-        run<T, 16, 1>(a, w, st);
-    else if (a.E <= 32)
-        run<T, 32, 1>(a, w, st);
-    else if (a.E <= 64)
-        run<T, 64, 1>(a, w, st);
-    else if (a.E <= 128)
-        run<T, 64, 2>(a, w, st);
-    else if (a.E <= 256)
-        run<T, 64, 4>(a, w, st);
-    else if (a.E <= 512)
-        run<T, 64, 8>(a, w, st);
+    if (a.E <= kLanes)
+        run_width<T, 1>(a, w, st);
+    else if (a.E <= 2 * kLanes)
+        run_width<T, 2>(a, w, st);
+    else if (a.E <= 4 * kLanes)
+        run_width<T, 4>(a, w, st);
+    else if (a.E <= 8 * kLanes)
+        run_width<T, 8>(a, w, st);
+    else if (a.E <= 16 * kLanes)
+        run_width<T, 16>(a, w, st);
+    else if (a.E <= 32 * kLanes)
+        run_width<T, 32>(a, w, st);
     else
-        run<T, 64, 16>(a, w, st);
-    if (a.fill && a.offsets && a.dlogits)
-        hipLaunchKernelGGL((fill_kernel<T>), grid_of(a.T), dim3(kWave), 0, st, a);
+        run_width<T, 64>(a, w, st);
 }
 
 }  // namespace
 
 long balance_count_chunks(int T, int G) { return T / count_size(T) + G; }
-long balance_grad_chunks(int T, int E, int G) { return T / std::max(1l, grad_size(T, E)) + G; }
+long balance_grad_chunks(int T, int G) { return T / grad_size(T) + G; }
 
 hipError_t launch_balance(const BalanceArgs &a, const BalanceWs &w, hipStream_t st)
 {
-    if (a.T > 0) {
-        hipLaunchKernelGGL(count_kernel, grid_of(balance_count_chunks(a.T, a.G)), dim3(kThreads),
+    const bool one = small(a.T, a.E);
+    if (!one)
+        hipLaunchKernelGGL(count_kernel, grid_of(w.count_chunks), dim3(kCounters),
                            (size_t)(a.E + 2) * 4, st, a, w, count_size(a.T));
-        if (a.dtype == 1)
-            run_rows<uint16_t>(a, w, st);
-        else
-            run_rows<float>(a, w, st);
-    }
-    hipLaunchKernelGGL(balance_sum_kernel, dim3(a.G), dim3(kThreads), 0, st, a, w,
-                       std::max(1l, grad_size(a.T, a.E)), count_size(a.T));
+    if (a.dtype == 1)
+        run_rows<uint16_t>(a, w, st);
+    else
+        run_rows<float>(a, w, st);
+    if (!one)
+        hipLaunchKernelGGL(balance_sum_kernel, dim3(a.G), dim3(kThreads), 0, st, a, w,
+                           grad_size(a.T));
     return hipGetLastError();
 }
 

@@ -106,10 +106,11 @@ struct BalanceArgs {
 struct BalanceWs {
     int32_t *count_part;   // [count chunks][E + 2]: tokens per expert, rows, bad indices
     double *sum_part;      // [gradient chunks][2]: sums of f . p and of the squared log-sum-exp
+    int32_t *rows;         // [G] rows that take part
     long count_chunks, grad_chunks;
 };
 long balance_count_chunks(int T, int G);
-long balance_grad_chunks(int T, int E, int G);
+long balance_grad_chunks(int T, int G);
 hipError_t launch_balance(const BalanceArgs &a, const BalanceWs &w, hipStream_t st);
 
 constexpr int kMaxTopK = 1024;

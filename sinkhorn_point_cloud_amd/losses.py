@@ -139,11 +139,13 @@ def _space(op, T, V, k, dt, device, workspace):
 
 def _run(entry, device, *args):
     """Calls an entry point on the current stream of the tensors' device."""
-    if device.index == torch.cuda.current_device():
-        _check(entry(*args, torch.cuda.current_stream(device).cuda_stream))
+    index = device.index
+    if index == torch.cuda.current_device():
+        # the raw handle: building a Stream object for it takes 2 us
+        _check(entry(*args, torch._C._cuda_getCurrentRawStream(index)))
     else:
-        with torch.cuda.device(device):
-            _check(entry(*args, torch.cuda.current_stream(device).cuda_stream))
+        with torch.cuda.device(index):
+            _check(entry(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
 def token_logprobs(logits, labels, scale: float = 1.0, out=None, workspace=None):

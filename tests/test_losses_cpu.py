@@ -98,7 +98,7 @@ SPACE = ALL
     ("token_logprobs_backward", dict(grad=None), sk.SK_ERR_INVALID_ARG),
     ("token_logprobs_backward", dict(dlogits=None), sk.SK_ERR_INVALID_ARG),
     *[(n, c, sk.SK_ERR_INVALID_ARG) for n in ("policy_loss", "preference_loss") for c in (
-        dict(offsets=None), dict(n=0), dict(loss=None), dict(flags=64))],
+        dict(offsets=None), dict(n=0), dict(n=(1 << 20) + 1), dict(loss=None), dict(flags=64))],
     *[("policy_loss", c, sk.SK_ERR_INVALID_ARG) for c in (
         dict(old=None), dict(adv=None), dict(klo=None), dict(lo=1.0), dict(lo=-0.1), dict(hi=-0.1),
         dict(hi=math.nan), dict(kl=math.inf))],
@@ -110,7 +110,7 @@ SPACE = ALL
         dict(tau=0.0), dict(tau=-1.0), dict(tau=math.nan))],
     *[("balance_loss", c, sk.SK_ERR_INVALID_ARG) for c in (
         dict(index=None), dict(loss=None), dict(zloss=None), dict(counts=None), dict(K=0),
-        dict(K=65), dict(G=0), dict(G=2, offsets=None), dict(V=1025, ld=1025, dld=1025),
+        dict(K=65), dict(G=0), dict(G=(1 << 20) + 1), dict(G=2, offsets=None), dict(V=1025, ld=1025, dld=1025),
         dict(flags=1), dict(bal=math.nan), dict(z=math.inf))],
 ])
 def test_refusals(lib, name, changes, code):
