@@ -36,16 +36,19 @@ struct Args {
 // student's logit there, and the entries of each owner thread as a linked list.
 struct List {
     int *head;   // [NT] first entry whose element the thread owns, or -1
+    int *mark;   // [NT] bit i: an entry lies in the thread's i-th chunk (modulo 32)
     int *next;   // [K]
     int *token;  // [K]
     float *p;    // [K]
+    float *take; // [K] what the gradient takes away for entry k, see link()
     float *z;    // [K]
     __device__ __forceinline__ List(int *room, int NT, int K)
-        : head(room), next(room + NT), token(next + K), p((float *)(token + K)), z(p + K)
+        : head(room), mark(room + NT), next(mark + NT), token(next + K), p((float *)(token + K)),
+          take(p + K), z(take + K)
     {
     }
 };
-size_t list_bytes(int NT, int K) { return (size_t)(NT + 4 * K) * 4; }
+size_t list_bytes(int NT, int K) { return (size_t)(2 * NT + 5 * K) * 4; }
 
 struct Teacher {
     double C, U;   // sum of p, log-sum-exp
@@ -64,8 +67,12 @@ struct Ahead {
 #pragma unroll
         for (int j = 0; j < n; ++j) {
             const int k = lane_id() + j * kWave;
-            v[j] = k < K ? a.d.index[t * K + k] : -1;
-            u[j] = k < K ? a.d.teacher[t * K + k] : 0.f;
+            v[j] = -1;
+            u[j] = 0.f;
+            if (j * kWave < K && k < K) {
+                v[j] = a.d.index[t * K + k];
+                u[j] = a.d.teacher[t * K + k];
+            }
         }
     }
     // f(k, token, logit) for every entry of this lane
@@ -75,7 +82,7 @@ struct Ahead {
 #pragma unroll
         for (int j = 0; j < n; ++j) {
             const int k = lane_id() + j * kWave;
-            if (k < K)
+            if (j * kWave < K && k < K)   // the first the same for the wave: a branch
                 f(k, v[j], u[j]);
         }
         for (int k = lane_id() + n * kWave; k < K; k += kWave)
@@ -83,13 +90,13 @@ struct Ahead {
     }
 };
 
-// One wave: the teacher's probabilities into the list.  The exponents are formed
-// in fp64, the exponentials and their sum are fp32.
+// One wave: the teacher's probabilities into the list, as fp32 exponentials of
+// the differences to the largest logit, or to the given log-sum-exp (fp64: the
+// two may be far from 0 and near each other).
 __device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const Ahead &in,
                                                 const List &l)
 {
     const int V = a.r.V;
-    const double c = a.r.scale * kLog2eD;   // log2(e) / tau
     float top = -kInf;
     int bad = 0;
     in.each(a, t, [&](int k, int v, float u) {
@@ -103,31 +110,33 @@ __device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const Ahe
     Teacher r;
     r.bad = __any(bad);
     r.any = top != -kInf;
-    // p_k = 2^((u_k - at) c - less) / sum
-    double at = (double)top, less = 0.0;
-    float sum = 1.f;
+    float C = 0.f;
     if (a.d.teacher_lse) {
+        const double c = a.r.scale * kLog2eD;   // log2(e) / tau
         r.U = (double)a.d.teacher_lse[t];
-        at = 0.0;
-        less = r.U * kLog2eD;
+        const double less = r.U * kLog2eD;
+        in.each(a, t, [&](int k, int v, float u) {
+            const float p = r.any && v >= 0 ? ex2((float)((double)u * c - less)) : 0.f;
+            l.p[k] = p;
+            C += p;
+        });
     } else {
         float s = 0.f;
-        in.each(a, t, [&](int, int v, float u) {
-            if (r.any && v >= 0)
-                s += ex2((float)(((double)u - at) * c));
+        in.each(a, t, [&](int k, int v, float u) {
+            const float e = r.any && v >= 0 ? a.c.pow(u - top) : 0.f;
+            l.p[k] = e;
+            s += e;
         });
-        sum = sum_wave(s);
-        r.U = at * a.r.scale + ln_of(sum);
+        s = sum_wave(s);
+        r.U = (double)top * a.r.scale + ln_of(s);
+        const float over = 1.f / s;
+        in.each(a, t, [&](int k, int, float) {
+            const float p = r.any ? l.p[k] * over : 0.f;
+            l.p[k] = p;
+            C += p;
+        });
     }
-    double C = 0.0;
-    in.each(a, t, [&](int k, int v, float u) {
-        // rounded once, to what the gradient subtracts; loss and gradient then
-        // belong to the same distribution
-        const float p = r.any && v >= 0 ? ex2((float)(((double)u - at) * c - less)) / sum : 0.f;
-        l.p[k] = p;
-        C += (double)p;
-    });
-    r.C = sum_wave(C);
+    r.C = (double)sum_wave(C);
     return r;
 }
 
@@ -144,52 +153,88 @@ __device__ __forceinline__ RowScalars student_side(const Args &a, long t, const 
     const int lane = lane_id();
     const double inv = a.r.scale, tau = 1.0 / inv;
     const double w = a.d.weights ? (double)a.d.weights[t] : 1.0;
-    // log p_k - log q_k = (u_k - (z_k - M)) / tau - (U - ln S)
-    double apart = 0.0;
+    // log p_k - log q_k = (u_k - (z_k - M)) / tau - (U - ln S): fp64, for it is
+    // small where the two agree
+    const double apart = r.U - ln_of(S);
+    double sum = 0.0;
     in.each(a, t, [&](int k, int, float u) {
         const double p = (double)l.p[k];
         if (p != 0.0)
-            apart += p * ((double)u - ((double)l.z[k] - (double)M));
+            sum += p * (((double)u - ((double)l.z[k] - (double)M)) * inv - apart);
     });
-    apart = sum_wave(apart) * inv - r.C * (r.U - ln_of(S));
+    sum = sum_wave(sum);
     const bool none = S == 0.f || (!r.any && !r.bad);
     const double nan = __builtin_nan("");
     if (writes && lane == 0)
-        a.d.loss[t] = none ? 0.f : (float)(r.bad ? nan : w * tau * tau * apart);
+        a.d.loss[t] = none ? 0.f : (float)(r.bad ? nan : w * tau * tau * sum);
     const double add = w * tau;
     return RowScalars{(float)(r.bad ? nan : add * r.C / (double)S), M, (float)add, none};
 }
 
-// The elements of the list that this thread owns, written over its dense values.
-template <typename T>
-__device__ __forceinline__ void write_list(const List &l, T *out, int K, const Dense &d, float sub)
-{
-    for (int k = l.head[threadIdx.x]; k >= 0; k = l.next[k]) {
-        const int v = l.token[k];
-        float p = l.p[k];
-        // the same token again?  Then every one of its entries writes the sum, in list order
-        bool twice = false;
-        for (int j = l.head[threadIdx.x]; j >= 0; j = l.next[j])
-            twice |= j != k && l.token[j] == v;
-        if (twice) {
-            p = 0.f;
-            for (int j = 0; j < K; ++j)
-                p += l.token[j] == v ? l.p[j] : 0.f;
-        }
-        Pack<T>::put(out + v, d.at(l.z[k]) - sub * p);
-    }
-}
-
-template <typename T, typename Src>
+// One wave: hands the entries to the threads that own their elements.  Of a
+// token's several entries the first takes away all of it, summed in list order,
+// whatever order the linked list has.
+template <int NT, typename Src>
 __device__ __forceinline__ void link(const List &l, const Src &src, int K)
 {
+    bool twice = false;
     for (int k = lane_id(); k < K; k += kWave) {
         const int v = l.token[k];
         const int who = src.owner(v);
-        if (who >= 0)
-            l.next[k] = atomicExch(&l.head[who], k);
+        l.take[k] = l.p[k];
+        if (who >= 0) {
+            const int before = atomicExch(&l.head[who], k);
+            l.next[k] = before;
+            atomicOr(&l.mark[who], 1 << (src.turn(v) & 31));
+            // every pair of a list's entries is met once
+            for (int j = before; j >= 0; j = l.next[j])
+                twice |= l.token[j] == v;
+        }
     }
+    if (__any(twice))
+        for (int k = lane_id(); k < K; k += kWave) {
+            const int v = l.token[k];
+            float sum = 0.f;
+            bool first = true;
+            for (int j = 0; j < K; ++j)
+                if (l.token[j] == v) {
+                    first &= j >= k;
+                    sum += l.p[j];
+                }
+            l.take[k] = first ? sum : 0.f;
+        }
 }
+
+// The entries that this thread owns, as terms of its gradient values.
+struct ListTerms {
+    const List &l;
+    int first;    // the thread's first entry
+    int mark;
+    float sub;    // -sub take_k at token k
+
+    __device__ __forceinline__ ListTerms(const List &list, float sub)
+        : l(list), first(list.head[threadIdx.x]), mark(list.mark[threadIdx.x]), sub(sub)
+    {
+    }
+    template <int n> __device__ __forceinline__ void chunk(int i, int at, float (&x)[n]) const
+    {
+        if (mark >> (i & 31) & 1)
+            for (int k = first; k >= 0; k = l.next[k]) {
+                const int off = l.token[k] - at;
+                const float s = sub * l.take[k];
+#pragma unroll
+                for (int j = 0; j < n; ++j)
+                    x[j] -= j == off ? s : 0.f;
+            }
+    }
+    __device__ __forceinline__ float edge(int v) const
+    {
+        float s = 0.f;
+        for (int k = first; k >= 0; k = l.next[k])
+            s -= l.token[k] == v ? sub * l.take[k] : 0.f;
+        return s;
+    }
+};
 
 __device__ __forceinline__ bool dropped(const Args &a, long t)
 {
@@ -218,6 +263,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Args a)
     }
     const List l(dyn, NT, K);
     l.head[threadIdx.x] = -1;
+    l.mark[threadIdx.x] = 0;
     __syncthreads();
     const T *row = (const T *)a.r.logits + t * a.r.ld;
     Src src(row, V, 0, 1, chunks);
@@ -232,7 +278,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Args a)
         });
         r = teacher_side(a, t, ahead, l);
         if (grad)
-            link<T>(l, src, K);
+            link<NT>(l, src, K);
     }
     float M = -kInf, S = 0.f;
     src.stats(a.c, M, S);
@@ -250,9 +296,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Args a)
         zero_row<T, NT>(out, V, 0, 1);
         return;
     }
-    const Dense d{k.A, k.M, a.c.hi};
-    src.dense(out, d);
-    write_list<T>(l, out, K, d, k.sub);
+    src.dense(out, Dense{k.A, k.M, a.c.hi}, ListTerms(l, k.sub));
 }
 
 // Few rows: partial statistics, and the student's logits at the list's tokens
@@ -297,6 +341,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
     }
     const List l(dyn, kSplit, K);
     l.head[threadIdx.x] = -1;
+    l.mark[threadIdx.x] = 0;
     __syncthreads();
     const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, run);
     if (threadIdx.x < kWave) {
@@ -306,7 +351,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
         for (int k = lane_id(); k < K; k += kWave)
             l.z[k] = a.d.zk[t * K + k];
         if (grad)
-            link<T>(l, src, K);
+            link<kSplit>(l, src, K);
         float M = -kInf, S = 0.f;
         const float2 *p = a.w.part + t * a.parts;
         for (int i = lane_id(); i < a.parts; i += kWave) {
@@ -327,9 +372,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
         zero_row<T, kSplit>(out, V, part, run);
         return;
     }
-    const Dense d{k.A, k.M, a.c.hi};
-    src.dense(out, d);
-    write_list<T>(l, out, K, d, k.sub);
+    src.dense(out, Dense{k.A, k.M, a.c.hi}, ListTerms(l, k.sub));
 }
 
 template <typename T> struct RunRows {

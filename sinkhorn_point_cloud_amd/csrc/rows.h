@@ -7,9 +7,10 @@
 // worth of values before the first and behind the last of them, the edge; the
 // edge values are dealt one to a thread.  Chunk c0 + i * threads + t belongs to
 // thread t, so that a wave's loads are 1 KB in a run and the thread that owns
-// an element is known from its index alone: an element with a sparse term is
-// written again by the thread that wrote its chunk, in that thread's own
-// program order, and needs no barrier.
+// an element is known from its index alone: that thread adds an element's sparse
+// term to the chunk before it stores it.  (Written again behind the dense store,
+// each such element is a 2- or 4-byte write to a line on its way to memory: 16384
+// rows of 32000 bf16 values with 64 terms took 398 us that way, 367 this way.)
 //
 // The exponentials are taken in base 2: with c = scale log2(e) and the row
 // maximum M, e_v = 2^((x_v - M) c).  The difference is formed first, so a row
@@ -148,6 +149,8 @@ template <typename T, int NT> struct Slice {
         const int c = (v - cut.head) / n;
         return c >= c0 && c < c1 ? (c - c0) % NT : -1;
     }
+    // which of its owner's chunks an owned element of a chunk is in
+    __device__ __forceinline__ int turn(int v) const { return ((v - cut.head) / n - c0) / NT; }
 };
 
 // Reductions over a wave without LDS: over each row of 16 lanes by lane moves,
@@ -261,10 +264,29 @@ __device__ __forceinline__ void merge_group(float &m, float &s, const Scale &c, 
     }
 }
 
-// coefficient x exponential of one row: out_v = A 2^((x_v - M) c), or zeros.
+// coefficient x exponential of one row: out_v = A 2^((x_v - M) c) plus sparse
+// terms.  Those are a `Terms` with
+//     chunk(i, first, x): adds to a thread's i-th chunk, whose first element is `first`,
+//     edge(v):            what to add to element v of the edge.
 struct Dense {
     float A, M, c;
     __device__ __forceinline__ float at(float x) const { return A * ex2((x - M) * c); }
+};
+
+// One term: `add` at element v.
+struct OneTerm {
+    int v;
+    float add;
+    template <int n> __device__ __forceinline__ void chunk(int, int first, float (&x)[n]) const
+    {
+        const int at = v - first;
+        if (at >= 0 && at < n) {
+#pragma unroll
+            for (int k = 0; k < n; ++k)
+                x[k] += k == at ? add : 0.f;
+        }
+    }
+    __device__ __forceinline__ float edge(int u) const { return u == v ? add : 0.f; }
 };
 
 template <typename T>
@@ -321,15 +343,25 @@ template <typename T, int NT> struct Streamed : Slice<T, NT> {
         }
     }
 
-    __device__ __forceinline__ void dense(T *out, const Dense &d) const
+    template <typename Terms>
+    __device__ __forceinline__ void dense(T *out, const Dense &d, const Terms &terms) const
     {
         const int t = threadIdx.x;
         const bool aligned = (((uintptr_t)(out + S::cut.head)) & 15) == 0;
         if (S::has_edge(t)) {
             const int v = S::edge_at(t);
-            Pack<T>::put(out + v, d.at(Pack<T>::get(S::row + v)));
+            Pack<T>::put(out + v, d.at(Pack<T>::get(S::row + v)) + terms.edge(v));
         }
-        T *base = out + S::cut.head;
+        auto put = [&](int i, u32x4 v) {
+            float x[n];
+            Pack<T>::open(v, x);
+#pragma unroll
+            for (int k = 0; k < n; ++k)
+                x[k] = d.at(x[k]);
+            const int first = S::cut.head + i * n;
+            terms.chunk((i - S::c0) / NT, first, x);
+            store_chunk<T>(out + first, x, aligned);
+        };
         int i = S::c0 + t;
         for (; i + (kUnroll - 1) * NT < S::c1; i += kUnroll * NT) {
             u32x4 v[kUnroll];
@@ -337,23 +369,11 @@ template <typename T, int NT> struct Streamed : Slice<T, NT> {
             for (int j = 0; j < kUnroll; ++j)
                 v[j] = *S::chunk(i + j * NT);
 #pragma unroll
-            for (int j = 0; j < kUnroll; ++j) {
-                float x[n];
-                Pack<T>::open(v[j], x);
-#pragma unroll
-                for (int k = 0; k < n; ++k)
-                    x[k] = d.at(x[k]);
-                store_chunk<T>(base + (size_t)(i + j * NT) * n, x, aligned);
-            }
+            for (int j = 0; j < kUnroll; ++j)
+                put(i + j * NT, v[j]);
         }
-        for (; i < S::c1; i += NT) {
-            float x[n];
-            Pack<T>::open(*S::chunk(i), x);
-#pragma unroll
-            for (int k = 0; k < n; ++k)
-                x[k] = d.at(x[k]);
-            store_chunk<T>(base + (size_t)i * n, x, aligned);
-        }
+        for (; i < S::c1; i += NT)
+            put(i, *S::chunk(i));
     }
 };
 
@@ -391,8 +411,10 @@ template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
         for (int i = 0; i < N; ++i) {
             v[i] = u32x4{Pack<T>::kNone, Pack<T>::kNone, Pack<T>::kNone, Pack<T>::kNone};
             const int at = S::c0 + i * NT + t;
+            // read once: kept out of the caches (2048 to 16384 rows of 64 to 256 KB:
+            // 2 to 7% faster, rows of just 128 KB 5% slower)
             if (at < S::c1)
-                v[i] = *S::chunk(at);
+                v[i] = __builtin_nontemporal_load(S::chunk(at));
         }
         if constexpr (L > 0) {
             u32x4 *wave = lds + wave_id_uniform() * kWave;
@@ -404,7 +426,7 @@ template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
             }
         }
     }
-    // f(chunk, values) for each held chunk, then for those beyond
+    // f(this thread's i-th, chunk, values) for each held chunk, then for those beyond
     template <bool First, typename F> __device__ __forceinline__ void each(F &&f) const
     {
         const int t = threadIdx.x;
@@ -413,7 +435,7 @@ template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
             if (S::c0 + i * NT < S::c1) {
                 float x[n];
                 Pack<T>::open(v[i], x);
-                f(S::c0 + i * NT + t, x);
+                f(i, S::c0 + i * NT + t, x);
             }
         if constexpr (L > 0) {
             // the loads into shared memory are this wave's own; the first pass waits for them
@@ -425,7 +447,7 @@ template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
                 if (at < S::c1) {
                     float x[n];
                     Pack<T>::open(lds[i * NT + t], x);
-                    f(at, x);
+                    f(N + i, at, x);
                 }
             }
             int i = S::c0 + (N + L) * NT + t;
@@ -438,35 +460,39 @@ template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
                 for (int j = 0; j < kUnroll; ++j) {
                     float x[n];
                     Pack<T>::open(w[j], x);
-                    f(i + j * NT, x);
+                    f((i - S::c0) / NT + j, i + j * NT, x);
                 }
             }
             for (; i < S::c1; i += NT) {
                 float x[n];
                 Pack<T>::open(*S::chunk(i), x);
-                f(i, x);
+                f((i - S::c0) / NT, i, x);
             }
         }
     }
     __device__ __forceinline__ void stats(const Scale &c, float &m, float &s) const
     {
-        each<true>([&](int, const float (&x)[n]) { absorb<n>(x, c, m, s); });
+        each<true>([&](int, int, const float (&x)[n]) { absorb<n>(x, c, m, s); });
         const float x[1] = {e};
         absorb<1>(x, c, m, s);
     }
-    __device__ __forceinline__ void dense(T *out, const Dense &d) const
+    template <typename Terms>
+    __device__ __forceinline__ void dense(T *out, const Dense &d, const Terms &terms) const
     {
         const int t = threadIdx.x;
         const bool aligned = (((uintptr_t)(out + S::cut.head)) & 15) == 0;
-        if (S::has_edge(t))
-            Pack<T>::put(out + S::edge_at(t), d.at(e));
-        T *base = out + S::cut.head;
-        each<false>([&](int at, float (&x)[n]) {
+        if (S::has_edge(t)) {
+            const int u = S::edge_at(t);
+            Pack<T>::put(out + u, d.at(e) + terms.edge(u));
+        }
+        each<false>([&](int i, int at, float (&x)[n]) {
             if (at < S::c1) {
 #pragma unroll
                 for (int k = 0; k < n; ++k)
                     x[k] = d.at(x[k]);
-                store_chunk<T>(base + (size_t)at * n, x, aligned);
+                const int first = S::cut.head + at * n;
+                terms.chunk(i, first, x);
+                store_chunk<T>(out + first, x, aligned);
             }
         });
     }
@@ -484,6 +510,8 @@ template <typename T, typename F> void with_source(int len, size_t taken, F &&f)
     const bool room = taken + 9 * 1024 * 16 <= (160u << 10) - 512;
     if (chunks <= 256)
         f.template operator()<64, Held<T, 64, 4>>();
+    else if (chunks <= 512)
+        f.template operator()<64, Held<T, 64, 8>>();
     else if (chunks <= 1024)
         f.template operator()<256, Held<T, 256, 4>>();
     else if (chunks <= 2048)
@@ -502,13 +530,14 @@ template <typename T, typename F> void with_source(int len, size_t taken, F &&f)
         f.template operator()<1024, Held<T, 1024, 20, 9>>();
 }
 
-// The same for a pass that reads the row once.
-template <typename T, typename F> void with_stream(int len, F &&f)
+// The same for a pass that reads the row once.  Few rows take more threads each
+// (4 rows of 64 KB: 5.1 us with 256 threads a row, 4.2 with 1024).
+template <typename T, typename F> void with_stream(int len, int rows, F &&f)
 {
-    const long chunks = (long)len * (long)sizeof(T) / 16;
-    if (chunks <= 512)
+    const long chunks = (long)len * (long)sizeof(T) / 16 / (rows <= 256 ? 1 : 4);
+    if (chunks <= 128)
         f.template operator()<64, Streamed<T, 64>>();
-    else if (chunks <= 4096)
+    else if (chunks <= 1024)
         f.template operator()<256, Streamed<T, 256>>();
     else
         f.template operator()<1024, Streamed<T, 1024>>();

@@ -226,17 +226,6 @@ struct PolicyMode {
     }
 };
 
-// The row's gradient from its scalars; `zy` is the label's logit.
-template <typename T, typename Src>
-__device__ __forceinline__ void write_gradient(const Src &src, T *out, int label, float zy,
-                                               const RowScalars &k, const Scale &c)
-{
-    const Dense d{k.A, k.M, c.hi};
-    src.dense(out, d);
-    if (src.owner(label) == (int)threadIdx.x)
-        Pack<T>::put(out + label, d.at(zy) + k.add);
-}
-
 // A work-group per row: statistics, scalars and gradient in one launch.
 template <typename T, int NT, typename Src, typename Mode>
 __global__ __launch_bounds__(NT) void row_kernel(LabelArgs a)
@@ -282,7 +271,7 @@ __global__ __launch_bounds__(NT) void row_kernel(LabelArgs a)
     if (k.zero)
         zero_row<T, NT>(out, V, 0, 1);
     else
-        write_gradient<T>(src, out, label, zy, k, a.c);
+        src.dense(out, Dense{k.A, k.M, a.c.hi}, OneTerm{label, k.add});
 }
 
 // Few rows: each over `parts` work-groups.  First launch: partial statistics.
@@ -365,7 +354,7 @@ __global__ __launch_bounds__(kSplit) void join_kernel(LabelArgs a, int run)
         return;
     }
     const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, run);
-    write_gradient<T>(src, out, label, zy, k, a.c);
+    src.dense(out, Dense{k.A, k.M, a.c.hi}, OneTerm{label, k.add});
 }
 
 struct GradArgs {
@@ -381,9 +370,12 @@ struct GradArgs {
 // The gradient of rows whose statistics are known.
 template <typename T> __global__ __launch_bounds__(kSplit) void label_grad_kernel(GradArgs a)
 {
-    const long t = group_index() / a.parts;
+    // last rows first: they are the ones that the statistics' pass read last, and
+    // up to 256 MB of them are still in the last-level cache (8192 x 65536 bf16,
+    // half of them scored: 402 -> 394 us for the two passes)
+    const long t = a.r.T - 1 - group_index() / a.parts;
     const int part = (int)(group_index() % a.parts), V = a.r.V;
-    if (t >= a.r.T)
+    if (t < 0)
         return;
     T *out = (T *)a.r.dlogits + t * a.r.dld;
     const int label = a.labels[t];
@@ -401,14 +393,9 @@ template <typename T> __global__ __launch_bounds__(kSplit) void label_grad_kerne
     }
     const T *row = (const T *)a.r.logits + t * a.r.ld;
     const Streamed<T, kSplit> src(row, V, part, a.parts);
-    const bool mine = src.owner(label) == (int)threadIdx.x;
-    const float zy = mine ? Pack<T>::get(row + label) : 0.f;
     // a label beyond the row has no log-probability: NaN, like its loss
-    const RowScalars k{label < V ? (float)(-add * shrink) : __builtin_nanf(""), M, (float)add, 0};
-    const Dense d{k.A, k.M, a.c.hi};
-    src.dense(out, d);
-    if (mine)
-        Pack<T>::put(out + label, d.at(zy) + k.add);
+    const float A = label < V ? (float)(-add * shrink) : __builtin_nanf("");
+    src.dense(out, Dense{A, M, a.c.hi}, OneTerm{label, (float)add});
 }
 
 // --- per sequence
@@ -561,7 +548,7 @@ template <typename T, typename Mode> void launch_rows(const LabelArgs &a, hipStr
     if constexpr (Mode::kGradient)
         with_source<T>(a.r.V, 0, run);
     else
-        with_stream<T>(a.r.V, run);
+        with_stream<T>(a.r.V, a.r.T, run);
 }
 
 template <typename Mode> hipError_t dispatch_rows(const LabelArgs &a, hipStream_t st)

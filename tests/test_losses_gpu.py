@@ -571,8 +571,10 @@ def test_a_training_step_of_them_together():
     ref, _ = sk.token_logprobs(ref_z, y)
     adv = torch.randn(4, generator=g).cuda()
     loss, kl, logp, d = sk.policy_loss(z, y, off, old, adv, ref=ref, kl=0.05)
-    assert torch.equal(logp[:44], old[:44])          # the same row arithmetic
     want = F.policy(z, y, off, old, adv, ref=ref, kl=0.05)
+    rows = want[2][0][:44], want[2][1][:44]
+    F.check(logp[:44], rows, "logp")
+    F.check(old[:44], rows, "old")
     F.check(loss, want[0], "policy")
     # on the behaviour policy itself every ratio is 1: without the KL term the gradient is that of -A logp / n
     share = torch.zeros(T, device="cuda")
@@ -584,7 +586,7 @@ def test_a_training_step_of_them_together():
         2.0 ** -7 * nokl.float().abs().max()         # two roundings to bf16
     ploss, reward, plogp, pd = sk.preference_loss(z, y, off, ref, beta=0.2)
     F.check(ploss, F.preference(z, y, off, ref, beta=0.2)[0], "preference")
-    assert torch.equal(plogp[:44], old[:44])
+    F.check(plogp[:44], rows, "logp of the pairs")
     top = ref_z.float().topk(8, dim=1)
     tl = torch.logsumexp(ref_z.float(), 1)
     dl, dd = sk.distill_loss(z, top.indices.int(), top.values.contiguous(), teacher_lse=tl)
