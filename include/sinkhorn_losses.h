@@ -77,7 +77,8 @@ enum { SK_PREFERENCE_SIGMOID = 0, SK_PREFERENCE_SQUARE = 1 };
 size_t sinkhorn_losses_workspace_bytes(int op, int T, int V, int k, int dtype);
 
 /*
- * Log-probabilities of tokens: with s = scale (an inverse temperature),
+ * Log-probabilities of tokens: with s = scale (an inverse temperature, from
+ * 1e-20 to 1e20 here and below),
  *     logp[t] = s z_{t,labels[t]} - lse[t],   lse[t] = log sum_v exp(s z_tv).
  * Either output may be NULL (not both).  A row without a distribution has
  * logp 0 and lse -inf.

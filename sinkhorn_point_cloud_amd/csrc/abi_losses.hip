@@ -115,11 +115,11 @@ int check_grad(const void *logits, int64_t ld, const void *dlogits, int64_t dld,
                 "dlogits overlap the logits without being them (same address and row distance)");
 }
 
+// The range in which both pieces of scale log2(e) are ordinary fp32 numbers.
 int check_scale(double scale, const char *what)
 {
-    const double c = scale * kLog2eD;
-    if (!(scale > 0.0) || !(c >= 1e-30) || !(c <= 1e30))
-        return fail(SK_ERR_INVALID_ARG, "%s=%g must be in [1e-30, 1e30]", what, scale);
+    if (!(scale >= 1e-20 && scale <= 1e20))
+        return fail(SK_ERR_INVALID_ARG, "%s=%g must be in [1e-20, 1e20]", what, scale);
     return SK_OK;
 }
 

@@ -92,8 +92,8 @@ SPACE = ALL
         dict(dlogits=ctypes.c_void_p(4096 + 4 * 32), ld=96, dld=96))],   # columns that overlap
     *[(n, c, sk.SK_ERR_WORKSPACE) for n in SPACE for c in (dict(ws=None), dict(ws_bytes=8))],
     *[(n, c, sk.SK_ERR_INVALID_ARG) for n in ALL[:4] for c in (
-        dict(labels=None), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan),
-        dict(scale=math.inf), dict(V=(1 << 24) + 1, ld=1 << 25))],
+        dict(labels=None), dict(scale=0.0), dict(scale=1e-21), dict(scale=1e21), dict(scale=-1.0),
+        dict(scale=math.nan), dict(scale=math.inf), dict(V=(1 << 24) + 1, ld=1 << 25))],
     ("token_logprobs", dict(logp=None, lse=None), sk.SK_ERR_INVALID_ARG),
     ("token_logprobs_backward", dict(grad=None), sk.SK_ERR_INVALID_ARG),
     ("token_logprobs_backward", dict(dlogits=None), sk.SK_ERR_INVALID_ARG),

@@ -18,6 +18,11 @@ SIZES = [(1, 1), (1, 2), (3, 7), (2, 64), (5, 129), (4, 1000), (300, 33), (9, 20
          (1, 262151)]
 
 
+# more rows than are split, as long as registers, registers and LDS, and neither hold (the last
+# multiple of 16 bytes, one value more or less, and beyond)
+SIZES += [(130, 65537), (129, 70001), (130, 125003), (131, 140007)]
+
+
 @pytest.fixture(autouse=True)
 def _say(request):
     print(request.node.name, flush=True)
@@ -218,6 +223,38 @@ def test_balance_loss(T, E, K, G, dt):
     assert again[3] is None and all(torch.equal(x, y) for x, y in zip(got[:3], again[:3]))
 
 
+def test_distill_of_a_long_list_on_a_long_row():
+    # a list that leaves no room for a row in LDS
+    g = rng(21)
+    T, V, K = 129, 80003, 1024
+    z, _ = make(T, V, torch.float32, g)
+    idx = torch.randint(0, V, (T, K), generator=g)
+    idx[:, 700] = idx[:, 3]
+    u = torch.randn(T, K, generator=g)
+    args = (z, idx.int().cuda(), u.cuda())
+    got, want = sk.distill_loss(*args), F.distill(*args)
+    F.check(got[0], want[0], "loss")
+    F.check(got[1], want[1], "dlogits")
+
+
+def test_one_token_many_times():
+    # every entry the same token, and pairs of them on either side of a wave's 64 entries
+    g = rng(22)
+    for V, K in ((300, 200), (9000, 130), (40, 64)):
+        z, _ = make(5, V, torch.float32, g)
+        idx = torch.full((5, K), 7)
+        idx[1] = torch.arange(K) % (K // 2) % V
+        idx[2] = torch.arange(K) // 2 % V
+        idx[3, ::3] = -1
+        u = torch.randn(5, K, generator=g)
+        args = (z, idx.int().cuda(), u.cuda())
+        got, want = sk.distill_loss(*args), F.distill(*args)
+        F.check(got[0], want[0], "loss")
+        F.check(got[1], want[1], "dlogits")
+        for _ in range(3):
+            assert torch.equal(sk.distill_loss(*args)[1], got[1])
+
+
 # ------------------------------------------------------------------ every operator
 
 def _setup(name, T=37, V=900, dt="bf16", seed=5):
@@ -255,7 +292,7 @@ def _setup(name, T=37, V=900, dt="bf16", seed=5):
 
 NAMES = ("logp", "policy", "preference", "distill", "balance")
 SHAPES = [(37, 900, "bf16"), (37, 1001, "f32")]
-LARGE = [(40, 40009, "bf16"), (31, 20001, "f32")]
+LARGE = [(40, 70009, "bf16"), (31, 20001, "f32"), (130, 70001, "f32"), (31, 40001, "f32")]
 
 
 def sizes_for(name):
