@@ -238,7 +238,7 @@ __device__ __forceinline__ void group_rows(const BalanceArgs &a, long first, lon
         s = row16_sum(s);
         dot = row16_sum(dot);
         const bool used = chose && s != 0.f;
-        const float inv = used ? 1.f / s : 0.f, lse = used ? m + (float)rows::ln_of(s) : 0.f;
+        const float inv = used ? 1.f / s : 0.f, lse = used ? m + logf(s) : 0.f;
         dot *= inv;
         if (used && lane == 0) {
             dots += 1.0 + (double)dot;

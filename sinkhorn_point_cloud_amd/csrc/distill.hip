@@ -35,20 +35,21 @@ struct Args {
 // The list of a row in shared memory: entry k's token, probability and the
 // student's logit there, and the entries of each owner thread as a linked list.
 struct List {
-    int *head;   // [NT] first entry whose element the thread owns, or -1
-    int *mark;   // [NT] bit i: an entry lies in the thread's i-th chunk (modulo 32)
-    int *next;   // [K]
-    int *token;  // [K]
-    float *p;    // [K]
-    float *take; // [K] what the gradient takes away for entry k, see link()
-    float *z;    // [K]
-    __device__ __forceinline__ List(int *room, int NT, int K)
-        : head(room), mark(room + NT), next(mark + NT), token(next + K), p((float *)(token + K)),
-          take(p + K), z(take + K)
+    double *p;    // [K]
+    int *head;    // [NT] first entry whose element the thread owns, or -1
+    int *mark;    // [NT] bit i: an entry lies in the thread's i-th chunk (modulo 32)
+    int *next;    // [K]
+    int *token;   // [K]
+    float *u;     // [K] the teacher's logit
+    float *own;   // [K] the gradient at entry k's token
+    float *z;     // [K]
+    __device__ __forceinline__ List(void *room, int NT, int K)
+        : p((double *)room), head((int *)(p + K)), mark(head + NT), next(mark + NT),
+          token(next + K), u((float *)(token + K)), own(u + K), z(own + K)
     {
     }
 };
-size_t list_bytes(int NT, int K) { return (size_t)(2 * NT + 5 * K) * 4; }
+size_t list_bytes(int NT, int K) { return (size_t)(2 * NT + 7 * K) * 4; }
 
 struct Teacher {
     double C, U;   // sum of p, log-sum-exp
@@ -61,6 +62,7 @@ struct Ahead {
     static constexpr int n = 4;   // 256 entries
     int v[n];
     float u[n];
+    // one wave
     __device__ __forceinline__ void load(const Args &a, long t)
     {
         const int K = a.d.K;
@@ -75,32 +77,44 @@ struct Ahead {
             }
         }
     }
-    // f(k, token, logit) for every entry of this lane
-    template <typename F> __device__ __forceinline__ void each(const Args &a, long t, F &&f) const
+    // the whole list into shared memory; z(k, token): the student's logit there
+    template <typename Z>
+    __device__ __forceinline__ void list(const Args &a, long t, const List &l, Z &&z) const
     {
         const int K = a.d.K;
+        auto put = [&](int k, int token, float logit) {
+            l.token[k] = token;
+            l.u[k] = logit;
+            l.z[k] = z(k, token);
+        };
 #pragma unroll
         for (int j = 0; j < n; ++j) {
             const int k = lane_id() + j * kWave;
             if (j * kWave < K && k < K)   // the first the same for the wave: a branch
-                f(k, v[j], u[j]);
+                put(k, v[j], u[j]);
         }
         for (int k = lane_id() + n * kWave; k < K; k += kWave)
-            f(k, a.d.index[t * K + k], a.d.teacher[t * K + k]);
+            put(k, a.d.index[t * K + k], a.d.teacher[t * K + k]);
     }
 };
 
-// One wave: the teacher's probabilities into the list, as fp32 exponentials of
-// the differences to the largest logit, or to the given log-sum-exp (fp64: the
-// two may be far from 0 and near each other).
-__device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const Ahead &in,
-                                                const List &l)
+// f(k, token, logit) for every entry of this lane
+template <typename F> __device__ __forceinline__ void each(const List &l, int K, F &&f)
 {
-    const int V = a.r.V;
+    for (int k = lane_id(); k < K; k += kWave)
+        f(k, l.token[k], l.u[k]);
+}
+
+// One wave: the teacher's probabilities into the list, in fp64 from fp32
+// exponentials e_k of the differences to the largest logit: e_k / (1 + rest), the
+// rest without one maximum, so that a probability near 1 is as near to it as it
+// should be.  Against a given log-sum-exp they are 1 + expm1.
+__device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const List &l)
+{
+    const int V = a.r.V, K = a.d.K;
     float top = -kInf;
     int bad = 0;
-    in.each(a, t, [&](int k, int v, float u) {
-        l.token[k] = v;
+    each(l, K, [&](int, int v, float u) {
         if (v >= 0) {
             bad |= v >= V || u != u;
             top = fmaxf(top, u);
@@ -110,110 +124,107 @@ __device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const Ahe
     Teacher r;
     r.bad = __any(bad);
     r.any = top != -kInf;
-    float C = 0.f;
     if (a.d.teacher_lse) {
-        const double c = a.r.scale * kLog2eD;   // log2(e) / tau
         r.U = (double)a.d.teacher_lse[t];
-        const double less = r.U * kLog2eD;
-        in.each(a, t, [&](int k, int v, float u) {
-            const float p = r.any && v >= 0 ? ex2((float)((double)u * c - less)) : 0.f;
+        double C = 0.0;
+        each(l, K, [&](int k, int v, float u) {
+            const float g = (float)((double)u * a.r.scale - r.U);
+            const double p = !r.any || v < 0   ? 0.0
+                             : fabsf(g) < 1.f ? 1.0 + (double)expm1_of(g)
+                                              : (double)ex2(g * kLog2e);
             l.p[k] = p;
             C += p;
         });
+        r.C = sum_wave(C);
     } else {
-        float s = 0.f;
-        in.each(a, t, [&](int k, int v, float u) {
+        float rest = 0.f;
+        int tops = 0;
+        each(l, K, [&](int k, int v, float u) {
             const float e = r.any && v >= 0 ? a.c.pow(u - top) : 0.f;
-            l.p[k] = e;
-            s += e;
+            l.p[k] = (double)e;
+            if (r.any && v >= 0 && u == top)
+                ++tops;
+            else
+                rest += e;
         });
-        s = sum_wave(s);
-        r.U = (double)top * a.r.scale + ln_of(s);
-        const float over = 1.f / s;
-        in.each(a, t, [&](int k, int, float) {
-            const float p = r.any ? l.p[k] * over : 0.f;
-            l.p[k] = p;
-            C += p;
-        });
+        rest = sum_wave(rest) + (float)(wave_sum(tops) - 1);
+        r.U = (double)top * a.r.scale + ln_sum(rest);
+        const double over = r.any ? 1.0 / (1.0 + (double)rest) : 0.0;
+        each(l, K, [&](int k, int, float) { l.p[k] *= over; });
+        r.C = r.any ? 1.0 : 0.0;
     }
-    r.C = (double)sum_wave(C);
     return r;
 }
 
 struct RowScalars {
-    float A, M, sub;   // out_v = A 2^((z_v - M) c) - sub sum_{k: i_k = v} p_k
+    float A, M;   // out_v = A 2^((z_v - M) c) for tokens that are not in the list
     int zero;
 };
 
-// One wave, once the row's (M, S) and the list are there: loss and coefficients.
-__device__ __forceinline__ RowScalars student_side(const Args &a, long t, const Ahead &in,
-                                                   const List &l, const Teacher &r, float M,
-                                                   float S, bool writes)
-{
-    const int lane = lane_id();
-    const double inv = a.r.scale, tau = 1.0 / inv;
-    const double w = a.d.weights ? (double)a.d.weights[t] : 1.0;
-    // log p_k - log q_k = (u_k - (z_k - M)) / tau - (U - ln S): fp64, for it is
-    // small where the two agree
-    const double apart = r.U - ln_of(S);
-    double sum = 0.0;
-    in.each(a, t, [&](int k, int, float u) {
-        const double p = (double)l.p[k];
-        if (p != 0.0)
-            sum += p * (((double)u - ((double)l.z[k] - (double)M)) * inv - apart);
-    });
-    sum = sum_wave(sum);
-    const bool none = S == 0.f || (!r.any && !r.bad);
-    const double nan = __builtin_nan("");
-    if (writes && lane == 0)
-        a.d.loss[t] = none ? 0.f : (float)(r.bad ? nan : w * tau * tau * sum);
-    const double add = w * tau;
-    return RowScalars{(float)(r.bad ? nan : add * r.C / (double)S), M, (float)add, none};
-}
-
-// One wave: hands the entries to the threads that own their elements.  Of a
-// token's several entries the first takes away all of it, summed in list order,
-// whatever order the linked list has.
-template <int NT, typename Src>
-__device__ __forceinline__ void link(const List &l, const Src &src, int K)
+// One wave: hands the entries to the threads that own their elements.  Returns
+// whether a token stands in the list more than once.
+template <typename Src>
+__device__ __forceinline__ bool link(const List &l, const Src &src, int K)
 {
     bool twice = false;
     for (int k = lane_id(); k < K; k += kWave) {
         const int v = l.token[k];
         const int who = src.owner(v);
-        l.take[k] = l.p[k];
         if (who >= 0) {
             const int before = atomicExch(&l.head[who], k);
             l.next[k] = before;
             atomicOr(&l.mark[who], 1 << (src.turn(v) & 31));
-            // every pair of a list's entries is met once
+            // every pair of a linked list's entries is met once
             for (int j = before; j >= 0; j = l.next[j])
                 twice |= l.token[j] == v;
         }
     }
-    if (__any(twice))
-        for (int k = lane_id(); k < K; k += kWave) {
-            const int v = l.token[k];
-            float sum = 0.f;
-            bool first = true;
-            for (int j = 0; j < K; ++j)
-                if (l.token[j] == v) {
-                    first &= j >= k;
-                    sum += l.p[j];
-                }
-            l.take[k] = first ? sum : 0.f;
-        }
+    return __any(twice);
 }
 
-// The entries that this thread owns, as terms of its gradient values.
+// One wave, once the row's (M, R) and the list are there: loss, coefficients and
+// the gradient at the list's tokens, add (C q - p).
+__device__ __forceinline__ RowScalars student_side(const Args &a, long t, const List &l,
+                                                   const Teacher &r, bool twice,
+                                                   float M, float R, bool writes)
+{
+    const int lane = lane_id(), K = a.d.K;
+    const double inv = a.r.scale, tau = 1.0 / inv;
+    const double w = a.d.weights ? (double)a.d.weights[t] : 1.0;
+    const double nan = __builtin_nan("");
+    const double add = w * tau, over = r.bad ? nan : r.C / row_sum(M, R);
+    // log p_k - log q_k = (u_k - (z_k - M)) / tau - (U - ln(1 + R)): fp64, for it
+    // is small where the two agree
+    const double apart = r.U - ln_sum(R);
+    double sum = 0.0;
+    each(l, K, [&](int k, int, float u) {
+        const double p = l.p[k];
+        if (p != 0.0)
+            sum += p * (((double)u - ((double)l.z[k] - (double)M)) * inv - apart);
+        double P = p;
+        if (twice) {
+            // all of the token's entries, in list order: the same for each of them
+            P = 0.0;
+            for (int j = 0; j < K; ++j)
+                P += l.token[j] == l.token[k] ? l.p[j] : 0.0;
+        }
+        l.own[k] = (float)(add * (over * (double)a.c.pow(l.z[k] - M) - P));
+    });
+    sum = sum_wave(sum);
+    const bool none = row_empty(M, R) || (!r.any && !r.bad);
+    if (writes && lane == 0)
+        a.d.loss[t] = none ? 0.f : (float)(r.bad ? nan : w * tau * tau * sum);
+    return RowScalars{(float)(add * over), M, none};
+}
+
+// The entries that this thread owns, as values of its gradient.
 struct ListTerms {
     const List &l;
     int first;    // the thread's first entry
     int mark;
-    float sub;    // -sub take_k at token k
 
-    __device__ __forceinline__ ListTerms(const List &list, float sub)
-        : l(list), first(list.head[threadIdx.x]), mark(list.mark[threadIdx.x]), sub(sub)
+    __device__ __forceinline__ explicit ListTerms(const List &list)
+        : l(list), first(list.head[threadIdx.x]), mark(list.mark[threadIdx.x])
     {
     }
     template <int n> __device__ __forceinline__ void chunk(int i, int at, float (&x)[n]) const
@@ -221,18 +232,17 @@ struct ListTerms {
         if (mark >> (i & 31) & 1)
             for (int k = first; k >= 0; k = l.next[k]) {
                 const int off = l.token[k] - at;
-                const float s = sub * l.take[k];
+                const float own = l.own[k];
 #pragma unroll
                 for (int j = 0; j < n; ++j)
-                    x[j] -= j == off ? s : 0.f;
+                    x[j] = j == off ? own : x[j];
             }
     }
-    __device__ __forceinline__ float edge(int v) const
+    __device__ __forceinline__ float edge(int v, float y) const
     {
-        float s = 0.f;
         for (int k = first; k >= 0; k = l.next[k])
-            s -= l.token[k] == v ? sub * l.take[k] : 0.f;
-        return s;
+            y = l.token[k] == v ? l.own[k] : y;
+        return y;
     }
 };
 
@@ -242,7 +252,7 @@ __device__ __forceinline__ bool dropped(const Args &a, long t)
 }
 
 template <typename T, int NT, typename Src>
-__global__ __launch_bounds__(NT) void distill_kernel(Args a)
+__global__ __launch_bounds__(NT, Src::waves) void distill_kernel(Args a)
 {
     extern __shared__ u32x4 chunks[];   // [Src::lds_chunks], then the list
     __shared__ float2 room[NT / kWave];
@@ -250,7 +260,6 @@ __global__ __launch_bounds__(NT) void distill_kernel(Args a)
     const long t = group_index();
     if (t >= a.r.T)
         return;
-    int *dyn = (int *)(chunks + Src::lds_chunks);
     const int V = a.r.V, K = a.d.K;
     T *out = (T *)a.r.dlogits + t * a.r.dld;
     const bool grad = a.r.dlogits;
@@ -261,30 +270,31 @@ __global__ __launch_bounds__(NT) void distill_kernel(Args a)
             zero_row<T, NT>(out, V, 0, 1);
         return;
     }
-    const List l(dyn, NT, K);
+    const List l(chunks + Src::lds_chunks, NT, K);
     l.head[threadIdx.x] = -1;
     l.mark[threadIdx.x] = 0;
     __syncthreads();
     const T *row = (const T *)a.r.logits + t * a.r.ld;
     Src src(row, V, 0, 1, chunks);
     Teacher r{};
+    bool twice = false;
     Ahead ahead;
     if (threadIdx.x < kWave)
         ahead.load(a, t);
     src.load();
     if (threadIdx.x < kWave) {
-        ahead.each(a, t, [&](int k, int v, float) {
-            l.z[k] = v >= 0 && v < V ? Pack<T>::get(row + v) : 0.f;
+        ahead.list(a, t, l, [&](int, int v) {
+            return v >= 0 && v < V ? Pack<T>::get(row + v) : 0.f;
         });
-        r = teacher_side(a, t, ahead, l);
+        r = teacher_side(a, t, l);
         if (grad)
-            link<NT>(l, src, K);
+            twice = link(l, src, K);
     }
-    float M = -kInf, S = 0.f;
-    src.stats(a.c, M, S);
-    merge_group<NT>(M, S, a.c, room);
+    float M = -kInf, R = 0.f;
+    src.stats(a.c, M, R);
+    merge_group<NT>(M, R, a.c, room);
     if (threadIdx.x < kWave) {
-        const RowScalars k = student_side(a, t, ahead, l, r, M, S, true);
+        const RowScalars k = student_side(a, t, l, r, twice, M, R, true);
         if (threadIdx.x == 0)
             scal = k;
     }
@@ -296,7 +306,7 @@ __global__ __launch_bounds__(NT) void distill_kernel(Args a)
         zero_row<T, NT>(out, V, 0, 1);
         return;
     }
-    src.dense(out, Dense{k.A, k.M, a.c.hi}, ListTerms(l, k.sub));
+    src.dense(out, Dense{k.A, k.M, a.c.hi}, ListTerms(l));
 }
 
 // Few rows: partial statistics, and the student's logits at the list's tokens
@@ -324,7 +334,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_part_ker
 
 template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_kernel(Args a, int run)
 {
-    extern __shared__ int dyn[];
+    extern __shared__ u32x4 chunks[];   // the list
     __shared__ RowScalars scal;
     const long t = group_index() / run;
     const int part = (int)(group_index() % run), V = a.r.V, K = a.d.K;
@@ -339,7 +349,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
             zero_row<T, kSplit>(out, V, part, run);
         return;
     }
-    const List l(dyn, kSplit, K);
+    const List l(chunks, kSplit, K);
     l.head[threadIdx.x] = -1;
     l.mark[threadIdx.x] = 0;
     __syncthreads();
@@ -347,20 +357,14 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
     if (threadIdx.x < kWave) {
         Ahead ahead;
         ahead.load(a, t);
-        const Teacher r = teacher_side(a, t, ahead, l);
-        for (int k = lane_id(); k < K; k += kWave)
-            l.z[k] = a.d.zk[t * K + k];
-        if (grad)
-            link<kSplit>(l, src, K);
-        float M = -kInf, S = 0.f;
-        const float2 *p = a.w.part + t * a.parts;
-        for (int i = lane_id(); i < a.parts; i += kWave) {
-            const float mn = fmaxf(M, p[i].x), at = shift_of(mn);
-            S = S * a.c.pow(M - at) + p[i].y * a.c.pow(p[i].x - at);
-            M = mn;
-        }
-        merge_wave(M, S, a.c);
-        const RowScalars k = student_side(a, t, ahead, l, r, M, S, part == 0);
+        ahead.list(a, t, l, [&](int k, int) { return a.d.zk[t * K + k]; });
+        const Teacher r = teacher_side(a, t, l);
+        const bool twice = grad && link(l, src, K);
+        const float2 p = lane_id() < a.parts ? a.w.part[t * a.parts + lane_id()]
+                                             : make_float2(-kInf, 0.f);
+        float M = p.x, R = p.y;
+        merge_wave(M, R, a.c);
+        const RowScalars k = student_side(a, t, l, r, twice, M, R, part == 0);
         if (threadIdx.x == 0)
             scal = k;
     }
@@ -372,7 +376,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
         zero_row<T, kSplit>(out, V, part, run);
         return;
     }
-    src.dense(out, Dense{k.A, k.M, a.c.hi}, ListTerms(l, k.sub));
+    src.dense(out, Dense{k.A, k.M, a.c.hi}, ListTerms(l));
 }
 
 template <typename T> struct RunRows {

@@ -7,15 +7,18 @@
 // worth of values before the first and behind the last of them, the edge; the
 // edge values are dealt one to a thread.  Chunk c0 + i * threads + t belongs to
 // thread t, so that a wave's loads are 1 KB in a run and the thread that owns
-// an element is known from its index alone: that thread adds an element's sparse
-// term to the chunk before it stores it.  (Written again behind the dense store,
+// an element is known from its index alone: that thread puts an element's own
+// value into the chunk before it stores it.  (Written again behind the dense store,
 // each such element is a 2- or 4-byte write to a line on its way to memory: 16384
 // rows of 32000 bf16 values with 64 terms took 398 us that way, 367 this way.)
 //
 // The exponentials are taken in base 2: with c = scale log2(e) and the row
 // maximum M, e_v = 2^((x_v - M) c).  The difference is formed first, so a row
-// of the type's lowest finite values is an ordinary row.  Values of -inf take
-// no part; a row of nothing else has the sum 0.  NaN and +inf give a NaN sum.
+// of the type's lowest finite values is an ordinary row.  What is summed is the
+// rest R = sum_v e_v - 1, every term but one that is 1: where one value has
+// nearly all of the probability, ln(1 + R) and 1 - q keep their relative
+// precision.  Values of -inf take no part; a row of nothing else has M = -inf
+// and R = 0.  NaN gives a NaN rest.
 #pragma once
 
 #include "common.h"
@@ -194,14 +197,6 @@ __device__ __forceinline__ double sum_wave(double v)
     return (read_lane(v, 0) + read_lane(v, 16)) + (read_lane(v, 32) + read_lane(v, 48));
 }
 
-// ln of a positive sum in fp64, off by about 2^-24: the exponent is exact, the
-// logarithm of the mantissa is the hardware's, between -1 and 0.
-__device__ __forceinline__ double ln_of(float s)
-{
-    const int e = __builtin_amdgcn_frexp_expf(s);
-    return ((double)e + (double)lg2(__builtin_amdgcn_frexp_mantf(s))) * kLn2D;
-}
-
 // c = scale log2(e) in two pieces.  With one, every exponent of a row's sum would
 // be off by the same relative 2^-25: an error of one sign, about 1e-7 in each
 // log-probability, which adds up over a sequence.  hi lies below c, so that lo is
@@ -219,74 +214,151 @@ inline Scale scale_of_row(double scale)
     return Scale{hi, (float)(c - (double)hi)};
 }
 
-// Running maximum and sum of exponentials.  The shift of an empty state is 0,
-// so that no difference of two infinities is formed.
+// Running maximum and rest.  The shift of an empty state is 0, so that no
+// difference of two infinities is formed.
 __device__ __forceinline__ float shift_of(float m) { return m == -kInf ? 0.f : m; }
 
-template <int K>
-__device__ __forceinline__ void absorb(const float (&x)[K], const Scale &k, float &m, float &s)
+// Minimum and maximum that keep a NaN.
+__device__ __forceinline__ float min_of(float a, float b)
 {
-    float top = x[0];
+    return __builtin_elementwise_minimum(a, b);
+}
+__device__ __forceinline__ float max_of(float a, float b)
+{
+    return __builtin_elementwise_maximum(a, b);
+}
+
+// Takes K values into (m, r).  A chain of exchanges leaves the largest in `top`
+// and all the others, each once, in `low`.
+template <int K>
+__device__ __forceinline__ void absorb(const float (&x)[K], const Scale &k, float &m, float &r)
+{
+    float low[K], top = x[0];
+#pragma unroll
+    for (int i = 1; i < K; ++i) {
+        low[i] = min_of(top, x[i]);
+        top = max_of(top, x[i]);
+    }
+    const float mn = max_of(m, top), at = shift_of(mn);
+    const float f = k.pow(min_of(m, top) - at);   // the smaller of the two maxima
+    float sum = f;
 #pragma unroll
     for (int i = 1; i < K; ++i)
-        top = fmaxf(top, x[i]);
-    const float mn = fmaxf(m, top), at = shift_of(mn);
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < K; ++i)
-        sum += k.pow(x[i] - at);
-    s = fmaf(s, k.pow(m - at), sum);
+        sum += k.pow(low[i] - at);
+    r = fmaf(r, top > m ? f : 1.f, sum);
     m = mn;
 }
 
-__device__ __forceinline__ void merge_wave(float &m, float &s, const Scale &c)
+// (M, R) of a wave, the same in all its lanes.
+__device__ __forceinline__ void merge_wave(float &m, float &r, const Scale &c)
 {
     const float top = max_wave(m), at = shift_of(top);
-    s = sum_wave(s * c.pow(m - at));
+    const float f = c.pow(m - at);
+    // the first lane that has the maximum leaves its 1 out, every other counts
+    const bool holds = __ffsll(__ballot(m == top)) - 1 == lane_id();
+    r = sum_wave(holds ? r : fmaf(r, f, f));
     m = top;
 }
 
-// (M, S) of the whole work-group in every thread.  `room`: one entry per wave.
+// (M, R) of the whole work-group in every thread.  `room`: one entry per wave.
 // One barrier; `room` may be written again only behind another one.
 template <int NT>
-__device__ __forceinline__ void merge_group(float &m, float &s, const Scale &c, float2 *room)
+__device__ __forceinline__ void merge_group(float &m, float &r, const Scale &c, float2 *room)
 {
-    merge_wave(m, s, c);
+    merge_wave(m, r, c);
     if constexpr (NT > kWave) {
         constexpr int waves = NT / kWave;
         if (lane_id() == 0)
-            room[threadIdx.x / kWave] = make_float2(m, s);
+            room[threadIdx.x / kWave] = make_float2(m, r);
         __syncthreads();
-        const float2 r = lane_id() < waves ? room[lane_id()] : make_float2(-kInf, 0.f);
-        m = r.x;
-        s = r.y;
-        merge_wave(m, s, c);
+        const float2 v = lane_id() < waves ? room[lane_id()] : make_float2(-kInf, 0.f);
+        m = v.x;
+        r = v.y;
+        merge_wave(m, r, c);
     }
 }
 
-// coefficient x exponential of one row: out_v = A 2^((x_v - M) c) plus sparse
-// terms.  Those are a `Terms` with
-//     chunk(i, first, x): adds to a thread's i-th chunk, whose first element is `first`,
-//     edge(v):            what to add to element v of the edge.
+// A row without any probability, and the sum 1 + R in fp64: NaN for a maximum of
+// +inf, whose terms would be differences of infinities.
+__device__ __forceinline__ bool row_empty(float M, float R) { return M == -kInf && R == 0.f; }
+__device__ __forceinline__ double row_sum(float M, float R)
+{
+    return M == kInf ? __builtin_nan("") : 1.0 + (double)R;
+}
+
+// ln(1 + R) to fp64 precision: 2 artanh(t), t = R / (2 + R), or for larger R the
+// same for the sum's mantissa m between sqrt(1/2) and sqrt(2), t = (m - 1) /
+// (m + 1).  |t| <= 0.172: the first term left out, t^17/17, is below 2^-47 t.
+// (The library's logarithm, with its tables of extra precision, took several
+// times as long while the row's other waves waited.)
+__device__ __forceinline__ double ln_sum(float R)
+{
+    double e = 0.0, a = (double)R, b = 2.0 + a;
+    if (R >= 0.4140625f) {
+        const double s = 1.0 + a;
+        double m = __builtin_amdgcn_frexp_mant(s);
+        int k = __builtin_amdgcn_frexp_exp(s);
+        if (m < 0.7071067811865476) {
+            m *= 2.0;
+            --k;
+        }
+        e = (double)k;
+        a = m - 1.0;
+        b = m + 1.0;
+    }
+    const double t = a / b, q = t * t;
+    double p = 1.0 / 15;
+    p = fma(p, q, 1.0 / 13);
+    p = fma(p, q, 1.0 / 11);
+    p = fma(p, q, 1.0 / 9);
+    p = fma(p, q, 1.0 / 7);
+    p = fma(p, q, 1.0 / 5);
+    p = fma(p, q, 1.0 / 3);
+    return fma(e, kLn2D, 2.0 * fma(p * q, t, t));
+}
+
+// e^g - 1 to fp32 precision, relative also near 0 (|g| < 1: the first term left
+// out, g^12/12!, is below 2^-27 of the value)
+__device__ __forceinline__ float expm1_of(float g)
+{
+    if (!(fabsf(g) < 1.f))
+        return ex2(g * kLog2e) - 1.f;
+    float r = 1.f / 39916800.f;
+    r = fmaf(r, g, 1.f / 3628800.f);
+    r = fmaf(r, g, 1.f / 362880.f);
+    r = fmaf(r, g, 1.f / 40320.f);
+    r = fmaf(r, g, 1.f / 5040.f);
+    r = fmaf(r, g, 1.f / 720.f);
+    r = fmaf(r, g, 1.f / 120.f);
+    r = fmaf(r, g, 1.f / 24.f);
+    r = fmaf(r, g, 1.f / 6.f);
+    r = fmaf(r, g, 0.5f);
+    return fmaf(r * g, g, g);
+}
+
+// coefficient x exponential of one row, out_v = A 2^((x_v - M) c), but for the
+// elements that have a value of their own.  Those are a `Terms` with
+//     chunk(i, first, x): sets them in a thread's i-th chunk, whose first element is `first`,
+//     edge(v, y):         the value of element v of the edge, y if it has none.
 struct Dense {
     float A, M, c;
     __device__ __forceinline__ float at(float x) const { return A * ex2((x - M) * c); }
 };
 
-// One term: `add` at element v.
+// One element.
 struct OneTerm {
     int v;
-    float add;
+    float value;
     template <int n> __device__ __forceinline__ void chunk(int, int first, float (&x)[n]) const
     {
         const int at = v - first;
         if (at >= 0 && at < n) {
 #pragma unroll
             for (int k = 0; k < n; ++k)
-                x[k] += k == at ? add : 0.f;
+                x[k] = k == at ? value : x[k];
         }
     }
-    __device__ __forceinline__ float edge(int u) const { return u == v ? add : 0.f; }
+    __device__ __forceinline__ float edge(int u, float y) const { return u == v ? value : y; }
 };
 
 template <typename T>
@@ -306,7 +378,7 @@ __device__ __forceinline__ void store_chunk(T *out, const float (&y)[Pack<T>::n]
 template <typename T, int NT> struct Streamed : Slice<T, NT> {
     using S = Slice<T, NT>;
     static constexpr int n = S::n;
-    static constexpr int lds_chunks = 0;
+    static constexpr int lds_chunks = 0, waves = 8;
     static constexpr int kUnroll = 4;
     __device__ __forceinline__ Streamed(const T *p, int len, int part, int parts,
                                         u32x4 * = nullptr)
@@ -350,7 +422,7 @@ template <typename T, int NT> struct Streamed : Slice<T, NT> {
         const bool aligned = (((uintptr_t)(out + S::cut.head)) & 15) == 0;
         if (S::has_edge(t)) {
             const int v = S::edge_at(t);
-            Pack<T>::put(out + v, d.at(Pack<T>::get(S::row + v)) + terms.edge(v));
+            Pack<T>::put(out + v, terms.edge(v, d.at(Pack<T>::get(S::row + v))));
         }
         auto put = [&](int i, u32x4 v) {
             float x[n];
@@ -394,6 +466,9 @@ template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
     using S = Slice<T, NT>;
     static constexpr int n = S::n;
     static constexpr int lds_chunks = L * NT;
+    // waves per SIMD: with up to 8 chunks a thread all of a compute unit's 2048
+    // threads fit (64 registers each), so that rows overlap
+    static constexpr int waves = N <= 8 ? 8 : 4;
     static constexpr int kUnroll = 2;   // registers are taken
     u32x4 v[N];
     float e;
@@ -483,7 +558,7 @@ template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
         const bool aligned = (((uintptr_t)(out + S::cut.head)) & 15) == 0;
         if (S::has_edge(t)) {
             const int u = S::edge_at(t);
-            Pack<T>::put(out + u, d.at(e) + terms.edge(u));
+            Pack<T>::put(out + u, terms.edge(u, d.at(e)));
         }
         each<false>([&](int i, int at, float (&x)[n]) {
             if (at < S::c1) {

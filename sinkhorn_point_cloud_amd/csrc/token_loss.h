@@ -30,14 +30,14 @@ int token_parts(int T, int V, int dtype);
 int grad_parts(int T, int V, int dtype);
 
 struct TokenWs {
-    float2 *part;   // [T][parts] partial (maximum, sum); parts > 1 only
+    float2 *part;   // [T][parts] partial (maximum, rest); parts > 1 only
     float *zlab;    // [T] label's logit; parts > 1 only
 };
 
-// What a row's statistics leave for a later pass: its maximum, sum and the
-// label's log-probability before it is rounded.
+// What a row's statistics leave for a later pass: its maximum, the rest of its
+// sum and the label's log-probability before it is rounded.
 struct RowStat {
-    float M, S;
+    float M, R;
     double logp;
 };
 

@@ -1,10 +1,11 @@
 // token_loss.hip -- log-probabilities of tokens and the losses on them: one
 // log-sum-exp per row of logits and the gradient coefficient x (1[label] - softmax).
 //
-// With q = softmax(s z) of a row, y its label and M, S the row maximum and the
-// sum of 2^((z_v - M) c), c = s log2(e):
-//     logp = s (z_y - M) - ln S,        lse = s M + ln S,
-//     d logp / d z_v = s (1[v = y] - q_v),   q_v = 2^((z_v - M) c) / S.
+// With q = softmax(s z) of a row, y its label, M the row maximum and R the sum
+// of e_v = 2^((z_v - M) c), c = s log2(e), but for one maximum:
+//     logp = s (z_y - M) - ln(1 + R),        lse = s M + ln(1 + R),
+//     d logp / d z_v = -s q_v = -s e_v / (1 + R)  for v other than y,
+//                      -s expm1(logp)             for y.
 // Sums and maxima are fp32 over non-negative terms.  The log-probability is put
 // together in fp64 (off by about 1e-7) and so are its differences to given ones:
 // a ratio is clipped by the same decision as in 64 bits unless it is that near
@@ -25,7 +26,7 @@ constexpr int kSplit = 256;   // threads of a work-group that shares its row wit
 
 // What the scalar phase of a row leaves for its gradient pass.
 struct RowScalars {
-    float A, M, add;   // out_v = A 2^((z_v - M) c) + add [v = label]
+    float A, M, own;   // out_v = A 2^((z_v - M) c), `own` for the label
     int zero;          // the row's gradient is zero
 };
 
@@ -75,6 +76,20 @@ __device__ __forceinline__ RowState row_state(const LabelArgs &a, long t, int la
 
 // --- the scalar phase: fp64, one wave, the same in every lane
 
+__device__ __forceinline__ double row_ln(float M, float R)
+{
+    return M == kInf ? __builtin_nan("") : ln_sum(R);
+}
+
+// add (1[v = label] - q_v).  A NaN log-probability (a label beyond the row)
+// makes the whole row NaN.
+__device__ __forceinline__ RowScalars coefficients(double add, double logp, float M, float R)
+{
+    const float own = (float)-add * expm1_of((float)logp);
+    const float A = logp == logp ? (float)(-add / row_sum(M, R)) : __builtin_nanf("");
+    return RowScalars{A, M, own, row_empty(M, R)};
+}
+
 struct LogpMode {
     static constexpr bool kGradient = false;
     struct Row {};
@@ -84,17 +99,17 @@ struct LogpMode {
         return Row{};
     }
     __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &,
-                                                     float M, float S, float zy, bool writes)
+                                                     float M, float R, float zy, bool writes)
     {
-        const double lnS = ln_of(S), s = a.r.scale;
-        const bool none = S == 0.f;
+        const double lnS = row_ln(M, R), s = a.r.scale;
+        const bool none = row_empty(M, R);
         if (writes && lane_id() == 0) {
             if (a.out.logp)
                 a.out.logp[t] = none ? 0.f : (float)(((double)zy - (double)M) * s - lnS);
             if (a.out.lse)
                 a.out.lse[t] = none ? -kInf : (float)((double)M * s + lnS);
             if (a.out.stat)
-                a.out.stat[t] = RowStat{M, S, none ? 0.0 : ((double)zy - (double)M) * s - lnS};
+                a.out.stat[t] = RowStat{M, R, none ? 0.0 : ((double)zy - (double)M) * s - lnS};
         }
         return RowScalars{0.f, 0.f, 0.f, 1};
     }
@@ -105,7 +120,7 @@ struct LogpMode {
         if (a.out.lse)
             a.out.lse[t] = 0.f;
         if (a.out.stat)
-            a.out.stat[t] = RowStat{0.f, 0.f, 0.0};
+            a.out.stat[t] = RowStat{-kInf, 0.f, 0.0};
     }
 };
 
@@ -119,13 +134,10 @@ struct BackwardMode {
         return Row{};
     }
     __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &,
-                                                     float M, float S, float zy, bool)
+                                                     float M, float R, float zy, bool)
     {
-        const double add = (double)a.G[t] * a.r.scale;
-        const bool none = S == 0.f;
-        // a label beyond the row has no log-probability: NaN, like its loss
-        const float A = zy == zy ? (float)(-add / (double)S) : __builtin_nanf("");
-        return RowScalars{A, M, (float)add, none};
+        const double logp = ((double)zy - (double)M) * a.r.scale - row_ln(M, R);
+        return coefficients((double)a.G[t] * a.r.scale, logp, M, R);
     }
     __device__ __forceinline__ static void unused(const LabelArgs &, long) {}
 };
@@ -187,13 +199,13 @@ struct PolicyMode {
         return Row{(float)w, q.adv[q.adv_per_token ? t : i]};
     }
     __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &info,
-                                                     float M, float S, float zy, bool writes)
+                                                     float M, float R, float zy, bool writes)
     {
         const PolicyArgs &q = a.pol;
-        const bool none = S == 0.f;
+        const bool none = row_empty(M, R);
         const double s = a.r.scale, w = (double)info.w;
         const float adv = info.adv;
-        const double logp = ((double)zy - (double)M) * s - ln_of(S);
+        const double logp = ((double)zy - (double)M) * s - row_ln(M, R);
         // the clipping decision is taken on the log-ratio, in fp64
         const double change = logp - (double)q.old[t];
         const float ratio = ex2((float)(change * kLog2eD));
@@ -215,8 +227,7 @@ struct PolicyMode {
                              : make_float2((float)(w * (q.kl * kl - gain)),
                                            (float)(w * kl));
         }
-        const double add = slope * w * s;
-        return RowScalars{(float)(-add / (double)S), M, (float)add, none};
+        return coefficients(slope * w * s, logp, M, R);
     }
     __device__ __forceinline__ static void unused(const LabelArgs &a, long t)
     {
@@ -228,7 +239,7 @@ struct PolicyMode {
 
 // A work-group per row: statistics, scalars and gradient in one launch.
 template <typename T, int NT, typename Src, typename Mode>
-__global__ __launch_bounds__(NT) void row_kernel(LabelArgs a)
+__global__ __launch_bounds__(NT, Src::waves) void row_kernel(LabelArgs a)
 {
     extern __shared__ u32x4 chunks[];   // [Src::lds_chunks]
     __shared__ float2 room[NT / kWave];
@@ -256,11 +267,11 @@ __global__ __launch_bounds__(NT) void row_kernel(LabelArgs a)
     const float zy = label < V ? Pack<T>::get(row + label) : __builtin_nanf("");
     src.load();
     const typename Mode::Row info = Mode::template begin<NT>(a, t, count);
-    float M = -kInf, S = 0.f;
-    src.stats(a.c, M, S);
-    merge_group<NT>(M, S, a.c, room);
+    float M = -kInf, R = 0.f;
+    src.stats(a.c, M, R);
+    merge_group<NT>(M, R, a.c, room);
     if (threadIdx.x < kWave) {
-        const RowScalars k = Mode::row(a, t, info, M, S, zy, true);
+        const RowScalars k = Mode::row(a, t, info, M, R, zy, true);
         if (threadIdx.x == 0)
             scal = k;
     }
@@ -271,7 +282,7 @@ __global__ __launch_bounds__(NT) void row_kernel(LabelArgs a)
     if (k.zero)
         zero_row<T, NT>(out, V, 0, 1);
     else
-        src.dense(out, Dense{k.A, k.M, a.c.hi}, OneTerm{label, k.add});
+        src.dense(out, Dense{k.A, k.M, a.c.hi}, OneTerm{label, k.own});
 }
 
 // Few rows: each over `parts` work-groups.  First launch: partial statistics.
@@ -297,19 +308,14 @@ template <typename T> __global__ __launch_bounds__(kSplit) void part_kernel(Labe
     }
 }
 
-// (M, S) of a row from its partial ones, in every lane of the calling wave.
+// (M, R) of a row from its partial ones, one to a lane.
 __device__ __forceinline__ void merge_parts(const float2 *part, int parts, const Scale &c, float &M,
-                                            float &S)
+                                            float &R)
 {
-    M = -kInf;
-    S = 0.f;
-    for (int i = lane_id(); i < parts; i += kWave) {
-        const float2 p = part[i];
-        const float mn = fmaxf(M, p.x), at = shift_of(mn);
-        S = S * c.pow(M - at) + p.y * c.pow(p.x - at);
-        M = mn;
-    }
-    merge_wave(M, S, c);
+    const float2 p = lane_id() < parts ? part[lane_id()] : make_float2(-kInf, 0.f);
+    M = p.x;
+    R = p.y;
+    merge_wave(M, R, c);
 }
 
 // Second launch: the merged statistics, the scalars (by every part for itself)
@@ -339,9 +345,9 @@ __global__ __launch_bounds__(kSplit) void join_kernel(LabelArgs a, int run)
     const float zy = a.w.zlab[t];
     const typename Mode::Row info = Mode::template begin<kSplit>(a, t, count);
     if (threadIdx.x < kWave) {
-        float M, S;
-        merge_parts(a.w.part + t * a.parts, a.parts, a.c, M, S);
-        const RowScalars k = Mode::row(a, t, info, M, S, zy, part == 0);
+        float M, R;
+        merge_parts(a.w.part + t * a.parts, a.parts, a.c, M, R);
+        const RowScalars k = Mode::row(a, t, info, M, R, zy, part == 0);
         if (threadIdx.x == 0)
             scal = k;
     }
@@ -354,7 +360,7 @@ __global__ __launch_bounds__(kSplit) void join_kernel(LabelArgs a, int run)
         return;
     }
     const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, run);
-    src.dense(out, Dense{k.A, k.M, a.c.hi}, OneTerm{label, k.add});
+    src.dense(out, Dense{k.A, k.M, a.c.hi}, OneTerm{label, k.own});
 }
 
 struct GradArgs {
@@ -382,20 +388,15 @@ template <typename T> __global__ __launch_bounds__(kSplit) void label_grad_kerne
     const RowState state = row_state(a.p, t, a.r.T, label);
     if (state == kOutside)
         return;
-    const RowStat k0 = state == kUsed ? a.stat[t] : RowStat{0.f, 0.f, 0.0};
-    const float M = k0.M;
-    const double shrink = 1.0 / (double)k0.S;   // softmax = 2^((z - M) c) * shrink
-    const bool none = k0.S == 0.f;
+    const RowStat stat = state == kUsed ? a.stat[t] : RowStat{-kInf, 0.f, 0.0};
     const double add = (state == kUsed ? (double)a.G[t] : 0.0) * a.r.scale;
-    if (state == kZeroRow || none) {
+    const RowScalars k = coefficients(add, stat.logp, stat.M, stat.R);
+    if (k.zero) {
         zero_row<T, kSplit>(out, V, part, a.parts);
         return;
     }
-    const T *row = (const T *)a.r.logits + t * a.r.ld;
-    const Streamed<T, kSplit> src(row, V, part, a.parts);
-    // a label beyond the row has no log-probability: NaN, like its loss
-    const float A = label < V ? (float)(-add * shrink) : __builtin_nanf("");
-    src.dense(out, Dense{A, M, a.c.hi}, OneTerm{label, (float)add});
+    const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, a.parts);
+    src.dense(out, Dense{k.A, k.M, a.c.hi}, OneTerm{label, k.own});
 }
 
 // --- per sequence
@@ -471,7 +472,7 @@ __global__ __launch_bounds__(kSeqThreads) void preference_kernel(const int32_t *
     int n = 0;
     for (long t = first; t < r.last; t += half)
         // a row without any finite logit drops out like one without a label
-        if (labels[t] >= 0 && a.stat[t].S != 0.f) {
+        if (labels[t] >= 0 && !row_empty(a.stat[t].M, a.stat[t].R)) {
             sum += a.stat[t].logp - (a.ref ? (double)a.ref[t] : 0.0);
             ++n;
         }

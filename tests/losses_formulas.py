@@ -10,11 +10,10 @@ joins add 30 more, each rounding by 2^-24.  So the sum S is off, relative, by at
 lse and logp by eps_S and their own rounding (2^-24 relative), and an element q_v of the softmax,
 relative, by eps_S + 2^-23 + 3 ln 2 2^-24 |argument| + 4 roundings.
 
-The logarithm of S, taken as its exponent and the logarithm of its mantissa, is off by 2^-24,
-which the 30 above leave room for (at most 10 joins take place).
+The logarithm of S is taken in fp64.
 
-A teacher's probability p_k is an fp32 exponential of an argument formed in fp64 and rounded once
-(2^-24 |argument|), over the fp32 sum of K of them (K/64 + 10 additions), divided and stored: off,
+A teacher's probability p_k is an fp32 exponential of an argument rounded once (2^-24 |argument|)
+and, where the K are normalised among themselves, over a sum of such (K/64 + 10 additions): off,
 relative, by at most 2^-24 (14 + K/64 + |argument|).
 """
 import math

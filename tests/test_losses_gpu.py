@@ -237,6 +237,45 @@ def test_distill_of_a_long_list_on_a_long_row():
     F.check(got[1], want[1], "dlogits")
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("T,V", [(9, 900), (9, 40000), (9, 90001), (133, 70001)])
+def test_one_value_has_nearly_all_of_the_probability(T, V, dt):
+    """log q and 1 - q near 0 to their own size.  The rest of the sum, without the largest term, is
+    off relative by the terms' own errors (arguments up to 40: 3 ln 2 2^-24 * 40, and 2^-23) and
+    its additions, as eps_S; the logarithm and the last roundings add 4 units."""
+    g = rng(T + V)
+    z = (torch.randn(T, V, generator=g)).to(TYPES[dt])
+    y = torch.randint(0, V, (T,), generator=g)
+    y[0], y[1], y[2] = 0, V - 1, 5
+    z[torch.arange(T), y] = torch.linspace(12, 27, T).to(TYPES[dt])
+    z, y = z.cuda(), y.int().cuda()
+    R = F.Rows(z)
+    x = R.z.clone()
+    x[torch.arange(T), y.cpu().long()] = -math.inf
+    rest = torch.exp(x - R.M[:, None]).sum(1)
+    logp = -torch.log1p(rest)
+    rel = F.U * (2 + 2.1 * 40 + V / 512 + 100 + 4)
+    got, _ = sk.token_logprobs(z, y)
+    F.check(got, (logp, rel * logp.abs()), "logp")
+    far = rest / (1 + rest)               # 1 - q at the label
+    want = -R.q
+    want[torch.arange(T), y.cpu().long()] = far
+    # bf16: the rounding of each value, fp32: within eps_S and the argument's error, relative
+    tol = (rel + F.HALF[z.dtype]) * 1.01 * want.abs()
+    F.check(sk.token_logprobs_backward(z, y, torch.ones(T).cuda()), (want, tol), "dlogits")
+    off = torch.tensor([0, T]).cuda()
+    loss, reward, lp, d = sk.preference_loss(z, y, torch.tensor([0, T, T]).cuda(), kind="square",
+                                             beta=1.0)
+    slope = 2 * (logp.sum() - 0.5)
+    F.check(d, (want * slope, tol * slope.abs() + rel * (want * slope).abs()), "pairs")
+    _, _, _, d = sk.policy_loss(z, y, off, got, torch.ones(T).cuda(), mean=False)
+    F.check(d, (-want, tol + 4 * rel * want.abs()), "policy")
+    u = torch.zeros(T, 1).cuda()
+    loss, d = sk.distill_loss(z, y[:, None], u)
+    F.check(loss, (-logp, rel * logp.abs()), "loss")
+    F.check(d, (-want, tol), "distill")
+
+
 def test_one_token_many_times():
     # every entry the same token, and pairs of them on either side of a wave's 64 entries
     g = rng(22)
