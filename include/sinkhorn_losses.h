@@ -15,6 +15,7 @@
  *   - dlogits has the logits' dtype and rows `dld` apart.  It may be the logits
  *     themselves (the same address and row distance): the gradient is then
  *     written over them.  Any other overlap is refused.  NULL: no gradient.
+ *     No other output may share memory with an input.
  *   - 0 <= T <= 2^24 rows and 1 <= V <= 2^24 values.  With T == 0 the pointers
  *     of row arrays may be NULL.
  *   - labels is [T] int32.  A negative label marks a row that is not scored (a
@@ -110,7 +111,7 @@ int sinkhorn_token_logprobs_backward(const void *logits, int dtype, int64_t ld,
  * w_i = weights[i] (1 if NULL), divided by the sequence's number of labels with
  * SK_LOSS_MEAN.  At a border (r = 1 - clip_lo or 1 + clip_hi exactly) the row
  * is not clipped.  0 <= clip_lo < 1, clip_hi >= 0 (infinite: never), and
- * kl_coef finite.  loss, kl: [n]; logp [T] may be NULL.
+ * kl_coef finite (0: kl is reported alone).  loss, kl: [n]; logp [T] may be NULL.
  */
 int sinkhorn_policy_loss(const void *logits, int dtype, int64_t ld, const int32_t *labels,
                          int T, int V, const int64_t *offsets, int n,
@@ -149,8 +150,8 @@ int sinkhorn_preference_loss(const void *logits, int dtype, int64_t ld, const in
  * w_t = weights[t] (1 if NULL).  A row of weight 0 is not read; its loss and
  * gradient are 0.  A negative index, or a teacher logit of -inf, is no entry; a
  * row without entries has loss and gradient 0.  A token may stand in the list
- * more than once.  An index of V or more makes the row NaN.  p is rounded to
- * fp32 once, for loss and gradient alike.
+ * more than once.  An index of V or more, or a teacher logit of NaN or +inf,
+ * makes the row NaN.
  */
 int sinkhorn_distill_loss(const void *logits, int dtype, int64_t ld, int T, int V,
                           const int32_t *index, const float *teacher, int K,

@@ -116,7 +116,7 @@ __device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const Lis
     int bad = 0;
     each(l, K, [&](int, int v, float u) {
         if (v >= 0) {
-            bad |= v >= V || u != u;
+            bad |= v >= V || !(u < kInf);
             top = fmaxf(top, u);
         }
     });
@@ -195,7 +195,7 @@ __device__ __forceinline__ RowScalars student_side(const Args &a, long t, const 
     const double add = w * tau, over = r.bad ? nan : r.C / row_sum(M, R);
     // log p_k - log q_k = (u_k - (z_k - M)) / tau - (U - ln(1 + R)): fp64, for it
     // is small where the two agree
-    const double apart = r.U - ln_sum(R);
+    const double apart = r.U - row_ln(M, R);
     double sum = 0.0;
     each(l, K, [&](int k, int, float u) {
         const double p = l.p[k];
@@ -306,7 +306,7 @@ __global__ __launch_bounds__(NT, Src::waves) void distill_kernel(Args a)
         zero_row<T, NT>(out, V, 0, 1);
         return;
     }
-    src.dense(out, Dense{k.A, k.M, a.c.hi}, ListTerms(l));
+    src.dense(out, Dense{k.A, k.M, a.c.near}, ListTerms(l));
 }
 
 // Few rows: partial statistics, and the student's logits at the list's tokens
@@ -376,7 +376,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
         zero_row<T, kSplit>(out, V, part, run);
         return;
     }
-    src.dense(out, Dense{k.A, k.M, a.c.hi}, ListTerms(l));
+    src.dense(out, Dense{k.A, k.M, a.c.near}, ListTerms(l));
 }
 
 template <typename T> struct RunRows {

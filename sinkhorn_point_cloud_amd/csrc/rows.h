@@ -202,7 +202,7 @@ __device__ __forceinline__ double sum_wave(double v)
 // log-probability, which adds up over a sequence.  hi lies below c, so that lo is
 // positive and a difference of -inf gives -inf in both terms.
 struct Scale {
-    float hi, lo;
+    float hi, lo, near;   // near: c rounded, for what no sum takes up
     __device__ __forceinline__ float pow(float d) const { return ex2(fmaf(d, hi, d * lo)); }
 };
 inline Scale scale_of_row(double scale)
@@ -211,7 +211,7 @@ inline Scale scale_of_row(double scale)
     float hi = (float)c;
     if ((double)hi >= c)
         hi = nextafterf(hi, 0.f);
-    return Scale{hi, (float)(c - (double)hi)};
+    return Scale{hi, (float)(c - (double)hi), (float)c};
 }
 
 // Running maximum and rest.  The shift of an empty state is 0, so that no
@@ -284,6 +284,11 @@ __device__ __forceinline__ bool row_empty(float M, float R) { return M == -kInf 
 __device__ __forceinline__ double row_sum(float M, float R)
 {
     return M == kInf ? __builtin_nan("") : 1.0 + (double)R;
+}
+__device__ __forceinline__ double ln_sum(float R);
+__device__ __forceinline__ double row_ln(float M, float R)
+{
+    return M == kInf ? __builtin_nan("") : ln_sum(R);
 }
 
 // ln(1 + R) to fp64 precision: 2 artanh(t), t = R / (2 + R), or for larger R the

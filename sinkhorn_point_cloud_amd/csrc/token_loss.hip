@@ -76,11 +76,6 @@ __device__ __forceinline__ RowState row_state(const LabelArgs &a, long t, int la
 
 // --- the scalar phase: fp64, one wave, the same in every lane
 
-__device__ __forceinline__ double row_ln(float M, float R)
-{
-    return M == kInf ? __builtin_nan("") : ln_sum(R);
-}
-
 // add (1[v = label] - q_v).  A NaN log-probability (a label beyond the row)
 // makes the whole row NaN.
 __device__ __forceinline__ RowScalars coefficients(double add, double logp, float M, float R)
@@ -213,18 +208,21 @@ struct PolicyMode {
         const bool below = adv < 0.f && change < q.log_lo;
         const double gain = (above ? q.hi : below ? q.lo : (double)ratio) * (double)adv;
         double slope = above || below ? 0.0 : -(double)ratio * (double)adv;   // d(-gain)/d logp
-        double kl = 0.0;
+        double kl = 0.0, cost = 0.0;
         if (q.ref) {
             const float gap = (float)((double)q.ref[t] - logp);
             const float over = exp_over(gap);   // e^gap - 1 - gap
             kl = (double)over;
-            slope -= q.kl * ((double)over + (double)gap);
+            if (q.kl != 0.0) {   // only reported else, and it may be infinite
+                cost = q.kl * kl;
+                slope -= q.kl * ((double)over + (double)gap);
+            }
         }
         if (writes && lane_id() == 0) {
             if (q.logp)
                 q.logp[t] = none ? 0.f : (float)logp;
             q.term[t] = none ? make_float2(0.f, 0.f)
-                             : make_float2((float)(w * (q.kl * kl - gain)),
+                             : make_float2((float)(w * (cost - gain)),
                                            (float)(w * kl));
         }
         return coefficients(slope * w * s, logp, M, R);
@@ -282,7 +280,7 @@ __global__ __launch_bounds__(NT, Src::waves) void row_kernel(LabelArgs a)
     if (k.zero)
         zero_row<T, NT>(out, V, 0, 1);
     else
-        src.dense(out, Dense{k.A, k.M, a.c.hi}, OneTerm{label, k.own});
+        src.dense(out, Dense{k.A, k.M, a.c.near}, OneTerm{label, k.own});
 }
 
 // Few rows: each over `parts` work-groups.  First launch: partial statistics.
@@ -360,7 +358,7 @@ __global__ __launch_bounds__(kSplit) void join_kernel(LabelArgs a, int run)
         return;
     }
     const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, run);
-    src.dense(out, Dense{k.A, k.M, a.c.hi}, OneTerm{label, k.own});
+    src.dense(out, Dense{k.A, k.M, a.c.near}, OneTerm{label, k.own});
 }
 
 struct GradArgs {
@@ -396,7 +394,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void label_grad_kerne
         return;
     }
     const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, a.parts);
-    src.dense(out, Dense{k.A, k.M, a.c.hi}, OneTerm{label, k.own});
+    src.dense(out, Dense{k.A, k.M, a.c.near}, OneTerm{label, k.own});
 }
 
 // --- per sequence
@@ -498,7 +496,10 @@ __global__ __launch_bounds__(kSeqThreads) void preference_kernel(const int32_t *
             // -(1 - eps) log sigma(h) - eps log sigma(-h), h = beta gap
             const double x = beta * gap, eps = a.smoothing;
             const double e = exp(-fabs(x)), far = log1p(e);
-            loss = x != x ? x : (1.0 - eps) * (far + fmax(-x, 0.0)) + eps * (far + fmax(x, 0.0));
+            // (a side without weight has no part, though it may be infinite)
+            loss = eps < 1.0 ? (1.0 - eps) * (far + fmax(-x, 0.0)) : 0.0;
+            loss += eps > 0.0 ? eps * (far + fmax(x, 0.0)) : 0.0;
+            loss = x != x ? x : loss;
             // sigma(-x)
             slope = beta * (eps - (x > 0.0 ? e : 1.0) / (1.0 + e));
         } else {
@@ -539,9 +540,11 @@ template <typename T, typename Mode> struct RunRows {
 template <typename T, typename Mode> void launch_rows(const LabelArgs &a, hipStream_t st)
 {
     if (a.parts > 1) {
-        hipLaunchKernelGGL((part_kernel<T>), grid_of((long)a.r.T * a.parts), dim3(kSplit), 0, st, a);
+        hipLaunchKernelGGL((part_kernel<T>), grid_of((long)a.r.T * a.parts), dim3(kSplit), 0, st,
+                           a);
         const int run = Mode::kGradient && a.r.dlogits ? a.parts : 1;
-        hipLaunchKernelGGL((join_kernel<T, Mode>), grid_of((long)a.r.T * run), dim3(kSplit), 0, st, a, run);
+        hipLaunchKernelGGL((join_kernel<T, Mode>), grid_of((long)a.r.T * run), dim3(kSplit), 0,
+                           st, a, run);
         return;
     }
     const RunRows<T, Mode> run{a, st};

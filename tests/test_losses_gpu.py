@@ -578,6 +578,24 @@ def test_masked_label_takes_the_formula():
     F.check(loss, F.policy(z, y, off, old, torch.ones(6))[0], "loss")
     assert (d[2] == 0).all() and kl == 0
     assert sk.policy_loss(z, y, off, old, torch.ones(6).cuda(), ref=old, kl=0.1)[1] == math.inf
+    # with coefficient 0 the infinite KL is reported and enters nothing
+    loss0, kl0, _, d0 = sk.policy_loss(z, y, off, old, torch.ones(6).cuda(), ref=old, kl=0.0)
+    assert kl0 == math.inf and torch.equal(loss0, loss) and torch.equal(d0, d)
+    # an impossible token: of the other sequence, the loss is 0 and nothing is left to learn; of the
+    # preferred one, it is infinite
+    pair = torch.tensor([0, 2, 4]).cuda()
+    loss, reward, _, d = sk.preference_loss(z, y, pair)
+    assert loss == 0 and reward[1] == -math.inf and (d == 0).all()
+    loss, reward, _, d = sk.preference_loss(z, y, torch.tensor([1, 4, 6]).cuda())
+    assert loss == math.inf and reward[0] == -math.inf and d.isfinite().all()
+    # distillation towards it: infinite loss, finite gradient
+    idx = torch.tensor([[3, 4]] * 6, dtype=torch.int32).cuda()
+    u = torch.zeros(6, 2).cuda()
+    loss, d = sk.distill_loss(z, idx, u)
+    assert loss[2] == math.inf and d.isfinite().all() and d[2, 3].item() == -0.5
+    u[1, 0], u[4, 1] = math.inf, math.nan
+    loss, d = sk.distill_loss(z, idx, u)
+    assert loss[[1, 4]].isnan().all() and d[[1, 4]].isnan().all() and d[[0, 2, 3, 5]].isfinite().all()
 
 
 def test_ratio_at_a_border_is_not_clipped():
