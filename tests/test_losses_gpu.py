@@ -712,3 +712,52 @@ def test_long_rows_pass_32_bits():
     ref, t = F.Rows(tail).label_grad(y[-4:], torch.ones(4).double(), torch.full((4,), 4 * tol).double())
     F.check(d[-4:], (ref, t), "dlogits")
     assert (d[:-4].view(torch.int16) == 0).all()
+
+
+@pytest.mark.parametrize("T,V", [((1 << 20) * 3 + 7, 3), (2, 1 << 24)])
+def test_many_rows_and_the_longest(T, V):
+    # more work-groups than one dimension of a launch is given, and the largest row
+    g = rng(31)
+    z = torch.randn(T, V, generator=g)
+    y = torch.randint(-1, V, (T,), generator=g).int()
+    y[-1] = V - 1
+    zd, yd = z.cuda(), y.cuda()
+    R = F.Rows(z)
+    logp, _ = sk.token_logprobs(zd, yd)
+    F.check(logp, R.logp(y), "logp")
+    w = torch.randn(T, generator=g)
+    d = sk.token_logprobs_backward(zd, yd, w.cuda())
+    F.check(d, R.label_grad(y, w.double(), torch.zeros(T).double()), "dlogits")
+    idx = torch.randint(0, V, (T, 2), generator=g).int()
+    u = torch.randn(T, 2, generator=g)
+    loss, dd = sk.distill_loss(zd, idx.cuda(), u.cuda())
+    rows = torch.tensor([0, 1, T // 2, T - 1])
+    want = F.distill(z[rows], idx[rows], u[rows])
+    F.check(loss[rows.cuda()], want[0], "loss")
+    F.check(dd[rows.cuda()], want[1], "distill")
+
+
+def test_many_routed_rows():
+    g = rng(32)
+    T, E, K = (1 << 21) + 3, 4, 2
+    z = torch.randn(T, E, generator=g)
+    idx = z.topk(K, dim=1).indices.int()
+    off = torch.tensor([0, 5, T // 3, T // 3, T])
+    loss, zloss, counts, d = sk.balance_loss(z.cuda(), idx.cuda(), off.cuda(), balance=2.0, z=0.5)
+    q, lse = torch.softmax(z.double(), 1), torch.logsumexp(z.double(), 1)
+    for i, (a, b) in enumerate(F.ranges(off, T)):
+        n = b - a
+        hot = torch.bincount(idx[a:b].reshape(-1).long(), minlength=E)
+        assert torch.equal(counts[i].cpu().long(), hot)
+        if not n:
+            assert loss[i] == 0 and zloss[i] == 0
+            continue
+        f = hot.double() * E / (K * n)
+        dot = (q[a:b] * f).sum(1)
+        # per row: the softmax's eps_S, f's rounding; the sum over rows is fp64
+        assert abs(loss[i].item() - dot.mean().item()) <= (F.eps_sum(E) + 8 * F.U) * f.max().item()
+        want = q[a:b] * (2.0 * (f - dot[:, None]) + lse[a:b, None]) / n
+        size = (2 * (f.max() + dot[:, None]) + lse[a:b, None].abs()) * q[a:b] / n
+        assert ((d[a:b].cpu().double() - want).abs() <= 2 * (F.eps_sum(E) + 16 * F.U) * size).all()
+        assert abs(zloss[i].item() - (lse[a:b] ** 2).mean().item()) <= \
+            (2 * F.eps_sum(E) + 8 * F.U) * ((lse[a:b].abs() + 1) ** 2).mean().item()
