@@ -52,10 +52,6 @@ hipError_t launch_logp(const LogitRows &r, const int32_t *labels, const Packed &
 // dlogits = G_t scale (1[v = label] - softmax), the softmax found on the way
 hipError_t launch_logp_backward(const LogitRows &r, const int32_t *labels, const float *G,
                                 const TokenWs &w, hipStream_t st);
-// the same with the rows' statistics given
-hipError_t launch_label_grad(const LogitRows &r, const int32_t *labels, const Packed &p,
-                             const RowStat *stat, const float *G, hipStream_t st);
-
 struct PolicyArgs {
     const float *old, *ref, *adv, *weights;
     int adv_per_token, mean;

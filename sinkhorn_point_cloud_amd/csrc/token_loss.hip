@@ -68,6 +68,13 @@ __device__ __forceinline__ SeqRange seq_range(const Packed &p, int i, long T)
     return r;
 }
 
+// The sequence of a row, of at most kWave of them: as many as end at or before it.
+__device__ __forceinline__ int seq_of(const Packed &p, long t)
+{
+    const bool ends = lane_id() < p.n && (long)p.offsets[lane_id() + 1] <= t;
+    return min((int)__popcll(__ballot(ends)), p.n - 1);
+}
+
 __device__ __forceinline__ RowState row_state(const LabelArgs &a, long t, int label)
 {
     const RowState r = row_state(a.p, t, a.r.T, label);
@@ -172,10 +179,7 @@ struct PolicyMode {
             const float2 info = q.info[t];
             return Row{info.x, info.y};
         }
-        // the sequence is the number of sequences that end at or before t
-        const int lane = lane_id();
-        const bool ends = lane < a.p.n && (long)a.p.offsets[lane + 1] <= t;
-        const int i = min((int)__popcll(__ballot(ends)), a.p.n - 1);
+        const int lane = lane_id(), i = seq_of(a.p, t);
         double w = q.weights ? (double)q.weights[i] : 1.0;
         if (q.mean) {
             const SeqRange r = seq_range(a.p, i, a.r.T);
@@ -361,42 +365,6 @@ __global__ __launch_bounds__(kSplit) void join_kernel(LabelArgs a, int run)
     src.dense(out, Dense{k.A, k.M, a.c.near}, OneTerm{label, k.own});
 }
 
-struct GradArgs {
-    LogitRows r;
-    const int32_t *labels;
-    Packed p;
-    const RowStat *stat;
-    const float *G;
-    int parts;
-    Scale c;
-};
-
-// The gradient of rows whose statistics are known.
-template <typename T> __global__ __launch_bounds__(kSplit) void label_grad_kernel(GradArgs a)
-{
-    // last rows first: they are the ones that the statistics' pass read last, and
-    // up to 256 MB of them are still in the last-level cache (8192 x 65536 bf16,
-    // half of them scored: 402 -> 394 us for the two passes)
-    const long t = a.r.T - 1 - group_index() / a.parts;
-    const int part = (int)(group_index() % a.parts), V = a.r.V;
-    if (t < 0)
-        return;
-    T *out = (T *)a.r.dlogits + t * a.r.dld;
-    const int label = a.labels[t];
-    const RowState state = row_state(a.p, t, a.r.T, label);
-    if (state == kOutside)
-        return;
-    const RowStat stat = state == kUsed ? a.stat[t] : RowStat{-kInf, 0.f, 0.0};
-    const double add = (state == kUsed ? (double)a.G[t] : 0.0) * a.r.scale;
-    const RowScalars k = coefficients(add, stat.logp, stat.M, stat.R);
-    if (k.zero) {
-        zero_row<T, kSplit>(out, V, part, a.parts);
-        return;
-    }
-    const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, a.parts);
-    src.dense(out, Dense{k.A, k.M, a.c.near}, OneTerm{label, k.own});
-}
-
 // --- per sequence
 
 constexpr int kSeqThreads = 1024;
@@ -455,20 +423,22 @@ __global__ __launch_bounds__(kSeqThreads) void policy_sum_kernel(Packed p, long 
     }
 }
 
-// One pair: the two sequences' summed log-ratios (half of the threads each),
-// the loss and its slope.
-__global__ __launch_bounds__(kSeqThreads) void preference_kernel(const int32_t *labels, Packed p,
-                                                                 long T, PreferenceArgs a)
+// One pair, by a work-group of NT threads: the two sequences' summed log-ratios
+// (half of the threads each), the loss (written where asked for) and, left in
+// slopes, its derivative by a log-probability of either sequence.  One barrier
+// inside; `slopes` is there for every thread behind another.
+template <int NT>
+__device__ __forceinline__ void pair_slopes(const int32_t *labels, const Packed &p, long T,
+                                            const PreferenceArgs &a, int i, bool writes,
+                                            double (&room)[2][2][NT / 2 / kWave],
+                                            float (&slopes)[2])
 {
-    constexpr int half = kSeqThreads / 2, waves = half / kWave;
-    __shared__ double room[2][2][waves];
-    __shared__ float slopes[2];
-    const int i = blockIdx.x, h = threadIdx.x / half;
+    constexpr int half = NT / 2, waves = half / kWave;
+    const int h = threadIdx.x / half;
     const SeqRange r = seq_range(p, 2 * i + h, T);
-    const long first = r.first + threadIdx.x % half;
     double sum = 0.0;
     int n = 0;
-    for (long t = first; t < r.last; t += half)
+    for (long t = r.first + threadIdx.x % half; t < r.last; t += half)
         // a row without any finite logit drops out like one without a label
         if (labels[t] >= 0 && !row_empty(a.stat[t].M, a.stat[t].R)) {
             sum += a.stat[t].logp - (a.ref ? (double)a.ref[t] : 0.0);
@@ -481,44 +451,109 @@ __global__ __launch_bounds__(kSeqThreads) void preference_kernel(const int32_t *
         room[h][1][threadIdx.x % half / kWave] = (double)n;
     }
     __syncthreads();
-    if (threadIdx.x < kWave) {
-        double ratio[2], share[2];
-        for (int k = 0; k < 2; ++k) {
-            const double v = sum_wave(lane_id() < waves ? room[k][0][lane_id()] : 0.0);
-            const double c = sum_wave(lane_id() < waves ? room[k][1][lane_id()] : 0.0);
-            share[k] = a.mean ? (c > 0.0 ? 1.0 / c : 0.0) : 1.0;
-            ratio[k] = v * share[k];
-        }
-        const double beta = a.beta, gap = ratio[0] - ratio[1];
-        const double w = a.weights ? (double)a.weights[i] : 1.0;
-        double loss, slope;
-        if (a.kind == 0) {
-            // -(1 - eps) log sigma(h) - eps log sigma(-h), h = beta gap
-            const double x = beta * gap, eps = a.smoothing;
-            const double e = exp(-fabs(x)), far = log1p(e);
-            // (a side without weight has no part, though it may be infinite)
-            loss = eps < 1.0 ? (1.0 - eps) * (far + fmax(-x, 0.0)) : 0.0;
-            loss += eps > 0.0 ? eps * (far + fmax(x, 0.0)) : 0.0;
-            loss = x != x ? x : loss;
-            // sigma(-x)
-            slope = beta * (eps - (x > 0.0 ? e : 1.0) / (1.0 + e));
-        } else {
-            const double d = gap - 0.5 / beta;
-            loss = d * d;
-            slope = 2.0 * d;
-        }
-        if (threadIdx.x == 0) {
+    if (threadIdx.x >= kWave)
+        return;
+    double ratio[2], share[2];
+    for (int k = 0; k < 2; ++k) {
+        const double v = sum_wave(lane_id() < waves ? room[k][0][lane_id()] : 0.0);
+        const double c = sum_wave(lane_id() < waves ? room[k][1][lane_id()] : 0.0);
+        share[k] = a.mean ? (c > 0.0 ? 1.0 / c : 0.0) : 1.0;
+        ratio[k] = v * share[k];
+    }
+    const double beta = a.beta, gap = ratio[0] - ratio[1];
+    const double w = a.weights ? (double)a.weights[i] : 1.0;
+    double loss, slope;
+    if (a.kind == 0) {
+        // -(1 - eps) log sigma(h) - eps log sigma(-h), h = beta gap
+        const double x = beta * gap, eps = a.smoothing;
+        const double e = exp(-fabs(x)), far = log1p(e);
+        // (a side without weight has no part, though it may be infinite)
+        loss = eps < 1.0 ? (1.0 - eps) * (far + fmax(-x, 0.0)) : 0.0;
+        loss += eps > 0.0 ? eps * (far + fmax(x, 0.0)) : 0.0;
+        loss = x != x ? x : loss;
+        // sigma(-x)
+        slope = beta * (eps - (x > 0.0 ? e : 1.0) / (1.0 + e));
+    } else {
+        const double d = gap - 0.5 / beta;
+        loss = d * d;
+        slope = 2.0 * d;
+    }
+    if (threadIdx.x == 0) {
+        if (writes) {
             a.loss[i] = (float)(w * loss);
             a.reward[2 * i] = (float)(beta * ratio[0]);
             a.reward[2 * i + 1] = (float)(beta * ratio[1]);
-            slopes[0] = (float)(slope * w * share[0]);
-            slopes[1] = (float)(-slope * w * share[1]);
         }
+        slopes[0] = (float)(slope * w * share[0]);
+        slopes[1] = (float)(-slope * w * share[1]);
     }
+}
+
+__global__ __launch_bounds__(kSeqThreads) void preference_kernel(const int32_t *labels, Packed p,
+                                                                 long T, PreferenceArgs a)
+{
+    constexpr int half = kSeqThreads / 2;
+    __shared__ double room[2][2][half / kWave];
+    __shared__ float slopes[2];
+    const int i = blockIdx.x, h = threadIdx.x / half;
+    pair_slopes<kSeqThreads>(labels, p, T, a, i, true, room, slopes);
     __syncthreads();
+    const SeqRange r = seq_range(p, 2 * i + h, T);
     const float k = slopes[h];
-    for (long t = first; t < r.last; t += half)
+    for (long t = r.first + threadIdx.x % half; t < r.last; t += half)
         a.coef[t] = labels[t] >= 0 ? k : 0.f;
+}
+
+struct GradArgs {
+    LogitRows r;
+    const int32_t *labels;
+    Packed p;
+    PreferenceArgs q;
+    int parts;
+    Scale c;
+};
+
+// The gradient of a preference loss's rows, whose statistics are known.  Fold:
+// each work-group sums its own row's pair, and as many more work-groups as there
+// are pairs write the losses; else their slopes are in q.coef.
+template <typename T, bool Fold> __global__ __launch_bounds__(kSplit) void pair_grad_kernel(GradArgs a)
+{
+    __shared__ double room[2][2][kSplit / 2 / kWave];
+    __shared__ float slopes[2];
+    // last rows first: they are the ones that the statistics' pass read last, and
+    // up to 256 MB of them are still in the last-level cache (8192 x 65536 bf16,
+    // half of them scored: 402 -> 394 us for the two passes)
+    const long rows = a.r.dlogits ? a.r.T : 0;
+    const long t = rows - 1 - group_index() / a.parts;
+    const int part = (int)(group_index() % a.parts), V = a.r.V;
+    if (t < 0) {
+        const long i = group_index() - rows * a.parts;
+        if (Fold && i < a.p.n / 2)
+            pair_slopes<kSplit>(a.labels, a.p, a.r.T, a.q, (int)i, true, room, slopes);
+        return;
+    }
+    T *out = (T *)a.r.dlogits + t * a.r.dld;
+    const int label = a.labels[t];
+    const RowState state = row_state(a.p, t, a.r.T, label);
+    if (state == kOutside)
+        return;
+    const RowStat stat = state == kUsed ? a.q.stat[t] : RowStat{-kInf, 0.f, 0.0};
+    if (row_empty(stat.M, stat.R)) {
+        zero_row<T, kSplit>(out, V, part, a.parts);
+        return;
+    }
+    float G;
+    if constexpr (Fold) {
+        const int i = seq_of(a.p, t);
+        pair_slopes<kSplit>(a.labels, a.p, a.r.T, a.q, i / 2, false, room, slopes);
+        __syncthreads();
+        G = slopes[i % 2];
+    } else {
+        G = a.q.coef[t];
+    }
+    const RowScalars k = coefficients((double)G * a.r.scale, stat.logp, stat.M, stat.R);
+    const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, a.parts);
+    src.dense(out, Dense{k.A, k.M, a.c.near}, OneTerm{label, k.own});
 }
 
 }  // namespace
@@ -566,9 +601,9 @@ template <typename Mode> hipError_t dispatch_rows(const LabelArgs &a, hipStream_
 
 }  // namespace
 
-// A row's weight is found in its own work-group where that is cheap: the
-// sequences are one to a lane, and a sequence's labels a few to a thread.  It
-// saves a launch.
+// What a row needs of its sequence or pair (a count of labels, two sums) is found
+// in its own work-group where that is cheap: the sequences are one to a lane, and
+// a sequence's rows a few to a thread.  It saves a launch.
 static int fold_rows(int T, int n) { return n <= kWave && T <= 2048; }
 
 // Work-groups per row.  A row of up to 128 KB is one work-group's (one launch):
@@ -605,18 +640,6 @@ hipError_t launch_logp(const LogitRows &r, const int32_t *labels, const Packed &
     a.c = scale_of_row(r.scale);
     a.out = out;
     return dispatch_rows<LogpMode>(a, st);
-}
-
-hipError_t launch_label_grad(const LogitRows &r, const int32_t *labels, const Packed &p,
-                             const RowStat *stat, const float *G, hipStream_t st)
-{
-    GradArgs a{r, labels, p, stat, G, grad_parts(r.T, r.V, r.dtype), scale_of_row(r.scale)};
-    const dim3 grid = grid_of((long)r.T * a.parts);
-    if (r.dtype == 1)
-        hipLaunchKernelGGL((label_grad_kernel<uint16_t>), grid, dim3(kSplit), 0, st, a);
-    else
-        hipLaunchKernelGGL((label_grad_kernel<float>), grid, dim3(kSplit), 0, st, a);
-    return hipGetLastError();
 }
 
 hipError_t launch_logp_backward(const LogitRows &r, const int32_t *labels, const float *G,
@@ -656,6 +679,15 @@ hipError_t launch_policy(const LogitRows &r, const int32_t *labels, const Packed
     return hipGetLastError();
 }
 
+template <bool Fold> static void run_pairs(const GradArgs &a, hipStream_t st)
+{
+    const dim3 grid = grid_of((a.r.dlogits ? (long)a.r.T * a.parts : 0) + (Fold ? a.p.n / 2 : 0));
+    if (a.r.dtype == 1)
+        hipLaunchKernelGGL((pair_grad_kernel<uint16_t, Fold>), grid, dim3(kSplit), 0, st, a);
+    else
+        hipLaunchKernelGGL((pair_grad_kernel<float, Fold>), grid, dim3(kSplit), 0, st, a);
+}
+
 hipError_t launch_preference(const LogitRows &r, const int32_t *labels, const Packed &p,
                              const PreferenceArgs &q, const TokenWs &w, hipStream_t st)
 {
@@ -665,10 +697,15 @@ hipError_t launch_preference(const LogitRows &r, const int32_t *labels, const Pa
         if (e)
             return e;
     }
-    hipLaunchKernelGGL(preference_kernel, dim3(p.n / 2), dim3(kSeqThreads), 0, st, labels, p,
-                       (long)r.T, q);
-    if (r.T > 0 && r.dlogits)
-        return launch_label_grad(r, labels, p, q.stat, q.coef, st);
+    const GradArgs a{r, labels, p, q, grad_parts(r.T, r.V, r.dtype), scale_of_row(r.scale)};
+    if (fold_rows(r.T, p.n)) {
+        run_pairs<true>(a, st);
+    } else {
+        hipLaunchKernelGGL(preference_kernel, dim3(p.n / 2), dim3(kSeqThreads), 0, st, labels, p,
+                           (long)r.T, q);
+        if (r.dlogits)
+            run_pairs<false>(a, st);
+    }
     return hipGetLastError();
 }
 
