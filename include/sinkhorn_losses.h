@@ -11,7 +11,7 @@
  *   - logits is [T][V] in `dtype` (SK_F32 or SK_BF16), rows `ld` elements apart
  *     (ld >= V; the elements behind V are neither read nor written), at any
  *     address that suits its type.  Rows whose dlogits lie at the same address
- *     modulo 16 bytes as their logits are written fastest.
+ *     modulo 128 bytes as their logits are written fastest.
  *   - dlogits has the logits' dtype and rows `dld` apart.  It may be the logits
  *     themselves (the same address and row distance): the gradient is then
  *     written over them.  Any other overlap is refused.  NULL: no gradient.
@@ -35,7 +35,8 @@
  *     their sum.
  *   - Softmax sums are fp32; logarithms, ratios, clipping decisions and sums
  *     over rows are fp64.  Each output is rounded once.  Same inputs at the
- *     same alignment, same bits: no result depends on an order of atomics.
+ *     same addresses modulo 128 bytes, same bits: no result depends on an order
+ *     of atomics.
  *   - Every call enqueues kernels only and returns without waiting; it can be
  *     captured in a graph.  Calls that overlap need workspaces of their own,
  *     and a captured call's workspace has to outlive its graph.

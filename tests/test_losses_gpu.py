@@ -394,8 +394,8 @@ def test_strided_logits(name, size):
     call, _, z, _ = _setup(name, *size)
     want = call(None)
     T, V = z.shape
-    # 16 bytes more: the rows start at the same alignment, and the sums group alike
-    wide = torch.full((T, V + 16 // z.element_size()), math.nan, dtype=z.dtype, device="cuda")
+    # 128 bytes more: the rows start at the same alignment, and the sums group alike
+    wide = torch.full((T, V + 128 // z.element_size()), math.nan, dtype=z.dtype, device="cuda")
     wide[:, :V] = z
     columns = z.t().contiguous().t()
     for other in (wide[:, :V], columns):
