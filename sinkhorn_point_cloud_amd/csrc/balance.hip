@@ -41,55 +41,77 @@ constexpr int kCounters = 1024;  // a counting work-group, and a small group's
 constexpr int kLanes = 16;       // lanes of a row
 constexpr int kFillers = 64;     // work-groups that zero the rows outside every group
 
-// Where a chunk of `size` rows lies: its group, its rows, and the group's chunks.
+// How rows are cut into chunks: 2^count_bits of them to count, 2^grad_bits for the
+// gradient.  Row numbers and chunks fit 32 bits (2^24 rows, 2^20 groups).
+struct Sizes {
+    int count_bits, grad_bits;
+};
+__device__ __forceinline__ int chunks_of(int rows, int bits)
+{
+    return (rows + (1 << bits) - 1) >> bits;
+}
+
+// Where a chunk lies: its group, its rows, and the group's chunks of either kind.
 struct Place {
-    int group;            // -1: no such chunk
-    long first, last;     // rows of the chunk
-    long chunk0, chunks;  // the group's first chunk and how many it has
+    int group;                  // -1: no such chunk
+    int first, last;            // rows of the chunk
+    int count0, counts;         // the group's first counting chunk and how many it has
+    int grad0;                  // its first gradient chunk
 };
 
-__device__ __forceinline__ long clamp_row(long v, long T) { return min(max(v, 0l), T); }
-
-// Every lane of the calling wave gets the answer.
-__device__ Place place_of(const BalanceArgs &a, long chunk, long size)
+__device__ __forceinline__ int clamp_row(int64_t v, int T)
 {
-    const long T = a.T;
-    Place r{-1, 0, 0, 0, 0};
+    return (int)min(max(v, (int64_t)0), (int64_t)T);
+}
+
+__device__ __forceinline__ int upto_lane(int v)   // inclusive sum over the lanes
+{
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int o = __shfl_up(v, d, kWave);
+        if (lane_id() >= d)
+            v += o;
+    }
+    return v;
+}
+
+// The place of chunk number `chunk` of the one kind or the other; every lane of
+// the calling wave gets the answer.
+template <bool Grad> __device__ Place place_of(const BalanceArgs &a, const Sizes &z, long chunk)
+{
+    const int T = a.T, bits = Grad ? z.grad_bits : z.count_bits;
+    Place r{-1, 0, 0, 0, 0, 0};
     if (!a.offsets) {
-        r.chunks = (T + size - 1) / size;
-        if (chunk < r.chunks)
+        r.counts = chunks_of(T, z.count_bits);
+        if (chunk < chunks_of(T, bits))
             r.group = 0;
-        r.first = chunk * size;
-        r.last = min(r.first + size, T);
+        r.first = (int)chunk << bits;
+        r.last = min(r.first + (1 << bits), T);
         return r;
     }
-    long before = 0;
+    int before_c = 0, before_g = 0;
     for (int base = 0; base < a.G; base += kWave) {
         const int g = base + lane_id();
-        long b = 0, e = 0;
+        int b = 0, e = 0;
         if (g < a.G) {
             b = clamp_row(a.offsets[g], T);
             e = max(clamp_row(a.offsets[g + 1], T), b);
         }
-        const long n = (e - b + size - 1) / size;
-        long upto = n;   // inclusive sum over the lanes
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const long o = __shfl_up(upto, d, kWave);
-            if (lane_id() >= d)
-                upto += o;
-        }
-        const unsigned long long hit = __ballot(chunk < before + upto);
+        const int nc = chunks_of(e - b, z.count_bits), ng = chunks_of(e - b, z.grad_bits);
+        const int uc = before_c + upto_lane(nc), ug = before_g + upto_lane(ng);
+        const unsigned long long hit = __ballot(chunk < (Grad ? ug : uc));
         if (hit) {
             const int at = __ffsll(hit) - 1;
             r.group = base + at;
-            r.chunks = __shfl(n, at, kWave);
-            r.chunk0 = before + __shfl(upto, at, kWave) - r.chunks;
-            r.first = __shfl(b, at, kWave) + (chunk - r.chunk0) * size;
-            r.last = min(r.first + size, __shfl(e, at, kWave));
+            r.counts = __shfl(nc, at, kWave);
+            r.count0 = __shfl(uc - nc, at, kWave);
+            r.grad0 = __shfl(ug - ng, at, kWave);
+            r.first = __shfl(b, at, kWave) + (((int)chunk - (Grad ? r.grad0 : r.count0)) << bits);
+            r.last = min(r.first + (1 << bits), __shfl(e, at, kWave));
             return r;
         }
-        before += __shfl(upto, kWave - 1, kWave);
+        before_c = __shfl(uc, kWave - 1, kWave);
+        before_g = __shfl(ug, kWave - 1, kWave);
     }
     return r;
 }
@@ -97,11 +119,11 @@ __device__ Place place_of(const BalanceArgs &a, long chunk, long size)
 // Adds the choices of rows [first, last) to hist [E + 2]: tokens per expert,
 // rows with a choice, indices out of range.
 template <int NT>
-__device__ __forceinline__ void count_rows(const BalanceArgs &a, long first, long last, int *hist)
+__device__ __forceinline__ void count_rows(const BalanceArgs &a, int first, int last, int *hist)
 {
     int rows = 0, bad = 0;
-    for (long t = first + threadIdx.x; t < last; t += NT) {
-        const int32_t *idx = a.index + t * a.K;
+    for (int t = first + threadIdx.x; t < last; t += NT) {
+        const int32_t *idx = a.index + (long)t * a.K;
         bool any = false;
         for (int k = 0; k < a.K; k += 8) {
             int e[8];
@@ -126,13 +148,13 @@ __device__ __forceinline__ void count_rows(const BalanceArgs &a, long first, lon
     }
 }
 
-__global__ __launch_bounds__(kCounters) void count_kernel(BalanceArgs a, BalanceWs w, long size)
+__global__ __launch_bounds__(kCounters) void count_kernel(BalanceArgs a, BalanceWs w, Sizes z)
 {
     extern __shared__ int hist[];   // [E + 2]
     const long chunk = group_index();
     if (chunk >= w.count_chunks)
         return;
-    const Place at = place_of(a, chunk, size);
+    const Place at = place_of<false>(a, z, chunk);
     if (at.group < 0)
         return;
     for (int e = threadIdx.x; e < a.E + 2; e += kCounters)
@@ -168,7 +190,7 @@ template <typename T, int R, bool Wide> struct Values {
     {
         return (r / W * kLanes + lane) * W + r % W;
     }
-    __device__ __forceinline__ void load(const BalanceArgs &a, long t, int lane)
+    __device__ __forceinline__ void load(const BalanceArgs &a, int t, int lane)
     {
         const T *row = (const T *)a.logits + t * a.ld;
 #pragma unroll
@@ -186,89 +208,98 @@ template <typename T, int R, bool Wide> struct Values {
         }
         int any = -1;
         for (int k = lane; k < a.K; k += kLanes)
-            any = max(any, a.index[t * a.K + k]);
+            any = max(any, a.index[(long)t * a.K + k]);
         first = any;
     }
 };
 
 // The rows [first, last) of one group, NT threads: gradients, and this thread's
-// part of the sums.  f1 [E]: f - 1.
-template <typename T, int NT, int R, bool Wide>
-__device__ __forceinline__ void group_rows(const BalanceArgs &a, long first, long last,
-                                           const float *f1, int n, double &dots, double &squares)
-{
+// part of the sums.  The first rows are asked for before the group's counts are
+// known.
+template <typename T, int NT, int R, bool Wide> struct GroupRows {
     using V = Values<T, R, Wide>;
-    constexpr int W = V::W;
-    const int E = a.E, lane = threadIdx.x % kLanes, slots = NT / kLanes;
-    float f[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int c = V::column(r, lane);
-        f[r] = c < E ? f1[c] : 0.f;
-    }
-    const float over = n ? 1.f / (float)n : 0.f;
-    const float alpha = (float)a.balance * over, zeta = (float)(2.0 * a.z) * over;
+    static constexpr int W = V::W, slots = NT / kLanes;
+    const BalanceArgs &a;
+    const int first, last, lane, t0;
     V next;
-    const long t0 = first + threadIdx.x / kLanes;
-    if (t0 < last)
-        next.load(a, t0, lane);
-    // all lanes of a wave stay together: the lane moves need them
-    const long rounds = (last - first + slots - 1) / slots;
-    for (long i = 0; i < rounds; ++i) {
-        const long t = t0 + i * slots;
-        const V now = next;
-        if (t + slots < last)
-            next.load(a, t + slots, lane);
-        const bool row = t < last;
-        float x[R], m = -kInf, s = 0.f, dot = 0.f;
+
+    __device__ __forceinline__ GroupRows(const BalanceArgs &args, int first, int last)
+        : a(args), first(first), last(last), lane(threadIdx.x % kLanes),
+          t0(first + threadIdx.x / kLanes)
+    {
+        if (t0 < last)
+            next.load(a, t0, lane);
+    }
+    // f1 [E]: f - 1
+    __device__ __forceinline__ void run(const float *f1, int n, double &dots, double &squares)
+    {
+        const int E = a.E;
+        float f[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            x[r] = row && V::column(r, lane) < E ? Pack<T>::get(&now.w[r / W].v[r % W]) : -kInf;
-            m = fmaxf(m, x[r]);
+            const int c = V::column(r, lane);
+            f[r] = c < E ? f1[c] : 0.f;
         }
-        const bool chose = lanes_max(row && now.first >= 0 ? 1.f : 0.f) > 0.f;
-        m = lanes_max(m);
-        const float shift = shift_of(m);
+        const float over = n ? 1.f / (float)n : 0.f;
+        const float alpha = (float)a.balance * over, zeta = (float)(2.0 * a.z) * over;
+        // all lanes of a wave stay together: the lane moves need them
+        const int rounds = (last - first + slots - 1) / slots;
+        for (int i = 0; i < rounds; ++i) {
+            const int t = t0 + i * slots;
+            const V now = next;
+            if (t + slots < last)
+                next.load(a, t + slots, lane);
+            const bool row = t < last;
+            float x[R], m = -kInf, s = 0.f, dot = 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            x[r] = ex2((x[r] - shift) * kLog2e);
-            s += x[r];
-            dot = fmaf(x[r], f[r], dot);
-        }
-        s = row16_sum(s);
-        dot = row16_sum(dot);
-        const bool used = chose && s != 0.f;
-        const float inv = used ? 1.f / s : 0.f, lse = used ? m + logf(s) : 0.f;
-        dot *= inv;
-        if (used && lane == 0) {
-            dots += 1.0 + (double)dot;
-            squares += (double)lse * (double)lse;
-        }
-        if (a.dlogits && row) {
-            T *out = (T *)a.dlogits + t * a.dld;
-            const float base = fmaf(zeta, lse, -alpha * dot);
+            for (int r = 0; r < R; ++r) {
+                x[r] = row && V::column(r, lane) < E ? Pack<T>::get(&now.w[r / W].v[r % W]) : -kInf;
+                m = fmaxf(m, x[r]);
+            }
+            const bool chose = lanes_max(row && now.first >= 0 ? 1.f : 0.f) > 0.f;
+            m = lanes_max(m);
+            const float shift = shift_of(m);
 #pragma unroll
-            for (int i = 0; i < R / W; ++i) {
-                const int c = V::column(i * W, lane);
-                typename V::Word y;
+            for (int r = 0; r < R; ++r) {
+                x[r] = ex2((x[r] - shift) * kLog2e);
+                s += x[r];
+                dot = fmaf(x[r], f[r], dot);
+            }
+            s = row16_sum(s);
+            dot = row16_sum(dot);
+            const bool used = chose && s != 0.f;
+            const float inv = used ? 1.f / s : 0.f, lse = used ? m + logf(s) : 0.f;
+            dot *= inv;
+            if (used && lane == 0) {
+                dots += 1.0 + (double)dot;
+                squares += (double)lse * (double)lse;
+            }
+            if (a.dlogits && row) {
+                T *out = (T *)a.dlogits + t * a.dld;
+                const float base = fmaf(zeta, lse, -alpha * dot);
 #pragma unroll
-                for (int j = 0; j < W; ++j)
-                    Pack<T>::put(&y.v[j], used ? x[i * W + j] * inv *
-                                                     fmaf(alpha, f[i * W + j], base)
-                                               : 0.f);
-                if constexpr (Wide) {
-                    if (c < E)
-                        *reinterpret_cast<typename V::Word *>(out + c) = y;
-                } else {
+                for (int i = 0; i < R / W; ++i) {
+                    const int c = V::column(i * W, lane);
+                    typename V::Word y;
 #pragma unroll
                     for (int j = 0; j < W; ++j)
-                        if (c + j < E)
-                            out[c + j] = y.v[j];
+                        Pack<T>::put(&y.v[j], used ? x[i * W + j] * inv *
+                                                         fmaf(alpha, f[i * W + j], base)
+                                                   : 0.f);
+                    if constexpr (Wide) {
+                        if (c < E)
+                            *reinterpret_cast<typename V::Word *>(out + c) = y;
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < W; ++j)
+                            if (c + j < E)
+                                out[c + j] = y.v[j];
+                    }
                 }
             }
         }
     }
-}
+};
 
 // The two sums over the work-group, in a fixed order; thread 0 and 1 get them.
 template <int NT>
@@ -292,12 +323,12 @@ __device__ __forceinline__ double group_sums(double dots, double squares, double
 // Zeros over the rows outside every group, one of kFillers work-groups.
 template <typename T, int NT> __device__ void fill_rows(const BalanceArgs &a, int filler)
 {
-    const long first = clamp_row(a.offsets[0], a.T);
-    const long last = max(clamp_row(a.offsets[a.G], a.T), first);
-    const long count = first + a.T - last;
-    for (long i = filler * (NT / kWave) + threadIdx.x / kWave; i < count;
-         i += (long)kFillers * (NT / kWave)) {
-        T *out = (T *)a.dlogits + (i < first ? i : last + i - first) * a.dld;
+    const int first = clamp_row(a.offsets[0], a.T);
+    const int last = max(clamp_row(a.offsets[a.G], a.T), first);
+    const int count = first + a.T - last;
+    for (int i = filler * (NT / kWave) + threadIdx.x / kWave; i < count;
+         i += kFillers * (NT / kWave)) {
+        T *out = (T *)a.dlogits + (long)(i < first ? i : last + i - first) * a.dld;
         for (int e = lane_id(); e < a.E; e += kWave)
             Pack<T>::put(out + e, 0.f);
     }
@@ -305,8 +336,7 @@ template <typename T, int NT> __device__ void fill_rows(const BalanceArgs &a, in
 
 // One chunk of rows.
 template <typename T, int R, bool Wide>
-__global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a, BalanceWs w, long size,
-                                                           long count_size)
+__global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a, BalanceWs w, Sizes z)
 {
     extern __shared__ int dyn[];   // [E + 2] counts, [E] f - 1
     __shared__ double room[2 * kThreads / kWave];
@@ -316,34 +346,25 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a, Balanc
             fill_rows<T, kThreads>(a, (int)(chunk - w.grad_chunks));
         return;
     }
-    const Place at = place_of(a, chunk, size);
+    const Place at = place_of<true>(a, z, chunk);
     if (at.group < 0)
         return;
+    GroupRows<T, kThreads, R, Wide> rows(a, at.first, at.last);
     const int E = a.E, K = a.K;
     int *count = dyn;
     float *f1 = (float *)(dyn + E + 2);
     for (int e = threadIdx.x; e < E + 2; e += kThreads)
         count[e] = 0;
-    // the group's counts, from its chunks of the first pass
-    long c0 = 0, cn = (a.T + count_size - 1) / count_size;
-    if (a.offsets) {
-        // chunks of the groups before this one
-        for (int g = lane_id(); g < at.group; g += kWave) {
-            const long b = clamp_row(a.offsets[g], a.T);
-            c0 += (max(clamp_row(a.offsets[g + 1], a.T), b) - b + count_size - 1) / count_size;
-        }
-        c0 = wave_sum(c0);
-        const long b = clamp_row(a.offsets[at.group], a.T);
-        cn = (max(clamp_row(a.offsets[at.group + 1], a.T), b) - b + count_size - 1) / count_size;
-        cn = min(cn, w.count_chunks - c0);
-    }
+    // the group's counts, from its chunks of the first pass (the cap holds for
+    // offsets in order; out of order it keeps the reads in bounds)
+    const int c0 = at.count0, cn = min(at.counts, (int)w.count_chunks - c0);
     __syncthreads();
-    const int32_t *part = w.count_part + c0 * (E + 2);
+    const int32_t *part = w.count_part + (long)c0 * (E + 2);
     for (int e = lane_id(); e < E + 2; e += kWave) {
         int c = 0;
 #pragma unroll 8
-        for (long i = threadIdx.x / kWave; i < cn; i += kThreads / kWave)
-            c += part[i * (E + 2) + e];
+        for (int i = threadIdx.x / kWave; i < cn; i += kThreads / kWave)
+            c += part[(long)i * (E + 2) + e];
         atomicAdd(&count[e], c);
     }
     __syncthreads();
@@ -351,42 +372,40 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a, Balanc
     const double per = n ? (double)E / ((double)K * (double)n) : 0.0;
     for (int e = threadIdx.x; e < E; e += kThreads) {
         f1[e] = bad ? __builtin_nanf("") : (float)((double)count[e] * per - 1.0);
-        if (chunk == at.chunk0)
+        if (chunk == at.grad0)
             a.counts[(long)at.group * E + e] = count[e];
     }
-    if (chunk == at.chunk0 && threadIdx.x == 0)
+    if (chunk == at.grad0 && threadIdx.x == 0)
         w.rows[at.group] = n;
     __syncthreads();
     double dots = 0.0, squares = 0.0;
-    group_rows<T, kThreads, R, Wide>(a, at.first, at.last, f1, n, dots, squares);
+    rows.run(f1, n, dots, squares);
     const double v = group_sums<kThreads>(dots, squares, room);
     if (threadIdx.x < 2)
         w.sum_part[2 * chunk + threadIdx.x] = v;
 }
 
 // The losses of one group; the counts of a group without rows.
-__global__ __launch_bounds__(kThreads) void balance_sum_kernel(BalanceArgs a, BalanceWs w,
-                                                               long size)
+__global__ __launch_bounds__(kThreads) void balance_sum_kernel(BalanceArgs a, BalanceWs w, Sizes z)
 {
     __shared__ double room[2 * kThreads / kWave];
-    const int g = blockIdx.x, E = a.E;
-    const long T = a.T;
-    long b = 0, e = T, c0 = 0;
+    const int g = blockIdx.x, E = a.E, T = a.T;
+    int b = 0, e = T, c0 = 0;
     if (a.offsets) {
         for (int i = lane_id(); i < g; i += kWave) {
-            const long bi = clamp_row(a.offsets[i], T);
-            c0 += (max(clamp_row(a.offsets[i + 1], T), bi) - bi + size - 1) / size;
+            const int bi = clamp_row(a.offsets[i], T);
+            c0 += chunks_of(max(clamp_row(a.offsets[i + 1], T), bi) - bi, z.grad_bits);
         }
         c0 = wave_sum(c0);
         b = clamp_row(a.offsets[g], T);
         e = max(clamp_row(a.offsets[g + 1], T), b);
     }
     // the cap holds for offsets in order; out of order it keeps the reads in bounds
-    const long cn = min((e - b + size - 1) / size, w.grad_chunks - c0);
+    const int cn = min(chunks_of(e - b, z.grad_bits), (int)w.grad_chunks - c0);
     double dots = 0.0, squares = 0.0;
-    for (long i = threadIdx.x; i < cn; i += kThreads) {
-        dots += w.sum_part[2 * (c0 + i)];
-        squares += w.sum_part[2 * (c0 + i) + 1];
+    for (int i = threadIdx.x; i < cn; i += kThreads) {
+        dots += w.sum_part[2l * (c0 + i)];
+        squares += w.sum_part[2l * (c0 + i) + 1];
     }
     const double v = group_sums<kThreads>(dots, squares, room);
     if (threadIdx.x < 2) {
@@ -409,8 +428,9 @@ __global__ __launch_bounds__(kCounters) void balance_small_kernel(BalanceArgs a)
         fill_rows<T, kCounters>(a, g - a.G);
         return;
     }
-    const long first = a.offsets ? clamp_row(a.offsets[g], a.T) : 0;
-    const long last = a.offsets ? max(clamp_row(a.offsets[g + 1], a.T), first) : a.T;
+    const int first = a.offsets ? clamp_row(a.offsets[g], a.T) : 0;
+    const int last = a.offsets ? max(clamp_row(a.offsets[g + 1], a.T), first) : a.T;
+    GroupRows<T, kCounters, R, Wide> rows(a, first, last);
     int *count = dyn;
     float *f1 = (float *)(dyn + E + 2);
     for (int e = threadIdx.x; e < E + 2; e += kCounters)
@@ -426,19 +446,18 @@ __global__ __launch_bounds__(kCounters) void balance_small_kernel(BalanceArgs a)
     }
     __syncthreads();
     double dots = 0.0, squares = 0.0;
-    group_rows<T, kCounters, R, Wide>(a, first, last, f1, n, dots, squares);
+    rows.run(f1, n, dots, squares);
     const double v = group_sums<kCounters>(dots, squares, room);
     if (threadIdx.x < 2)
         (threadIdx.x ? a.zloss : a.loss)[g] = n ? (float)(v / (double)n) : 0.f;
 }
 
-// Rows of a chunk: 64 chunks or more to count, about 1024 work-groups for the rest.
-long count_size(int T) { return std::max(256l, ((long)T + 63) / 64); }
-long grad_size(int T)
+// 64 to 128 chunks to count and 1024 to 2048 for the rest, where there are rows
+// enough for at least 256 and 16 a chunk.
+Sizes sizes_of(int T)
 {
-    const long pass = kThreads / kLanes;   // rows a work-group takes at once
-    const long want = ((long)T + 1023) / 1024;
-    return std::max(1l, (want + pass - 1) / pass) * pass;
+    auto bits = [](int v) { return 31 - __builtin_clz((unsigned)v); };
+    return Sizes{std::max(8, bits(T / 64 + 1)), std::max(4, bits(T / 1024 + 1))};
 }
 
 // One work-group per group where that is little work even if a single group
@@ -455,7 +474,7 @@ void run(const BalanceArgs &a, const BalanceWs &w, hipStream_t st)
                            room, st, a);
     else
         hipLaunchKernelGGL((balance_kernel<T, R, Wide>), grid_of(w.grad_chunks + fillers),
-                           dim3(kThreads), room, st, a, w, grad_size(a.T), count_size(a.T));
+                           dim3(kThreads), room, st, a, w, sizes_of(a.T));
 }
 
 template <typename T, int R>
@@ -490,22 +509,23 @@ template <typename T> void run_rows(const BalanceArgs &a, const BalanceWs &w, hi
 
 }  // namespace
 
-long balance_count_chunks(int T, int G) { return T / count_size(T) + G; }
-long balance_grad_chunks(int T, int G) { return T / grad_size(T) + G; }
+// at most one chunk of a group is not full
+long balance_count_chunks(int T, int G) { return (T >> sizes_of(T).count_bits) + (long)G; }
+long balance_grad_chunks(int T, int G) { return (T >> sizes_of(T).grad_bits) + (long)G; }
 
 hipError_t launch_balance(const BalanceArgs &a, const BalanceWs &w, hipStream_t st)
 {
     const bool one = small(a.T, a.E);
     if (!one)
         hipLaunchKernelGGL(count_kernel, grid_of(w.count_chunks), dim3(kCounters),
-                           (size_t)(a.E + 2) * 4, st, a, w, count_size(a.T));
+                           (size_t)(a.E + 2) * 4, st, a, w, sizes_of(a.T));
     if (a.dtype == 1)
         run_rows<uint16_t>(a, w, st);
     else
         run_rows<float>(a, w, st);
     if (!one)
         hipLaunchKernelGGL(balance_sum_kernel, dim3(a.G), dim3(kThreads), 0, st, a, w,
-                           grad_size(a.T));
+                           sizes_of(a.T));
     return hipGetLastError();
 }
 
