@@ -149,7 +149,7 @@ __device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const Lis
         });
         rest = sum_wave(rest) + (float)(wave_sum(tops) - 1);
         r.U = (double)top * a.r.scale + ln_sum(rest);
-        const double over = r.any ? 1.0 / row_sum(top, rest) : 0.0;
+        const double over = r.any ? 1.0 / (1.0 + (double)rest) : 0.0;
         each(l, K, [&](int k, int, float) { l.p[k] *= over; });
         r.C = r.any ? 1.0 : 0.0;
     }

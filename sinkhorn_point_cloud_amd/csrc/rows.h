@@ -284,17 +284,12 @@ __device__ __forceinline__ void merge_group(float &m, float &r, const Scale &c, 
     }
 }
 
-// The rest in fp64.  v_exp_f32 is 3.2e-9 of its value too small on average (5e7
-// arguments, the same over every range): one sign, so that it adds up over the
-// tokens of a sequence, and is put right here.
-__device__ __forceinline__ double rest_of(float R) { return (double)R * (1.0 + 3.2e-9); }
-
 // A row without any probability, and the sum 1 + R in fp64: NaN for a maximum of
 // +inf, whose terms would be differences of infinities.
 __device__ __forceinline__ bool row_empty(float M, float R) { return M == -kInf && R == 0.f; }
 __device__ __forceinline__ double row_sum(float M, float R)
 {
-    return M == kInf ? __builtin_nan("") : 1.0 + rest_of(R);
+    return M == kInf ? __builtin_nan("") : 1.0 + (double)R;
 }
 __device__ __forceinline__ double ln_sum(float R);
 __device__ __forceinline__ double row_ln(float M, float R)
@@ -309,7 +304,7 @@ __device__ __forceinline__ double row_ln(float M, float R)
 // times as long while the row's other waves waited.)
 __device__ __forceinline__ double ln_sum(float R)
 {
-    double e = 0.0, a = rest_of(R), b = 2.0 + a;
+    double e = 0.0, a = (double)R, b = 2.0 + a;
     if (R >= 0.4140625f) {
         const double s = 1.0 + a;
         double m = __builtin_amdgcn_frexp_mant(s);
