@@ -761,3 +761,48 @@ def test_many_routed_rows():
         assert ((d[a:b].cpu().double() - want).abs() <= 2 * (F.eps_sum(E) + 16 * F.U) * size).all()
         assert abs(zloss[i].item() - (lse[a:b] ** 2).mean().item()) <= \
             (2 * F.eps_sum(E) + 8 * F.U) * ((lse[a:b].abs() + 1) ** 2).mean().item()
+
+
+@pytest.mark.parametrize("T,V,n", [(2500, 70, 5), (90, 300, 130), (3001, 33, 2), (2049, 257, 64),
+                                   (2048, 130, 64), (700, 9, 65)])
+@pytest.mark.parametrize("mean", [True, False])
+def test_many_sequences_and_long_ones(T, V, n, mean):
+    """More sequences than lanes and more rows than a row's own work-group looks through, and
+    the last sizes that it does."""
+    g = rng(T + V + n)
+    z, y = make(T, V, torch.float32, g)
+    off = cut(T, n, g, first=3, last=T - 7)
+    lp = F.Rows(z).logp(y)[0]
+    old = (lp + 0.25 * torch.randn(T, generator=g).double()).float().cuda()
+    ref = (lp + 0.3 * torch.randn(T, generator=g).double()).float().cuda()
+    w = torch.rand(n, generator=g).cuda()
+    adv = torch.randn(n, generator=g).cuda()
+    inside = (torch.arange(T) >= 3) & (torch.arange(T) < T - 7)
+    kw = dict(ref=ref, kl=0.1, weights=w, mean=mean)
+    got, want = sk.policy_loss(z, y, off, old, adv, **kw), F.policy(z, y, off, old, adv, **kw)
+    assert want[4][torch.isfinite(want[4])].min() > 1e-6
+    F.check(got[2], (torch.where(inside, want[2][0], 0.0), want[2][1]), "logp")
+    for k, name in ((0, "loss"), (1, "kl"), (3, "dlogits")):
+        F.check(got[k], want[k], name)
+    none = sk.policy_loss(z, y, off, old, adv, grad=False, **kw)
+    assert none[3] is None and all(torch.equal(a, b) for a, b in zip(none[:3], got[:3]))
+    if n % 2:
+        off = off[:-1]
+        n -= 1
+    inside = (torch.arange(T) >= 3) & (torch.arange(T) < int(off[-1]))
+    kw = dict(beta=0.2, smoothing=0.05, weights=w[:n // 2], mean=mean)
+    got, want = sk.preference_loss(z, y, off, ref, **kw), F.preference(z, y, off, ref, **kw)
+    F.check(got[2], (torch.where(inside, want[2][0], 0.0), want[2][1]), "logp of pairs")
+    for k, name in ((0, "loss"), (1, "reward"), (3, "dlogits")):
+        F.check(got[k], want[k], name)
+    none = sk.preference_loss(z, y, off, ref, grad=False, **kw)
+    assert none[3] is None and all(torch.equal(a, b) for a, b in zip(none[:3], got[:3]))
+    over = z.clone()
+    again = sk.preference_loss(over, y, off, ref, out=(*[o.clone() for o in got[:3]], over), **kw)
+    assert torch.equal(again[3][inside.cuda()], got[3][inside.cuda()])
+    assert torch.equal(over[~inside.cuda()], z[~inside.cuda()])
+    over = z.clone()
+    off2 = cut(T, n, g)
+    new = sk.policy_loss(z, y, off2, old, adv[:n], mean=mean)
+    sk.policy_loss(over, y, off2, old, adv[:n], mean=mean, out=(*[o.clone() for o in new[:3]], over))
+    assert torch.equal(over, new[3])
