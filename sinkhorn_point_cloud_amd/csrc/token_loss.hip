@@ -168,16 +168,18 @@ __device__ __forceinline__ float exp_over(float g)
 struct PolicyMode {
     static constexpr bool kGradient = true;
     struct Row {
-        float w, adv;   // row weight and advantage
+        float w, adv, old, ref;   // row weight, advantage, given log-probabilities
     };
-    // Every thread of the work-group, while the row's loads are in flight.
+    // Every thread of the work-group, while the row's loads are in flight: what the
+    // scalar phase needs is there when it begins.
     template <int NT>
     __device__ __forceinline__ static Row begin(const LabelArgs &a, long t, int *room)
     {
         const PolicyArgs &q = a.pol;
+        const float old = q.old[t], ref = q.ref ? q.ref[t] : 0.f;
         if (!a.fold) {
             const float2 info = q.info[t];
-            return Row{info.x, info.y};
+            return Row{info.x, info.y, old, ref};
         }
         const int lane = lane_id(), i = seq_of(a.p, t);
         double w = q.weights ? (double)q.weights[i] : 1.0;
@@ -195,7 +197,7 @@ struct PolicyMode {
             }
             w = n ? w / (double)n : 0.0;
         }
-        return Row{(float)w, q.adv[q.adv_per_token ? t : i]};
+        return Row{(float)w, q.adv[q.adv_per_token ? t : i], old, ref};
     }
     __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &info,
                                                      float M, float R, float zy, bool writes)
@@ -206,7 +208,7 @@ struct PolicyMode {
         const float adv = info.adv;
         const double logp = ((double)zy - (double)M) * s - row_ln(M, R);
         // the clipping decision is taken on the log-ratio, in fp64
-        const double change = logp - (double)q.old[t];
+        const double change = logp - (double)info.old;
         const float ratio = ex2((float)(change * kLog2eD));
         const bool above = adv > 0.f && change > q.log_hi;
         const bool below = adv < 0.f && change < q.log_lo;
@@ -214,7 +216,7 @@ struct PolicyMode {
         double slope = above || below ? 0.0 : -(double)ratio * (double)adv;   // d(-gain)/d logp
         double kl = 0.0, cost = 0.0;
         if (q.ref) {
-            const float gap = (float)((double)q.ref[t] - logp);
+            const float gap = (float)((double)info.ref - logp);
             const float over = exp_over(gap);   // e^gap - 1 - gap
             kl = (double)over;
             if (q.kl != 0.0) {   // only reported else, and it may be infinite
