@@ -165,6 +165,16 @@ __device__ __forceinline__ float exp_over(float g)
     return r * g * g;
 }
 
+// e^x to fp32 precision in the range of fp64: a ratio beyond fp32's range times an
+// advantage of 0 is 0.
+__device__ __forceinline__ double exp_of(double x)
+{
+    double y = x * kLog2eD;
+    y = y > 1100.0 ? 1100.0 : y < -1100.0 ? -1100.0 : y;   // NaN stays
+    const double whole = __builtin_rint(y);
+    return __builtin_amdgcn_ldexp((double)ex2((float)(y - whole)), y == y ? (int)whole : 0);
+}
+
 struct PolicyMode {
     static constexpr bool kGradient = true;
     struct Row {
@@ -209,11 +219,11 @@ struct PolicyMode {
         const double logp = ((double)zy - (double)M) * s - row_ln(M, R);
         // the clipping decision is taken on the log-ratio, in fp64
         const double change = logp - (double)info.old;
-        const float ratio = ex2((float)(change * kLog2eD));
+        const double ratio = exp_of(change);
         const bool above = adv > 0.f && change > q.log_hi;
         const bool below = adv < 0.f && change < q.log_lo;
-        const double gain = (above ? q.hi : below ? q.lo : (double)ratio) * (double)adv;
-        double slope = above || below ? 0.0 : -(double)ratio * (double)adv;   // d(-gain)/d logp
+        const double gain = (above ? q.hi : below ? q.lo : ratio) * (double)adv;
+        double slope = above || below ? 0.0 : -ratio * (double)adv;   // d(-gain)/d logp
         double kl = 0.0, cost = 0.0;
         if (q.ref) {
             const float gap = (float)((double)info.ref - logp);

@@ -806,3 +806,23 @@ def test_many_sequences_and_long_ones(T, V, n, mean):
     new = sk.policy_loss(z, y, off2, old, adv[:n], mean=mean)
     sk.policy_loss(over, y, off2, old, adv[:n], mean=mean, out=(*[o.clone() for o in new[:3]], over))
     assert torch.equal(over, new[3])
+
+
+def test_a_ratio_beyond_fp32():
+    """e^200 is an ordinary number in 64 bits: times an advantage of 0 it is 0, times a small one
+    a number.  The log-probability is off by eps_S, the exponential and two roundings by 2^-23."""
+    g = rng(61)
+    T, V = 6, 900
+    z, y = make(T, V, torch.float32, g)
+    y = y.abs() % V
+    off = torch.tensor([0, 2, 4, 6]).cuda()
+    lp = F.Rows(z).logp(y)[0]
+    old = (lp - torch.tensor([200.0, 200.0, 120.0, 120.0, -200.0, -200.0])).float().cuda()
+    adv = torch.tensor([0.0, -1e-30, 0.0]).cuda()
+    loss, kl, logp, d = sk.policy_loss(z, y, off, old, adv)
+    r = torch.exp(lp - old.cpu().double())
+    want = (r[2] + r[3]) / 2 * float(torch.tensor(1e-30).double())
+    assert loss[0] == 0 and loss[2] == 0 and kl.abs().sum() == 0
+    assert abs(float(loss[1]) / float(want) - 1) < F.eps_sum(V) + 4 * F.U * 2 + F.U * 40
+    assert torch.equal(d[:2], torch.zeros_like(d[:2])) and torch.equal(d[4:], torch.zeros_like(d[4:]))
+    assert torch.isfinite(d).all() and d[2].abs().max() > 0
