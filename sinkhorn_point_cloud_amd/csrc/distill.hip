@@ -168,8 +168,10 @@ __device__ __forceinline__ bool link(const List &l, const Src &src, int K)
 {
     bool twice = false;
     for (int k = lane_id(); k < K; k += kWave) {
+        // without probability: the dense value is the entry's own (a list padded with
+        // one token and -inf is no list of duplicates)
         const int v = l.token[k];
-        const int who = src.owner(v);
+        const int who = l.p[k] != 0.0 ? src.owner(v) : -1;
         if (who >= 0) {
             const int before = atomicExch(&l.head[who], k);
             l.next[k] = before;

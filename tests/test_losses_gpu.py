@@ -826,3 +826,23 @@ def test_a_ratio_beyond_fp32():
     assert abs(float(loss[1]) / float(want) - 1) < F.eps_sum(V) + 4 * F.U * 2 + F.U * 40
     assert torch.equal(d[:2], torch.zeros_like(d[:2])) and torch.equal(d[4:], torch.zeros_like(d[4:]))
     assert torch.isfinite(d).all() and d[2].abs().max() > 0
+
+
+@pytest.mark.parametrize("T,K", [(3, 7), (5, 300)])
+@pytest.mark.parametrize("V", [900, 70001])
+def test_lists_padded_with_a_token(T, K, V):
+    """Padding by a token that the list may hold, its logits -inf, changes nothing but roundings."""
+    g = rng(T + K + V)
+    z, _ = make(T, V, torch.float32, g)
+    idx = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(T)]).int()
+    u = 3 * torch.randn(T, K, generator=g)
+    u[:, K // 2:] = -math.inf
+    idx[:, K // 2:] = 5
+    idx[0, 0] = 5
+    loss, d = sk.distill_loss(z, idx.cuda(), u.cuda(), temperature=1.5)
+    (want, tol), grad = F.distill(z, idx, u, temperature=1.5)
+    F.check(loss, (want, tol), "loss")
+    F.check(d, grad, "dlogits")
+    cut_off = sk.distill_loss(z, idx[:, :K // 2].cuda(), u[:, :K // 2].cuda(), temperature=1.5)
+    F.check(cut_off[0], (want, tol), "loss of the list without padding")
+    F.check(cut_off[1], grad, "dlogits of the list without padding")
