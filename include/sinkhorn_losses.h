@@ -29,7 +29,7 @@
  *     every row output, or get zeros with SK_LOSS_FILL.
  *   - A logit of -inf has no probability (masked vocabulary, disabled expert).
  *     A row of nothing but -inf has no distribution and drops out like a row
- *     that is not scored, except that it stays in the count of a mean.  The
+ *     that is not scored (of a mean's count too where the operation says so).  The
  *     type's lowest finite value is an ordinary number.  NaN or +inf gives NaN.
  *   - The returned losses include their weights, and the gradient is that of
  *     their sum.
@@ -125,7 +125,8 @@ int sinkhorn_policy_loss(const void *logits, int dtype, int64_t ld, const int32_
  * Preference loss of pairs: sequence 2i is the preferred one of pair i and
  * sequence 2i + 1 the other (offsets has 2 pairs + 1 entries).  With
  *     R_j = sum_t (logp_t - ref[t]) over the scored rows of sequence j
- * (ref may be NULL: 0; the mean with SK_LOSS_MEAN), D_i = R_2i - R_2i+1:
+ * (ref may be NULL: 0; with SK_LOSS_MEAN the mean over them, here without the
+ * rows that have no distribution), D_i = R_2i - R_2i+1:
  *     sigmoid: loss[i] = w_i (-(1 - eps) log sigma(beta D) - eps log sigma(-beta D)),
  *     square:  loss[i] = w_i (D - 1 / (2 beta))^2,
  * eps = smoothing in [0, 1], beta > 0, w_i = weights[i] (1 if NULL).

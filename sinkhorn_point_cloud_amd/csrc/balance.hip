@@ -132,7 +132,7 @@ __device__ __forceinline__ void count_rows(const BalanceArgs &a, int first, int 
                 e[j] = k + j < a.K ? idx[k + j] : -1;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                any |= e[j] >= 0 && e[j] < a.E;
+                any |= e[j] >= 0;
                 bad += e[j] >= a.E;
                 if (e[j] >= 0 && e[j] < a.E)
                     atomicAdd(&hist[e[j]], 1);

@@ -846,3 +846,23 @@ def test_lists_padded_with_a_token(T, K, V):
     cut_off = sk.distill_loss(z, idx[:, :K // 2].cuda(), u[:, :K // 2].cuda(), temperature=1.5)
     F.check(cut_off[0], (want, tol), "loss of the list without padding")
     F.check(cut_off[1], grad, "dlogits of the list without padding")
+
+
+@pytest.mark.parametrize("T,E", [(40, 8), (3000, 40)])
+def test_rows_sent_to_no_expert_there_is(T, E):
+    """A row whose one index lies beyond E has an index: it counts in n, and its group has no
+    balance loss."""
+    g = rng(T + E)
+    z, _ = make(T, E, torch.float32, g)
+    idx = torch.randint(0, E, (T, 1), generator=g).int()
+    half = T // 2
+    idx[half:] = E
+    off = torch.tensor([0, half, T]).cuda()
+    loss, zloss, counts, d = sk.balance_loss(z, idx.cuda(), off, balance=0.3, z=0.02)
+    want = F.balance(z, idx, off.cpu(), balance=0.3, z=0.02)
+    assert torch.isnan(loss[1]) and torch.isnan(d[half:]).all() and counts[1].sum() == 0
+    for k, name in ((0, "loss"), (1, "zloss")):
+        F.check((loss, zloss)[k][:1], (want[k][0][:1], want[k][1][:1]), name)
+    F.check(d[:half], (want[3][0][:half], want[3][1][:half]), "dlogits")
+    whole = F.balance(z, idx.clamp(max=E - 1), off.cpu(), balance=0.3, z=0.02)
+    F.check(zloss, whole[1], "zloss of both")
