@@ -50,13 +50,18 @@ __device__ __forceinline__ int chunks_of(int rows, int bits)
 {
     return (rows + (1 << bits) - 1) >> bits;
 }
+// Chunk numbers of group g, which begins at row b: from g + floor(b / size) on.  A
+// group of b to e has floor(e / size) - floor(b / size) + 1 numbers that way, at
+// least as many as it needs, and no sum over the groups before it is formed.
+// Numbers left over are work-groups that end at once.
+__device__ __forceinline__ int chunk0_of(int g, int b, int bits) { return g + (b >> bits); }
 
-// Where a chunk lies: its group, its rows, and the group's chunks of either kind.
+// Where a chunk lies: its group and rows, and the group's chunks of either kind.
 struct Place {
     int group;                  // -1: no such chunk
     int first, last;            // rows of the chunk
     int count0, counts;         // the group's first counting chunk and how many it has
-    int grad0;                  // its first gradient chunk
+    bool leads;                 // the group's first chunk
 };
 
 __device__ __forceinline__ int clamp_row(int64_t v, int T)
@@ -64,55 +69,42 @@ __device__ __forceinline__ int clamp_row(int64_t v, int T)
     return (int)min(max(v, (int64_t)0), (int64_t)T);
 }
 
-__device__ __forceinline__ int upto_lane(int v)   // inclusive sum over the lanes
-{
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int o = __shfl_up(v, d, kWave);
-        if (lane_id() >= d)
-            v += o;
-    }
-    return v;
-}
-
 // The place of chunk number `chunk` of the one kind or the other; every lane of
-// the calling wave gets the answer.
-template <bool Grad> __device__ Place place_of(const BalanceArgs &a, const Sizes &z, long chunk)
+// the calling wave gets the answer.  The group is the last that begins at or
+// before the chunk: each round of the search asks for 64 groups at equal
+// distances, so 64 groups take one and 2^20 four.
+template <bool Grad> __device__ Place place_of(const BalanceArgs &a, const Sizes &z, int chunk)
 {
     const int T = a.T, bits = Grad ? z.grad_bits : z.count_bits;
-    Place r{-1, 0, 0, 0, 0, 0};
-    if (!a.offsets) {
-        r.counts = chunks_of(T, z.count_bits);
-        if (chunk < chunks_of(T, bits))
-            r.group = 0;
-        r.first = (int)chunk << bits;
-        r.last = min(r.first + (1 << bits), T);
+    Place r{-1, 0, 0, 0, 0, false};
+    int g = 0, b = 0, e = T;
+    if (a.offsets) {
+        for (int count = a.G;;) {
+            const int step = (count + kWave - 1) / kWave, at = g + lane_id() * step;
+            const int row = clamp_row(a.offsets[min(at, a.G)], T);
+            const bool begun = at < g + count && chunk0_of(at, row, bits) <= chunk;
+            const int lane = max((int)__popcll(__ballot(begun)) - 1, 0);
+            g += lane * step;
+            if (step == 1) {
+                b = __shfl(row, lane, kWave);
+                e = lane + 1 < kWave ? __shfl(row, lane + 1, kWave)
+                                     : clamp_row(a.offsets[g + 1], T);
+                e = max(e, b);
+                break;
+            }
+            count = min(step, count - lane * step);
+        }
+    }
+    const int i = chunk - chunk0_of(g, b, bits);
+    // (negative: offsets out of order)
+    if (i < 0 || i >= chunks_of(e - b, bits))
         return r;
-    }
-    int before_c = 0, before_g = 0;
-    for (int base = 0; base < a.G; base += kWave) {
-        const int g = base + lane_id();
-        int b = 0, e = 0;
-        if (g < a.G) {
-            b = clamp_row(a.offsets[g], T);
-            e = max(clamp_row(a.offsets[g + 1], T), b);
-        }
-        const int nc = chunks_of(e - b, z.count_bits), ng = chunks_of(e - b, z.grad_bits);
-        const int uc = before_c + upto_lane(nc), ug = before_g + upto_lane(ng);
-        const unsigned long long hit = __ballot(chunk < (Grad ? ug : uc));
-        if (hit) {
-            const int at = __ffsll(hit) - 1;
-            r.group = base + at;
-            r.counts = __shfl(nc, at, kWave);
-            r.count0 = __shfl(uc - nc, at, kWave);
-            r.grad0 = __shfl(ug - ng, at, kWave);
-            r.first = __shfl(b, at, kWave) + (((int)chunk - (Grad ? r.grad0 : r.count0)) << bits);
-            r.last = min(r.first + (1 << bits), __shfl(e, at, kWave));
-            return r;
-        }
-        before_c = __shfl(uc, kWave - 1, kWave);
-        before_g = __shfl(ug, kWave - 1, kWave);
-    }
+    r.group = g;
+    r.first = b + (i << bits);
+    r.last = min(r.first + (1 << bits), e);
+    r.count0 = chunk0_of(g, b, z.count_bits);
+    r.counts = chunks_of(e - b, z.count_bits);
+    r.leads = i == 0;
     return r;
 }
 
@@ -154,7 +146,7 @@ __global__ __launch_bounds__(kCounters) void count_kernel(BalanceArgs a, Balance
     const long chunk = group_index();
     if (chunk >= w.count_chunks)
         return;
-    const Place at = place_of<false>(a, z, chunk);
+    const Place at = place_of<false>(a, z, (int)chunk);
     if (at.group < 0)
         return;
     for (int e = threadIdx.x; e < a.E + 2; e += kCounters)
@@ -346,7 +338,7 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a, Balanc
             fill_rows<T, kThreads>(a, (int)(chunk - w.grad_chunks));
         return;
     }
-    const Place at = place_of<true>(a, z, chunk);
+    const Place at = place_of<true>(a, z, (int)chunk);
     if (at.group < 0)
         return;
     GroupRows<T, kThreads, R, Wide> rows(a, at.first, at.last);
@@ -372,10 +364,10 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a, Balanc
     const double per = n ? (double)E / ((double)K * (double)n) : 0.0;
     for (int e = threadIdx.x; e < E; e += kThreads) {
         f1[e] = bad ? __builtin_nanf("") : (float)((double)count[e] * per - 1.0);
-        if (chunk == at.grad0)
+        if (at.leads)
             a.counts[(long)at.group * E + e] = count[e];
     }
-    if (chunk == at.grad0 && threadIdx.x == 0)
+    if (at.leads && threadIdx.x == 0)
         w.rows[at.group] = n;
     __syncthreads();
     double dots = 0.0, squares = 0.0;
@@ -390,16 +382,12 @@ __global__ __launch_bounds__(kThreads) void balance_sum_kernel(BalanceArgs a, Ba
 {
     __shared__ double room[2 * kThreads / kWave];
     const int g = blockIdx.x, E = a.E, T = a.T;
-    int b = 0, e = T, c0 = 0;
+    int b = 0, e = T;
     if (a.offsets) {
-        for (int i = lane_id(); i < g; i += kWave) {
-            const int bi = clamp_row(a.offsets[i], T);
-            c0 += chunks_of(max(clamp_row(a.offsets[i + 1], T), bi) - bi, z.grad_bits);
-        }
-        c0 = wave_sum(c0);
         b = clamp_row(a.offsets[g], T);
         e = max(clamp_row(a.offsets[g + 1], T), b);
     }
+    const int c0 = chunk0_of(g, b, z.grad_bits);
     // the cap holds for offsets in order; out of order it keeps the reads in bounds
     const int cn = min(chunks_of(e - b, z.grad_bits), (int)w.grad_chunks - c0);
     double dots = 0.0, squares = 0.0;
@@ -509,7 +497,7 @@ template <typename T> void run_rows(const BalanceArgs &a, const BalanceWs &w, hi
 
 }  // namespace
 
-// at most one chunk of a group is not full
+// chunk numbers go up to the last group's: G - 1 + floor(T / size)
 long balance_count_chunks(int T, int G) { return (T >> sizes_of(T).count_bits) + (long)G; }
 long balance_grad_chunks(int T, int G) { return (T >> sizes_of(T).grad_bits) + (long)G; }
 

@@ -866,3 +866,47 @@ def test_rows_sent_to_no_expert_there_is(T, E):
     F.check(d[:half], (want[3][0][:half], want[3][1][:half]), "dlogits")
     whole = F.balance(z, idx.clamp(max=E - 1), off.cpu(), balance=0.3, z=0.02)
     F.check(zloss, whole[1], "zloss of both")
+
+
+@pytest.mark.parametrize("T,G", [(300007, 1 << 20), (70001, 4097), (20000, 65), (66000, 64)])
+def test_many_groups_of_routed_rows(T, G):
+    """Most of 2^20 groups empty, groups of one row and long ones: each group's counts, losses and
+    gradients against sums over rows in 64 bits."""
+    g = rng(T + G)
+    E, K = 8, 2
+    z = torch.randn(T, E, generator=g)
+    idx = z.topk(K, dim=1).indices.int()
+    idx[::7] = -1
+    cuts = torch.randint(3, T - 5, (G - 1,), generator=g).sort().values
+    cuts[:G // 3] = cuts[G // 3]     # the rows before it are one group
+    off = torch.cat([torch.tensor([3]), cuts, torch.tensor([T - 5])])
+    loss, zloss, counts, d = sk.balance_loss(z.cuda(), idx.cuda(), off.cuda(), balance=0.3, z=0.02)
+    seg = torch.bucketize(torch.arange(T), off[1:], right=True).clamp(max=G - 1)
+    inside = (torch.arange(T) >= 3) & (torch.arange(T) < T - 5)
+    used = inside & (idx[:, 0] >= 0)
+    n = torch.zeros(G, dtype=torch.float64).index_add_(0, seg, used.double())
+    hot = torch.zeros(T, E, dtype=torch.float64).scatter_(1, idx.long().clamp(min=0), 1.0)
+    hot = torch.where(used[:, None], hot, 0.0)
+    want = torch.zeros(G, E, dtype=torch.float64).index_add_(0, seg, hot)
+    assert torch.equal(counts.cpu(), want.int())
+    R = F.Rows(z)
+    over = 1.0 / n.clamp(min=1)
+    f = (want * (E / K) * over[:, None])[seg]
+    dot = (f * R.q).sum(1)
+    sums = lambda v: torch.zeros(G, dtype=torch.float64).index_add_(  # noqa: E731
+        0, seg, torch.where(used, v, 0.0)) * over
+    # as in F.balance: each f - 1 rounded once, p off by q_tol, the row sums by eps_S
+    e = F.eps_sum(E)
+    size = (R.q * (f - 1).abs()).sum(1)
+    off_by = size * (e + 24 * F.U) + E * F.U * size + (R.q_tol * (f - 1).abs()).sum(1)
+    F.check(loss, (sums(dot), sums(off_by) + 4 * F.U * sums(dot)), "loss")
+    lt = e + 4 * F.U * (R.lse.abs() + R.M.abs())
+    F.check(zloss, (sums(R.lse ** 2), sums(2 * R.lse.abs() * lt + lt * lt)
+                    + 4 * F.U * sums(R.lse ** 2)), "zloss")
+    inner = 0.3 * (f - dot[:, None]) + 0.04 * R.lse[:, None]
+    it = 0.3 * (off_by[:, None] + 6 * F.U * ((f - 1).abs() + size[:, None])) \
+        + 0.04 * (lt + 4 * F.U * R.lse.abs())[:, None]
+    k = torch.where(used, over[seg], 0.0)[:, None]
+    grad = R.q * inner * k
+    tol = (R.q * it + (R.q_tol + 6 * F.U * R.q) * (inner.abs() + it)) * k
+    F.check(d, (grad, tol + F.U * (grad.abs() + tol) * 1.01 + 1e-38), "dlogits")
