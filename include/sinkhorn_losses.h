@@ -33,8 +33,8 @@
  *     type's lowest finite value is an ordinary number.  NaN or +inf gives NaN.
  *   - The returned losses include their weights, and the gradient is that of
  *     their sum.
- *   - Softmax sums are fp32; logarithms, ratios, clipping decisions and sums
- *     over rows are fp64.  Each output is rounded once.  Same inputs at the
+ *   - Exponentials are fp32, and so are a thread's sums of them; their joins,
+ *     logarithms, ratios, clipping decisions and sums over rows are fp64.  Each output is rounded once.  Same inputs at the
  *     same addresses modulo 128 bytes, same bits: no result depends on an order
  *     of atomics.
  *   - Every call enqueues kernels only and returns without waiting; it can be

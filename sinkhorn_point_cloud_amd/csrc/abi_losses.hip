@@ -38,7 +38,7 @@ Ws carve(Carve &c, int op, int T, int V, int k, int dtype)
     }
     const int parts = token_parts(T, V, dtype);
     if (parts > 1) {
-        w.token.part = c.take<float2>(rows * parts);
+        w.token.part = c.take<RowPart>(rows * parts);
         if (op == SK_OP_DISTILL_LOSS)
             w.zk = c.take<float>(rows * k);
         else

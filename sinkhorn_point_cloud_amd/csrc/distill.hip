@@ -147,9 +147,9 @@ __device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const Lis
             else
                 rest += e;
         });
-        rest = sum_wave(rest) + (float)(wave_sum(tops) - 1);
-        r.U = (double)top * a.r.scale + ln_sum(rest);
-        const double over = r.any ? 1.0 / (1.0 + (double)rest) : 0.0;
+        const double others = sum_wave((double)rest) + (double)(wave_sum(tops) - 1);
+        r.U = (double)top * a.r.scale + ln_sum(others);
+        const double over = r.any ? 1.0 / (1.0 + others) : 0.0;
         each(l, K, [&](int k, int, float) { l.p[k] *= over; });
         r.C = r.any ? 1.0 : 0.0;
     }
@@ -188,7 +188,7 @@ __device__ __forceinline__ bool link(const List &l, const Src &src, int K)
 // the gradient at the list's tokens, add (C q - p).
 __device__ __forceinline__ RowScalars student_side(const Args &a, long t, const List &l,
                                                    const Teacher &r, bool twice,
-                                                   float M, float R, bool writes)
+                                                   float M, double R, bool writes)
 {
     const int lane = lane_id(), K = a.d.K;
     const double inv = a.r.scale, tau = 1.0 / inv;
@@ -257,7 +257,7 @@ template <typename T, int NT, typename Src>
 __global__ __launch_bounds__(NT, Src::waves) void distill_kernel(Args a)
 {
     extern __shared__ u32x4 chunks[];   // [Src::lds_chunks], then the list
-    __shared__ float2 room[NT / kWave];
+    __shared__ RowPart room[NT / kWave];
     __shared__ RowScalars scal;
     const long t = group_index();
     if (t >= a.r.T)
@@ -292,9 +292,9 @@ __global__ __launch_bounds__(NT, Src::waves) void distill_kernel(Args a)
         if (grad)
             twice = link(l, src, K);
     }
-    float M = -kInf, R = 0.f;
-    src.stats(a.c, M, R);
-    merge_group<NT>(M, R, a.c, room);
+    float M = -kInf, rest = 0.f;
+    src.stats(a.c, M, rest);
+    const double R = merge_group<NT>(M, rest, a.c, room);
     if (threadIdx.x < kWave) {
         const RowScalars k = student_side(a, t, l, r, twice, M, R, true);
         if (threadIdx.x == 0)
@@ -315,7 +315,7 @@ __global__ __launch_bounds__(NT, Src::waves) void distill_kernel(Args a)
 // (the second launch may write its gradient over the logits).
 template <typename T> __global__ __launch_bounds__(kSplit) void distill_part_kernel(Args a)
 {
-    __shared__ float2 room[kSplit / kWave];
+    __shared__ RowPart room[kSplit / kWave];
     const long t = group_index() / a.parts;
     const int part = (int)(group_index() % a.parts), K = a.d.K, V = a.r.V;
     if (t >= a.r.T || dropped(a, t))
@@ -329,9 +329,9 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_part_ker
     Streamed<T, kSplit> src(row, V, part, a.parts);
     float m = -kInf, s = 0.f;
     src.stats(a.c, m, s);
-    merge_group<kSplit>(m, s, a.c, room);
+    const double R = merge_group<kSplit>(m, s, a.c, room);
     if (threadIdx.x == 0)
-        a.w.part[t * a.parts + part] = make_float2(m, s);
+        a.w.part[t * a.parts + part] = RowPart{R, m};
 }
 
 template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_kernel(Args a, int run)
@@ -362,10 +362,8 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
         ahead.list(a, t, l, [&](int k, int) { return a.d.zk[t * K + k]; });
         const Teacher r = teacher_side(a, t, l);
         const bool twice = grad && link(l, src, K);
-        const float2 p = lane_id() < a.parts ? a.w.part[t * a.parts + lane_id()]
-                                             : make_float2(-kInf, 0.f);
-        float M = p.x, R = p.y;
-        merge_wave(M, R, a.c);
+        float M;
+        const double R = merge_parts(a.w.part + t * a.parts, a.parts, a.c, M);
         const RowScalars k = student_side(a, t, l, r, twice, M, R, part == 0);
         if (threadIdx.x == 0)
             scal = k;
@@ -403,7 +401,9 @@ template <typename T> void launch_rows(const Args &a, hipStream_t st)
     }
     const RunRows<T> run{a, st};
     // without a gradient too: the loss is then the same to the bit
-    with_source<T>(a.r.V, list_bytes(1024, a.d.K), run);
+    // up to 256 rows have a compute unit each (128 of 64 KB with 20 entries: 10.8 us at
+    // 64 registers a thread, 9.0 at 128)
+    with_source<T>(a.r.V, list_bytes(1024, a.d.K), a.r.T <= 256, run);
 }
 
 }  // namespace

@@ -25,6 +25,7 @@
 #pragma once
 
 #include "common.h"
+#include "token_loss.h"
 
 #include <algorithm>
 #include <math.h>
@@ -255,44 +256,99 @@ __device__ __forceinline__ void absorb(const float (&x)[K], const Scale &k, floa
     m = mn;
 }
 
-// (M, R) of a wave, the same in all its lanes.
-__device__ __forceinline__ void merge_wave(float &m, float &r, const Scale &c)
+// (M, R) of a wave from its lanes' own, the same in all of them.  Where many waves
+// share a row, sums of 16 lanes are fp32, whose roundings average out; the last
+// joins, whose would not, are fp64 here and below.
+template <bool Alone>
+__device__ __forceinline__ double merge_wave(float &m, float r, const Scale &c)
 {
     const float top = max_wave(m), at = shift_of(top);
     const float f = c.pow(m - at);
     // the first lane that has the maximum leaves its 1 out, every other counts
     const bool holds = __ffsll(__ballot(m == top)) - 1 == lane_id();
-    r = sum_wave(holds ? r : fmaf(r, f, f));
     m = top;
+    r = holds ? r : fmaf(r, f, f);
+    if constexpr (Alone)
+        return sum_wave((double)r);
+    r = row16_sum(r);
+    return ((double)read_lane(r, 0) + (double)read_lane(r, 16)) +
+           ((double)read_lane(r, 32) + (double)read_lane(r, 48));
 }
 
-// (M, R) of the whole work-group in every thread.  `room`: one entry per wave.
+// 2^((m - M) c) to 1e-10 of itself: the hardware's exponential, off by up to 2^-23,
+// would be most of the error of a sum of few parts.
+__device__ __forceinline__ double pow_fine(float d, const Scale &c)
+{
+    double y = (double)d * ((double)c.hi + (double)c.lo);
+    y = y < -1100.0 ? -1100.0 : y;   // NaN stays
+    const double whole = __builtin_rint(y), g = (y - whole) * kLn2D;   // |g| <= 0.347
+    double p = 1.0 / 40320;
+    p = fma(p, g, 1.0 / 5040);
+    p = fma(p, g, 1.0 / 720);
+    p = fma(p, g, 1.0 / 120);
+    p = fma(p, g, 1.0 / 24);
+    p = fma(p, g, 1.0 / 6);
+    p = fma(p, g, 0.5);
+    p = fma(p, g, 1.0);
+    return __builtin_amdgcn_ldexp(fma(p, g, 1.0), y == y ? (int)whole : 0);
+}
+
+// (M, R) from those of up to 64 parts, one to a lane (Lanes: 16, where there are no
+// more, in the first lanes).  One wave; every lane gets the result.  (With fp32
+// exponentials and sums here a log-probability was off by 5e-8 to 1e-7, the square
+// loss of a pair, a small difference of sums, by up to 1e-6 of itself.)
+template <int Lanes> __device__ __forceinline__ double merge_parts(float &m, double r, const Scale &c)
+{
+    const float top = max_wave(m), at = shift_of(top);
+    const double f = pow_fine(m - at, c);
+    const bool holds = __ffsll(__ballot(m == top)) - 1 == lane_id();
+    m = top;
+    r = holds ? r : fma(r, f, f);
+    if constexpr (Lanes > 16)
+        return sum_wave(r);
+    r += dpp_move<kDppXor1>(r);
+    r += dpp_move<kDppXor2>(r);
+    r += dpp_move<kDppHalfMirror>(r);
+    r += dpp_move<kDppMirror>(r);
+    return read_lane(r, 0);
+}
+__device__ __forceinline__ double merge_parts(const RowPart *part, int parts, const Scale &c, float &M)
+{
+    const RowPart p = lane_id() < parts ? part[lane_id()] : RowPart{0.0, -kInf};
+    M = p.m;
+    return merge_parts<kWave>(M, p.r, c);
+}
+
+// (M, R) of the whole work-group, in its first wave.  `room`: one entry per wave.
 // One barrier; `room` may be written again only behind another one.
 template <int NT>
-__device__ __forceinline__ void merge_group(float &m, float &r, const Scale &c, float2 *room)
+__device__ __forceinline__ double merge_group(float &m, float r, const Scale &c, RowPart *room)
 {
-    merge_wave(m, r, c);
+    double R = merge_wave<NT == kWave>(m, r, c);
     if constexpr (NT > kWave) {
         constexpr int waves = NT / kWave;
+        static_assert(waves <= 16);
         if (lane_id() == 0)
-            room[threadIdx.x / kWave] = make_float2(m, r);
+            room[threadIdx.x / kWave] = RowPart{R, m};
         __syncthreads();
-        const float2 v = lane_id() < waves ? room[lane_id()] : make_float2(-kInf, 0.f);
-        m = v.x;
-        r = v.y;
-        merge_wave(m, r, c);
+        if (threadIdx.x < kWave) {
+            const RowPart v = lane_id() < waves ? room[lane_id()] : RowPart{0.0, -kInf};
+            m = v.m;
+            R = merge_parts<16>(m, v.r, c);
+        }
     }
+    return R;
 }
 
 // A row without any probability, and the sum 1 + R in fp64: NaN for a maximum of
 // +inf, whose terms would be differences of infinities.
-__device__ __forceinline__ bool row_empty(float M, float R) { return M == -kInf && R == 0.f; }
-__device__ __forceinline__ double row_sum(float M, float R)
+__device__ __forceinline__ bool row_empty(float M, double R) { return M == -kInf && R == 0.0; }
+__device__ __forceinline__ double row_sum(float M, double R)
 {
-    return M == kInf ? __builtin_nan("") : 1.0 + (double)R;
+    return M == kInf ? __builtin_nan("") : 1.0 + R;
 }
-__device__ __forceinline__ double ln_sum(float R);
-__device__ __forceinline__ double row_ln(float M, float R)
+__device__ __forceinline__ double ln_sum(double R);
+__device__ __forceinline__ double row_ln(float M, double R)
 {
     return M == kInf ? __builtin_nan("") : ln_sum(R);
 }
@@ -302,10 +358,10 @@ __device__ __forceinline__ double row_ln(float M, float R)
 // (m + 1).  |t| <= 0.172: the first term left out, t^17/17, is below 2^-47 t.
 // (The library's logarithm, with its tables of extra precision, took several
 // times as long while the row's other waves waited.)
-__device__ __forceinline__ double ln_sum(float R)
+__device__ __forceinline__ double ln_sum(double R)
 {
-    double e = 0.0, a = (double)R, b = 2.0 + a;
-    if (R >= 0.4140625f) {
+    double e = 0.0, a = R, b = 2.0 + a;
+    if (R >= 0.4140625) {
         const double s = 1.0 + a;
         double m = __builtin_amdgcn_frexp_mant(s);
         int k = __builtin_amdgcn_frexp_exp(s);
@@ -590,7 +646,9 @@ template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
 // memory, and 464 KB with 20 and 9; longer rows are read twice beyond that.
 // `taken`: bytes of shared memory that the caller needs itself; where they leave
 // no room for chunks, a long row is read twice as a whole.
-template <typename T, typename F> void with_source(int len, size_t taken, F &&f)
+// `alone`: no two rows will share a compute unit, and the caller's own work would
+// spill registers beside 8 chunks a thread at 64.
+template <typename T, typename F> void with_source(int len, size_t taken, bool alone, F &&f)
 {
     const long chunks = (long)len * (long)sizeof(T) / 16;
     const bool room = taken + 9 * 1024 * 16 <= (160u << 10) - 512;
@@ -602,9 +660,9 @@ template <typename T, typename F> void with_source(int len, size_t taken, F &&f)
         f.template operator()<256, Held<T, 256, 4>>();
     else if (chunks <= 2048)
         f.template operator()<256, Held<T, 256, 8>>();
-    else if (chunks <= 4096)
+    else if (chunks <= 4096 && !alone)
         f.template operator()<512, Held<T, 512, 8>>();
-    else if (chunks <= 8192)
+    else if (chunks <= 8192 && !alone)
         f.template operator()<1024, Held<T, 1024, 8>>();
     else if (chunks <= 16384)
         f.template operator()<1024, Held<T, 1024, 16>>();

@@ -29,9 +29,15 @@ int token_parts(int T, int V, int dtype);
 // work-groups a row's gradient is dealt to where the statistics are known
 int grad_parts(int T, int V, int dtype);
 
+// (maximum, rest) of a part of a row: of a wave, or of a work-group.
+struct RowPart {
+    double r;
+    float m;
+};
+
 struct TokenWs {
-    float2 *part;   // [T][parts] partial (maximum, rest); parts > 1 only
-    float *zlab;    // [T] label's logit; parts > 1 only
+    RowPart *part;   // [T][parts] the parts' (maximum, rest); parts > 1 only
+    float *zlab;     // [T] label's logit; parts > 1 only
 };
 
 // What a row's statistics leave for a later pass: its maximum, the rest of its

@@ -85,7 +85,7 @@ __device__ __forceinline__ RowState row_state(const LabelArgs &a, long t, int la
 
 // add (1[v = label] - q_v).  A NaN log-probability (a label beyond the row)
 // makes the whole row NaN.
-__device__ __forceinline__ RowScalars coefficients(double add, double logp, float M, float R)
+__device__ __forceinline__ RowScalars coefficients(double add, double logp, float M, double R)
 {
     const float own = (float)-add * expm1_of((float)logp);
     const float A = logp == logp ? (float)(-add / row_sum(M, R)) : __builtin_nanf("");
@@ -101,7 +101,7 @@ struct LogpMode {
         return Row{};
     }
     __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &,
-                                                     float M, float R, float zy, bool writes)
+                                                     float M, double R, float zy, bool writes)
     {
         const double lnS = row_ln(M, R), s = a.r.scale;
         const bool none = row_empty(M, R);
@@ -111,7 +111,7 @@ struct LogpMode {
             if (a.out.lse)
                 a.out.lse[t] = none ? -kInf : (float)((double)M * s + lnS);
             if (a.out.stat)
-                a.out.stat[t] = RowStat{M, R, none ? 0.0 : ((double)zy - (double)M) * s - lnS};
+                a.out.stat[t] = RowStat{M, (float)R, none ? 0.0 : ((double)zy - (double)M) * s - lnS};
         }
         return RowScalars{0.f, 0.f, 0.f, 1};
     }
@@ -136,7 +136,7 @@ struct BackwardMode {
         return Row{};
     }
     __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &,
-                                                     float M, float R, float zy, bool)
+                                                     float M, double R, float zy, bool)
     {
         const double logp = ((double)zy - (double)M) * a.r.scale - row_ln(M, R);
         return coefficients((double)a.G[t] * a.r.scale, logp, M, R);
@@ -210,7 +210,7 @@ struct PolicyMode {
         return Row{(float)w, q.adv[q.adv_per_token ? t : i], old, ref};
     }
     __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &info,
-                                                     float M, float R, float zy, bool writes)
+                                                     float M, double R, float zy, bool writes)
     {
         const PolicyArgs &q = a.pol;
         const bool none = row_empty(M, R);
@@ -256,7 +256,7 @@ template <typename T, int NT, typename Src, typename Mode>
 __global__ __launch_bounds__(NT, Src::waves) void row_kernel(LabelArgs a)
 {
     extern __shared__ u32x4 chunks[];   // [Src::lds_chunks]
-    __shared__ float2 room[NT / kWave];
+    __shared__ RowPart room[NT / kWave];
     __shared__ int count[NT / kWave];
     __shared__ RowScalars scal;
     const long t = group_index();
@@ -281,9 +281,9 @@ __global__ __launch_bounds__(NT, Src::waves) void row_kernel(LabelArgs a)
     const float zy = label < V ? Pack<T>::get(row + label) : __builtin_nanf("");
     src.load();
     const typename Mode::Row info = Mode::template begin<NT>(a, t, count);
-    float M = -kInf, R = 0.f;
-    src.stats(a.c, M, R);
-    merge_group<NT>(M, R, a.c, room);
+    float M = -kInf, r = 0.f;
+    src.stats(a.c, M, r);
+    const double R = merge_group<NT>(M, r, a.c, room);
     if (threadIdx.x < kWave) {
         const RowScalars k = Mode::row(a, t, info, M, R, zy, true);
         if (threadIdx.x == 0)
@@ -302,7 +302,7 @@ __global__ __launch_bounds__(NT, Src::waves) void row_kernel(LabelArgs a)
 // Few rows: each over `parts` work-groups.  First launch: partial statistics.
 template <typename T> __global__ __launch_bounds__(kSplit) void part_kernel(LabelArgs a)
 {
-    __shared__ float2 room[kSplit / kWave];
+    __shared__ RowPart room[kSplit / kWave];
     const long t = group_index() / a.parts;
     const int part = (int)(group_index() % a.parts);
     if (t >= a.r.T)
@@ -314,22 +314,12 @@ template <typename T> __global__ __launch_bounds__(kSplit) void part_kernel(Labe
     Streamed<T, kSplit> src(row, a.r.V, part, a.parts);
     float m = -kInf, s = 0.f;
     src.stats(a.c, m, s);
-    merge_group<kSplit>(m, s, a.c, room);
+    const double R = merge_group<kSplit>(m, s, a.c, room);
     if (threadIdx.x == 0) {
-        a.w.part[t * a.parts + part] = make_float2(m, s);
+        a.w.part[t * a.parts + part] = RowPart{R, m};
         if (part == 0)
             a.w.zlab[t] = label < a.r.V ? Pack<T>::get(row + label) : __builtin_nanf("");
     }
-}
-
-// (M, R) of a row from its partial ones, one to a lane.
-__device__ __forceinline__ void merge_parts(const float2 *part, int parts, const Scale &c, float &M,
-                                            float &R)
-{
-    const float2 p = lane_id() < parts ? part[lane_id()] : make_float2(-kInf, 0.f);
-    M = p.x;
-    R = p.y;
-    merge_wave(M, R, c);
 }
 
 // Second launch: the merged statistics, the scalars (by every part for itself)
@@ -359,8 +349,8 @@ __global__ __launch_bounds__(kSplit) void join_kernel(LabelArgs a, int run)
     const float zy = a.w.zlab[t];
     const typename Mode::Row info = Mode::template begin<kSplit>(a, t, count);
     if (threadIdx.x < kWave) {
-        float M, R;
-        merge_parts(a.w.part + t * a.parts, a.parts, a.c, M, R);
+        float M;
+        const double R = merge_parts(a.w.part + t * a.parts, a.parts, a.c, M);
         const RowScalars k = Mode::row(a, t, info, M, R, zy, part == 0);
         if (threadIdx.x == 0)
             scal = k;
@@ -597,7 +587,7 @@ template <typename T, typename Mode> void launch_rows(const LabelArgs &a, hipStr
     const RunRows<T, Mode> run{a, st};
     // a loss keeps its launch shape without a gradient: the same to the bit
     if constexpr (Mode::kGradient)
-        with_source<T>(a.r.V, 0, run);
+        with_source<T>(a.r.V, 0, false, run);
     else
         with_stream<T>(a.r.V, a.r.T, run);
 }
