@@ -910,3 +910,10 @@ def test_many_groups_of_routed_rows(T, G):
     grad = R.q * inner * k
     tol = (R.q * it + (R.q_tol + 6 * F.U * R.q) * (inner.abs() + it)) * k
     F.check(d, (grad, tol + F.U * (grad.abs() + tol) * 1.01 + 1e-38), "dlogits")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("T,V", [(256, 9001), (257, 9001), (258, 17011), (259, 30011), (260, 60013)])
+def test_distill_of_more_rows_than_compute_units(T, V, dt):
+    """Up to 256 rows take more registers each than longer batches do."""
+    test_distill_loss(T, V, dt)
