@@ -37,8 +37,10 @@ using rows::grid_of;
 using rows::group_index;
 
 constexpr int kThreads = 256;    // a chunk's work-group
-constexpr int kCounters = 1024;  // a counting work-group, and a small group's
+constexpr int kCounters = 512;   // a counting work-group
+constexpr int kSmall = 1024;     // a small group's
 constexpr int kLanes = 16;       // lanes of a row
+constexpr int kBatch = 16;       // partial counts a thread asks for at once
 constexpr int kFillers = 64;     // work-groups that zero the rows outside every group
 
 // How rows are cut into chunks: 2^count_bits of them to count, 2^grad_bits for the
@@ -352,12 +354,37 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a, Balanc
     const int c0 = at.count0, cn = min(at.counts, (int)w.count_chunks - c0);
     __syncthreads();
     const int32_t *part = w.count_part + (long)c0 * (E + 2);
-    for (int e = lane_id(); e < E + 2; e += kWave) {
-        int c = 0;
+    const int total = cn * (E + 2);
+    if (total <= kBatch * kThreads) {
+        // few: as one run, all of a thread's loads in flight together (256 experts, 65536
+        // rows in 24 groups: 22.1 -> 20.5 us; 8192 rows in 4: 9.1 -> 7.0)
+        int c[kBatch], e = threadIdx.x % (E + 2);
+        const int turn = kThreads % (E + 2);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = threadIdx.x + j * kThreads;
+            c[j] = 0;
+            if (j * kThreads < total && i < total)   // the first the same for all: a branch
+                c[j] = part[i];
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (j * kThreads < total) {
+                if (c[j])
+                    atomicAdd(&count[e], c[j]);
+                e += turn;
+                e -= e >= E + 2 ? E + 2 : 0;
+            }
+    } else {
+        // many: a column of a wave's chunks to a lane (one group of 64 experts, 64
+        // chunks: 6.4 us, as one run 7.4)
+        for (int e = lane_id(); e < E + 2; e += kWave) {
+            int c = 0;
 #pragma unroll 8
-        for (int i = threadIdx.x / kWave; i < cn; i += kThreads / kWave)
-            c += part[(long)i * (E + 2) + e];
-        atomicAdd(&count[e], c);
+            for (int i = threadIdx.x / kWave; i < cn; i += kThreads / kWave)
+                c += part[(long)i * (E + 2) + e];
+            atomicAdd(&count[e], c);
+        }
     }
     __syncthreads();
     const int n = count[E], bad = count[E + 1];
@@ -407,45 +434,46 @@ __global__ __launch_bounds__(kThreads) void balance_sum_kernel(BalanceArgs a, Ba
 
 // A small group as a whole.
 template <typename T, int R, bool Wide>
-__global__ __launch_bounds__(kCounters) void balance_small_kernel(BalanceArgs a)
+__global__ __launch_bounds__(kSmall) void balance_small_kernel(BalanceArgs a)
 {
     extern __shared__ int dyn[];   // [E + 2] counts, [E] f - 1
-    __shared__ double room[2 * kCounters / kWave];
+    __shared__ double room[2 * kSmall / kWave];
     const int g = blockIdx.x, E = a.E;
     if (g >= a.G) {
-        fill_rows<T, kCounters>(a, g - a.G);
+        fill_rows<T, kSmall>(a, g - a.G);
         return;
     }
     const int first = a.offsets ? clamp_row(a.offsets[g], a.T) : 0;
     const int last = a.offsets ? max(clamp_row(a.offsets[g + 1], a.T), first) : a.T;
-    GroupRows<T, kCounters, R, Wide> rows(a, first, last);
+    GroupRows<T, kSmall, R, Wide> rows(a, first, last);
     int *count = dyn;
     float *f1 = (float *)(dyn + E + 2);
-    for (int e = threadIdx.x; e < E + 2; e += kCounters)
+    for (int e = threadIdx.x; e < E + 2; e += kSmall)
         count[e] = 0;
     __syncthreads();
-    count_rows<kCounters>(a, first, last, count);
+    count_rows<kSmall>(a, first, last, count);
     __syncthreads();
     const int n = count[E], bad = count[E + 1];
     const double per = n ? (double)E / ((double)a.K * (double)n) : 0.0;
-    for (int e = threadIdx.x; e < E; e += kCounters) {
+    for (int e = threadIdx.x; e < E; e += kSmall) {
         f1[e] = bad ? __builtin_nanf("") : (float)((double)count[e] * per - 1.0);
         a.counts[(long)g * E + e] = count[e];
     }
     __syncthreads();
     double dots = 0.0, squares = 0.0;
     rows.run(f1, n, dots, squares);
-    const double v = group_sums<kCounters>(dots, squares, room);
+    const double v = group_sums<kSmall>(dots, squares, room);
     if (threadIdx.x < 2)
         (threadIdx.x ? a.zloss : a.loss)[g] = n ? (float)(v / (double)n) : 0.f;
 }
 
-// 64 to 128 chunks to count and 1024 to 2048 for the rest, where there are rows
-// enough for at least 256 and 16 a chunk.
+// 128 to 256 chunks to count (64 to 128 of twice the threads took 7.0 us for 65536 x 8
+// choices, these 5.3) and 1024 to 2048 for the rest, where there are rows enough for
+// at least 256 and 16 a chunk.
 Sizes sizes_of(int T)
 {
     auto bits = [](int v) { return 31 - __builtin_clz((unsigned)v); };
-    return Sizes{std::max(8, bits(T / 64 + 1)), std::max(4, bits(T / 1024 + 1))};
+    return Sizes{std::max(8, bits(T / 128 + 1)), std::max(4, bits(T / 1024 + 1))};
 }
 
 // One work-group per group where that is little work even if a single group
@@ -458,7 +486,7 @@ void run(const BalanceArgs &a, const BalanceWs &w, hipStream_t st)
     const int fillers = a.fill && a.offsets && a.dlogits ? kFillers : 0;
     const size_t room = (size_t)(2 * a.E + 2) * 4;
     if (small(a.T, a.E))
-        hipLaunchKernelGGL((balance_small_kernel<T, R, Wide>), dim3(a.G + fillers), dim3(kCounters),
+        hipLaunchKernelGGL((balance_small_kernel<T, R, Wide>), dim3(a.G + fillers), dim3(kSmall),
                            room, st, a);
     else
         hipLaunchKernelGGL((balance_kernel<T, R, Wide>), grid_of(w.grad_chunks + fillers),
