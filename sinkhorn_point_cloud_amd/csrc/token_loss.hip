@@ -705,7 +705,7 @@ hipError_t launch_preference(const LogitRows &r, const int32_t *labels, const Pa
     } else {
         hipLaunchKernelGGL(preference_kernel, dim3(p.n / 2), dim3(kSeqThreads), 0, st, labels, p,
                            (long)r.T, q);
-        if (r.dlogits)
+        if (r.dlogits && r.T > 0)   // without rows there is no grid to launch
             run_pairs<false>(a, st);
     }
     return hipGetLastError();

@@ -4,6 +4,8 @@ import ctypes
 import math
 import os
 import re
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -131,6 +133,28 @@ def test_no_rows_need_no_row_pointers(lib):
     for name in ("token_logprobs", "distill_loss"):
         assert _call(lib, name, none) == sk.SK_OK, lib.sinkhorn_last_error()
     assert _call(lib, "token_logprobs_backward", dict(none, grad=None)) == sk.SK_OK
+
+
+@pytest.mark.parametrize("n", [2, 40])
+def test_no_rows_with_a_gradient_buffer(n):
+    """Any number of sequences without rows, a gradient buffer given: a launch on no device is an
+    error (5), and the process lives."""
+    program = f"""
+import ctypes
+import sinkhorn_point_cloud_amd as sk
+lib, P = sk.load_library(), ctypes.c_void_p(4096)
+F = [ctypes.c_void_p(4096 * (k + 2)) for k in range(4)]
+tail = (P, 1 << 40, None)
+print(lib.sinkhorn_policy_loss(None, 0, 16, None, 0, 16, P, {n}, None, None, None, None, 1.0, 0.2,
+                               0.2, 0.0, 0, F[0], F[1], None, F[2], 16, *tail),
+      lib.sinkhorn_preference_loss(None, 0, 16, None, 0, 16, P, {n}, None, None, 1.0, 0, 0.1, 0.0, 0,
+                                   F[0], F[1], None, F[2], 16, *tail),
+      lib.sinkhorn_balance_loss(None, 0, 16, 0, 16, None, 2, P, {n}, 1.0, 0.0, 0, F[0], F[1], F[2],
+                                F[3], 16, *tail))
+"""
+    run = subprocess.run([sys.executable, "-c", program], cwd=ROOT, capture_output=True, text=True,
+                         env=dict(os.environ, HIP_VISIBLE_DEVICES="-1"))
+    assert run.returncode == 0 and run.stdout.split() == ["5", "5", "5"], run
 
 
 def test_binding_refusals():
