@@ -275,12 +275,11 @@ __device__ __forceinline__ double merge_wave(float &m, float r, const Scale &c)
            ((double)read_lane(r, 32) + (double)read_lane(r, 48));
 }
 
-// 2^((m - M) c) to 1e-10 of itself: the hardware's exponential, off by up to 2^-23,
-// would be most of the error of a sum of few parts.
-__device__ __forceinline__ double pow_fine(float d, const Scale &c)
+// 2^y in the range of fp64, off by less than 3e-10 of itself (the first term left
+// out, g^9/9!); NaN stays.
+__device__ __forceinline__ double exp2_fine(double y)
 {
-    double y = (double)d * ((double)c.hi + (double)c.lo);
-    y = y < -1100.0 ? -1100.0 : y;   // NaN stays
+    y = y < -1100.0 ? -1100.0 : y > 1100.0 ? 1100.0 : y;
     const double whole = __builtin_rint(y), g = (y - whole) * kLn2D;   // |g| <= 0.347
     double p = 1.0 / 40320;
     p = fma(p, g, 1.0 / 5040);
@@ -291,6 +290,13 @@ __device__ __forceinline__ double pow_fine(float d, const Scale &c)
     p = fma(p, g, 0.5);
     p = fma(p, g, 1.0);
     return __builtin_amdgcn_ldexp(fma(p, g, 1.0), y == y ? (int)whole : 0);
+}
+
+// 2^((m - M) c) in fp64: the hardware's exponential, off by up to 2^-23, would be
+// most of the error of a sum of few parts.
+__device__ __forceinline__ double pow_fine(float d, const Scale &c)
+{
+    return exp2_fine((double)d * ((double)c.hi + (double)c.lo));
 }
 
 // (M, R) from those of up to 64 parts, one to a lane (Lanes: 16, where there are no

@@ -144,25 +144,32 @@ struct BackwardMode {
     __device__ __forceinline__ static void unused(const LabelArgs &, long) {}
 };
 
-// e^g - 1 - g to fp32 precision: the series where the difference would cancel
-// (|g| < 1: the first term left out, g^12/12!, is below 2^-27 of the value)
-__device__ __forceinline__ float exp_over(float g)
+// The KL term e^g - 1 - g and its slope e^g - 1, in fp64 and its range: the term is a
+// multiple of e^g for a label that the reference finds likely, and after weights it
+// may be an ordinary number where e^g is beyond fp32.  Near 0 the series, where the
+// difference would cancel (|g| < 1: the first term left out, g^12/12!, is below
+// 2^-27 of the value).
+struct KlTerm {
+    double over, slope;
+};
+__device__ __forceinline__ KlTerm kl_term(double g)
 {
-    if (!(fabsf(g) < 1.f)) {
-        const float e = ex2(g * kLog2e);
-        return e == kInf ? e : e - 1.f - g;   // a label of probability 0: infinite
+    if (!(fabs(g) < 1.0)) {
+        const double e = exp2_fine(g * kLog2eD);
+        return KlTerm{e == (double)kInf ? e : e - 1.0 - g, e - 1.0};   // a label of probability 0
     }
-    float r = 1.f / 39916800.f;
-    r = fmaf(r, g, 1.f / 3628800.f);
-    r = fmaf(r, g, 1.f / 362880.f);
-    r = fmaf(r, g, 1.f / 40320.f);
-    r = fmaf(r, g, 1.f / 5040.f);
-    r = fmaf(r, g, 1.f / 720.f);
-    r = fmaf(r, g, 1.f / 120.f);
-    r = fmaf(r, g, 1.f / 24.f);
-    r = fmaf(r, g, 1.f / 6.f);
-    r = fmaf(r, g, 0.5f);
-    return r * g * g;
+    double r = 1.0 / 39916800.0;
+    r = fma(r, g, 1.0 / 3628800.0);
+    r = fma(r, g, 1.0 / 362880.0);
+    r = fma(r, g, 1.0 / 40320.0);
+    r = fma(r, g, 1.0 / 5040.0);
+    r = fma(r, g, 1.0 / 720.0);
+    r = fma(r, g, 1.0 / 120.0);
+    r = fma(r, g, 1.0 / 24.0);
+    r = fma(r, g, 1.0 / 6.0);
+    r = fma(r, g, 0.5);
+    const double over = r * g * g;
+    return KlTerm{over, over + g};
 }
 
 // e^x to fp32 precision in the range of fp64: a ratio beyond fp32's range times an
@@ -226,12 +233,11 @@ struct PolicyMode {
         double slope = above || below ? 0.0 : -ratio * (double)adv;   // d(-gain)/d logp
         double kl = 0.0, cost = 0.0;
         if (q.ref) {
-            const float gap = (float)((double)info.ref - logp);
-            const float over = exp_over(gap);   // e^gap - 1 - gap
-            kl = (double)over;
+            const KlTerm k = kl_term((double)info.ref - logp);
+            kl = k.over;
             if (q.kl != 0.0) {   // only reported else, and it may be infinite
                 cost = q.kl * kl;
-                slope -= q.kl * ((double)over + (double)gap);
+                slope -= q.kl * k.slope;
             }
         }
         if (writes && lane_id() == 0) {

@@ -1,0 +1,97 @@
+"""The losses over logits at the edges of their ranges: large KL gaps, coefficients beyond fp32,
+weights of 0, sums that cancel, and the calls around them.
+
+Most rows here are `even` ones: the label and one more token have the logit 0 and all others are
+masked or far below, so that the sum of a row is 2 without any rounding and the log-probability
+-ln 2 to 2^-44.  What is left of an error is then the function under test and the last roundings."""
+import math
+
+import pytest
+import torch
+
+import losses_formulas as F
+import sinkhorn_point_cloud_amd as sk
+
+pytestmark = pytest.mark.gpu
+U = F.U
+# rows that a wave, a work-group and several hold
+WIDTHS = [900, 20001, 70001]
+
+
+@pytest.fixture(autouse=True)
+def _say(request):
+    print(request.node.name, flush=True)
+    yield
+
+
+def even(T, V, dtype=torch.float32):
+    """(logits [T, V], labels [T]) on the GPU; the label 3, its equal V - 2, one token 40 below at
+    column 5, nothing else."""
+    z = torch.full((T, V), -math.inf, dtype=dtype)
+    z[:, 3] = z[:, V - 2] = 0.0
+    z[:, 5] = -40.0
+    return z.cuda(), torch.full((T,), 3, dtype=torch.int32).cuda()
+
+
+def near(got, want, rel, what):
+    """Equal where the fp32 value of `want` is 0 or infinite, else within rel of it."""
+    want = want.double()
+    w32 = want.float()
+    got = got.cpu()
+    plain = w32.isfinite() & (w32 != 0)
+    assert torch.equal(got.float()[~plain], w32[~plain]), (what, got[~plain], w32[~plain])
+    off = (got.double() - want)[plain].abs() / want[plain].abs()
+    assert off.numel() == 0 or off.max() <= rel, (what, off.max().item() / U, "units of 2^-24")
+
+
+GAPS = [-1000.0, -30.3, -5.7, -1.1, -0.01, 0.3, 5.3, 20.7, 90.1]
+
+
+@pytest.mark.parametrize("n", [9, 1])
+@pytest.mark.parametrize("V", WIDTHS)
+def test_kl_far_from_the_reference(V, n):
+    """k = e^d - d - 1 and its slope 1 - e^d for d = ref - logp from -1000 to 90, where e^d lies
+    beyond fp32 and the weighted loss does not.  kl, loss: the function within half a unit, a
+    term and the output rounded, 3 units.  The gradient: slope, exponential at the label (|logp| <
+    1: a series of 11 terms, the last few roundings) and the product, 8 units; 40 below the
+    maximum, an exponent of 58 rounded three times, 3 * 58 ln 2 units more."""
+    T = len(GAPS)
+    z, y = even(T, V)
+    lp = torch.full((T,), -math.log(2.0), dtype=torch.float64)
+    ref = (lp + torch.tensor(GAPS, dtype=torch.float64)).float()
+    gap = ref.double() - lp
+    w, coef = 2.0 ** -10, 0.01
+    kw = dict(ref=ref.cuda(), kl=coef, mean=False)
+    k = torch.exp(gap) - gap - 1
+    k[4] = gap[4] ** 2 / 2 * (1 + gap[4] / 3 * (1 + gap[4] / 4 * (1 + gap[4] / 5)))
+    slope = -coef * w * torch.expm1(gap)
+    if n == 1:      # one sequence of all rows
+        off, weights = torch.tensor([0, T]), torch.tensor([w])
+    else:
+        off, weights = torch.arange(T + 1), torch.full((T,), w)
+    adv = torch.zeros(T).cuda()
+    loss, kl, logp, d = sk.policy_loss(z, y, off.cuda(), lp.float().cuda(), adv,
+                                       weights=weights.cuda(), **kw)
+    total = (lambda x: x.sum()[None]) if n == 1 else (lambda x: x)
+    near(kl, total(w * k), 3 * U, "kl")
+    near(loss, total(coef * w * k), 3 * U, "loss")
+    want = torch.zeros(T, V, dtype=torch.float64)
+    want[:, 3], want[:, V - 2] = slope / 2, -slope / 2
+    far = -slope * math.exp(-40) / 2
+    near(d[:, 5], far, (8 + 3 * 58 * math.log(2)) * U, "gradient of the far token")
+    d[:, 5] = 0
+    near(d, want, 8 * U, "gradient")
+
+
+@pytest.mark.parametrize("V", WIDTHS)
+def test_a_label_that_the_reference_forbids(V):
+    """ref = -inf: e^d is 0, the term infinite and its slope that of -d, 1 (8 units as above)."""
+    z, y = even(3, V)
+    old = torch.full((3,), -math.log(2.0)).cuda()
+    ref = old.clone()
+    ref[1] = -math.inf
+    loss, kl, _, d = sk.policy_loss(z, y, torch.arange(4).cuda(), old, torch.zeros(3).cuda(),
+                                    ref=ref, kl=0.25)
+    assert kl[1] == math.inf and loss[1] == math.inf and loss[[0, 2]].isfinite().all()
+    assert d.isfinite().all()
+    near(d[1, [3, V - 2]], torch.tensor([0.125, -0.125], dtype=torch.float64), 8 * U, "gradient")
