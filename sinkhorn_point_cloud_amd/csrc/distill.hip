@@ -157,7 +157,8 @@ __device__ __forceinline__ Teacher teacher_side(const Args &a, long t, const Lis
 }
 
 struct RowScalars {
-    float A, M;   // out_v = A 2^((z_v - M) c) for tokens that are not in the list
+    Coefficient a;
+    float M;   // out_v = a 2^((z_v - M) c) for tokens that are not in the list
     int zero;
 };
 
@@ -216,7 +217,7 @@ __device__ __forceinline__ RowScalars student_side(const Args &a, long t, const 
     const bool none = row_empty(M, R) || (!r.any && !r.bad);
     if (writes && lane == 0)
         a.d.loss[t] = none ? 0.f : (float)(r.bad ? nan : w * tau * tau * sum);
-    return RowScalars{(float)(add * over), M, none};
+    return RowScalars{coefficient(add * over), M, none};
 }
 
 // The entries that this thread owns, as values of its gradient.
@@ -308,7 +309,7 @@ __global__ __launch_bounds__(NT, Src::waves) void distill_kernel(Args a)
         zero_row<T, NT>(out, V, 0, 1);
         return;
     }
-    src.dense(out, Dense{k.A, k.M, a.c.near}, ListTerms(l));
+    src.dense(out, Dense{k.a.A, k.M, a.c.near, k.a.up}, ListTerms(l));
 }
 
 // Few rows: partial statistics, and the student's logits at the list's tokens
@@ -376,7 +377,7 @@ template <typename T> __global__ __launch_bounds__(kSplit) void distill_join_ker
         zero_row<T, kSplit>(out, V, part, run);
         return;
     }
-    src.dense(out, Dense{k.A, k.M, a.c.near}, ListTerms(l));
+    src.dense(out, Dense{k.a.A, k.M, a.c.near, k.a.up}, ListTerms(l));
 }
 
 template <typename T> struct RunRows {

@@ -409,13 +409,25 @@ __device__ __forceinline__ float expm1_of(float g)
     return fmaf(r * g, g, g);
 }
 
-// coefficient x exponential of one row, out_v = A 2^((x_v - M) c), but for the
+// coefficient x exponential of one row, out_v = A 2^((x_v - M) c + up), but for the
 // elements that have a value of their own.  Those are a `Terms` with
 //     chunk(i, first, x): sets them in a thread's i-th chunk, whose first element is `first`,
 //     edge(v, y):         the value of element v of the edge, y if it has none.
+// `up` is 0 but for a coefficient beyond fp32, of which A is then the mantissa: the
+// coefficient is no output, and times a probability of 0 it is 0.
+struct Coefficient {
+    float A, up;
+};
+__device__ __forceinline__ Coefficient coefficient(double a)
+{
+    if (fabs(a) > 3.4028234663852886e38 && fabs(a) < __builtin_inf())
+        return Coefficient{(float)__builtin_amdgcn_frexp_mant(a),
+                           (float)__builtin_amdgcn_frexp_exp(a)};
+    return Coefficient{(float)a, 0.f};
+}
 struct Dense {
-    float A, M, c;
-    __device__ __forceinline__ float at(float x) const { return A * ex2((x - M) * c); }
+    float A, M, c, up;
+    __device__ __forceinline__ float at(float x) const { return A * ex2(fmaf(x - M, c, up)); }
 };
 
 // One element.

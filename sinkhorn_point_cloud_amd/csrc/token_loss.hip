@@ -26,8 +26,9 @@ constexpr int kSplit = 256;   // threads of a work-group that shares its row wit
 
 // What the scalar phase of a row leaves for its gradient pass.
 struct RowScalars {
-    float A, M, own;   // out_v = A 2^((z_v - M) c), `own` for the label
-    int zero;          // the row's gradient is zero
+    Coefficient a;
+    float M, own;   // out_v = a 2^((z_v - M) c), `own` for the label
+    int zero;       // the row's gradient is zero
 };
 
 enum RowState { kOutside, kZeroRow, kUsed };
@@ -87,9 +88,9 @@ __device__ __forceinline__ RowState row_state(const LabelArgs &a, long t, int la
 // makes the whole row NaN.
 __device__ __forceinline__ RowScalars coefficients(double add, double logp, float M, double R)
 {
-    const float own = (float)-add * expm1_of((float)logp);
-    const float A = logp == logp ? (float)(-add / row_sum(M, R)) : __builtin_nanf("");
-    return RowScalars{A, M, own, row_empty(M, R)};
+    const float own = (float)(-add * (double)expm1_of((float)logp));
+    const double a = logp == logp ? -add / row_sum(M, R) : __builtin_nan("");
+    return RowScalars{coefficient(a), M, own, row_empty(M, R)};
 }
 
 struct LogpMode {
@@ -113,7 +114,7 @@ struct LogpMode {
             if (a.out.stat)
                 a.out.stat[t] = RowStat{M, (float)R, none ? 0.0 : ((double)zy - (double)M) * s - lnS};
         }
-        return RowScalars{0.f, 0.f, 0.f, 1};
+        return RowScalars{{0.f, 0.f}, 0.f, 0.f, 1};
     }
     __device__ __forceinline__ static void unused(const LabelArgs &a, long t)
     {
@@ -302,7 +303,7 @@ __global__ __launch_bounds__(NT, Src::waves) void row_kernel(LabelArgs a)
     if (k.zero)
         zero_row<T, NT>(out, V, 0, 1);
     else
-        src.dense(out, Dense{k.A, k.M, a.c.near}, OneTerm{label, k.own});
+        src.dense(out, Dense{k.a.A, k.M, a.c.near, k.a.up}, OneTerm{label, k.own});
 }
 
 // Few rows: each over `parts` work-groups.  First launch: partial statistics.
@@ -370,7 +371,7 @@ __global__ __launch_bounds__(kSplit) void join_kernel(LabelArgs a, int run)
         return;
     }
     const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, run);
-    src.dense(out, Dense{k.A, k.M, a.c.near}, OneTerm{label, k.own});
+    src.dense(out, Dense{k.a.A, k.M, a.c.near, k.a.up}, OneTerm{label, k.own});
 }
 
 // --- per sequence
@@ -561,7 +562,7 @@ template <typename T, bool Fold> __global__ __launch_bounds__(kSplit) void pair_
     }
     const RowScalars k = coefficients((double)G * a.r.scale, stat.logp, stat.M, stat.R);
     const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, a.parts);
-    src.dense(out, Dense{k.A, k.M, a.c.near}, OneTerm{label, k.own});
+    src.dense(out, Dense{k.a.A, k.M, a.c.near, k.a.up}, OneTerm{label, k.own});
 }
 
 }  // namespace

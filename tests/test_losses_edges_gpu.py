@@ -95,3 +95,35 @@ def test_a_label_that_the_reference_forbids(V):
     assert kl[1] == math.inf and loss[1] == math.inf and loss[[0, 2]].isfinite().all()
     assert d.isfinite().all()
     near(d[1, [3, V - 2]], torch.tensor([0.125, -0.125], dtype=torch.float64), 8 * U, "gradient")
+
+
+@pytest.mark.parametrize("V", WIDTHS)
+def test_coefficients_beyond_fp32(V):
+    """A row's coefficient (here up to 1.2e39) is no output: where it meets a probability of 0 the
+    gradient is 0, and 40 below the maximum an ordinary number.  Tolerances as for the KL gaps."""
+    far_rel = (8 + 3 * 58 * math.log(2)) * U
+    far = math.exp(-40) / 2
+
+    def check(d, G, what):
+        """d = G (1[label] - q), or G (q - 1[label]) of -G, per row."""
+        want = torch.zeros(d.shape, dtype=torch.float64)
+        want[:, 3], want[:, V - 2] = G / 2, -G / 2
+        near(d[:, 5], -G * far, far_rel, what + " far")
+        d = d.clone()
+        d[:, 5] = 0
+        near(d, want, 8 * U, what)
+
+    z, y = even(2, V)
+    G = torch.tensor([3e38, -2.5e38])
+    check(sk.token_logprobs_backward(z, y, G.cuda(), scale=1.0), G.double(), "backward")
+    half = z / 2        # twice the gradient, half the logits: the same softmax
+    check(sk.token_logprobs_backward(half, y, G.cuda(), scale=2.0), 2 * G.double(), "scaled")
+    old = torch.full((2,), -math.log(2.0)).cuda()
+    ref = (old.double() + 90.1).float()
+    d = sk.policy_loss(z, y, torch.arange(3).cuda(), old, torch.zeros(2).cuda(), ref=ref, kl=1.0)[3]
+    gap = ref.cpu().double() + math.log(2.0)
+    check(d, -torch.expm1(gap), "KL")
+    # temperature 2 over twice the logits: w tau (q - 1[token])
+    w = G.abs().cuda()
+    d = sk.distill_loss(z * 2, y[:, None], torch.zeros(2, 1).cuda(), temperature=2.0, weights=w)[1]
+    check(d, -2 * w.cpu().double(), "distillation")
