@@ -32,7 +32,9 @@
  *     that is not scored (of a mean's count too where the operation says so).  The
  *     type's lowest finite value is an ordinary number.  NaN or +inf gives NaN.
  *   - The returned losses include their weights, and the gradient is that of
- *     their sum.
+ *     their sum.  A sequence, pair or row of weight 0 has loss (and KL) 0 and
+ *     gradient 0, whatever its rows hold; the log-probabilities and rewards of a
+ *     sequence or pair are reported all the same.
  *   - Exponentials are fp32, and so are a thread's sums of them; their joins,
  *     logarithms, ratios, clipping decisions and sums over rows are fp64.  Each output is rounded once.  Same inputs at the
  *     same addresses modulo 128 bytes, same bits: no result depends on an order

@@ -221,7 +221,8 @@ struct PolicyMode {
                                                      float M, double R, float zy, bool writes)
     {
         const PolicyArgs &q = a.pol;
-        const bool none = row_empty(M, R);
+        // without a distribution, or weighted out: no part, whatever the row holds
+        const bool empty = row_empty(M, R), none = empty || info.w == 0.f;
         const double s = a.r.scale, w = (double)info.w;
         const float adv = info.adv;
         const double logp = ((double)zy - (double)M) * s - row_ln(M, R);
@@ -243,12 +244,14 @@ struct PolicyMode {
         }
         if (writes && lane_id() == 0) {
             if (q.logp)
-                q.logp[t] = none ? 0.f : (float)logp;
+                q.logp[t] = empty ? 0.f : (float)logp;
             q.term[t] = none ? make_float2(0.f, 0.f)
                              : make_float2((float)(w * (cost - gain)),
                                            (float)(w * kl));
         }
-        return coefficients(slope * w * s, logp, M, R);
+        RowScalars k = coefficients(slope * w * s, logp, M, R);
+        k.zero = none;
+        return k;
     }
     __device__ __forceinline__ static void unused(const LabelArgs &a, long t)
     {
@@ -487,6 +490,8 @@ __device__ __forceinline__ void pair_slopes(const int32_t *labels, const Packed 
         loss = d * d;
         slope = 2.0 * d;
     }
+    if (w == 0.0)   // weighted out, whatever its rows hold
+        loss = slope = 0.0;
     if (threadIdx.x == 0) {
         if (writes) {
             a.loss[i] = (float)(w * loss);
@@ -559,6 +564,10 @@ template <typename T, bool Fold> __global__ __launch_bounds__(kSplit) void pair_
         G = slopes[i % 2];
     } else {
         G = a.q.coef[t];
+    }
+    if (G == 0.f) {
+        zero_row<T, kSplit>(out, V, part, a.parts);
+        return;
     }
     const RowScalars k = coefficients((double)G * a.r.scale, stat.logp, stat.M, stat.R);
     const Streamed<T, kSplit> src((const T *)a.r.logits + t * a.r.ld, V, part, a.parts);

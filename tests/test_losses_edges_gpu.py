@@ -127,3 +127,48 @@ def test_coefficients_beyond_fp32(V):
     w = G.abs().cuda()
     d = sk.distill_loss(z * 2, y[:, None], torch.zeros(2, 1).cuda(), temperature=2.0, weights=w)[1]
     check(d, -2 * w.cpu().double(), "distillation")
+
+
+@pytest.mark.parametrize("n", [4, 80])
+@pytest.mark.parametrize("V", WIDTHS)
+@pytest.mark.parametrize("mean", [True, False])
+def test_a_weight_of_zero_takes_a_sequence_out(V, n, mean):
+    """Sequences weighted out because they hold NaN, an impossible label or an infinite KL: their
+    losses and gradients are 0, their log-probabilities and rewards are reported, and the others are
+    as if alone, to the bit."""
+    g = torch.Generator().manual_seed(V + n)
+    T = 2 * n
+    z = torch.randn(T, V, generator=g)
+    y = torch.randint(0, V, (T,), generator=g, dtype=torch.int32)
+    clean = z.clone()
+    z[2, 7] = math.nan
+    z[3, y[3]] = -math.inf
+    z, y, clean = z.cuda(), y.cuda(), clean.cuda()
+    off = torch.arange(0, T + 1, 2).cuda()
+    w = torch.ones(n)
+    w[1] = 0.0
+    out = torch.ones(T, dtype=torch.bool)
+    out[2:4] = False
+    old = sk.token_logprobs(clean, y)[0]
+    ref = old + 0.1
+    args = (y, off, old, torch.ones(n).cuda())
+    kw = dict(ref=ref, kl=0.1, weights=w.cuda(), mean=mean)
+    loss, kl, logp, d = sk.policy_loss(z, *args, **kw)
+    want = sk.policy_loss(clean, *args, **kw)
+    assert loss[1] == 0 and kl[1] == 0 and (d[2:4] == 0).all()
+    assert logp[2].isnan() and logp[3] == -math.inf
+    for a, b in ((loss, want[0]), (kl, want[1])):
+        assert torch.equal(a[w.bool().cuda()], b[w.bool().cuda()])
+    for a, b in ((logp, want[2]), (d, want[3])):
+        assert torch.equal(a[out.cuda()], b[out.cuda()])
+    pw = w[:n // 2].clone()
+    pw[:2] = torch.tensor([0.0, 1.0])
+    for kind in ("sigmoid", "square"):
+        kw = dict(weights=pw.cuda(), mean=mean, kind=kind)
+        loss, reward, logp, d = sk.preference_loss(z, y, off, old, **kw)
+        want = sk.preference_loss(clean, y, off, old, **kw)
+        assert loss[0] == 0 and (d[:4] == 0).all() and reward[1].isnan()
+        assert logp[2].isnan() and logp[3] == -math.inf
+        assert torch.equal(loss, want[0]) and torch.equal(reward[2:], want[1][2:])
+        assert torch.equal(reward[0], want[1][0]) and torch.equal(d, want[3])
+        assert torch.equal(logp[out.cuda()], want[2][out.cuda()])
