@@ -9,7 +9,8 @@ Labels and indices are int32, offsets int64, everything else float32.  The work
 runs on the current stream of the tensors' device.  A returned gradient has the
 logits' dtype and, where their rows are padded, their row distance; it is the
 gradient of the sum of the returned losses.  ``out`` reuses buffers, and its
-gradient may be the logits themselves.  Rows outside every sequence get zeros in
+gradient may be the logits themselves; ``grad=False`` skips the gradient (None), also
+where ``out`` holds a buffer for it.  Rows outside every sequence get zeros in
 outputs that the call allocates and are left alone in the caller's.
 ``workspace`` is a uint8 tensor of at least ``losses_workspace_bytes``; calls
 that overlap, and graphs that are replayed, need one each.
@@ -194,8 +195,7 @@ def policy_loss(logits, labels, offsets, old, adv, ref=None, clip=(0.2, 0.2), kl
     sequence [n] or one per row [T] (where n == T, per row); ``ref`` [T]: a reference
     model's log-probabilities, for the KL term of coefficient ``kl``; ``weights`` [n]:
     one per sequence.  ``mean`` divides a sequence's sum by its number of labels.
-    ``grad=False`` skips the gradient (None).  ``out`` = (loss, kl, logp, dlogits),
-    the last two may be None."""
+    ``out`` = (loss, kl, logp, dlogits), the last two may be None."""
     lib = load_library()
     logits, dt, T, V, ld = _rows(logits)
     dev = logits.device
@@ -210,6 +210,7 @@ def policy_loss(logits, labels, offsets, old, adv, ref=None, clip=(0.2, 0.2), kl
     flags = (SK_LOSS_MEAN if mean else 0) | (SK_LOSS_ROW_ADVANTAGE if per_row else 0)
     if out is not None:
         loss, kls, logp, d = out
+        d = d if grad else None
         dld = _check_gradient(d, logits)
         if loss is None or kls is None:
             raise ValueError("out needs loss and kl tensors")
@@ -252,6 +253,7 @@ def preference_loss(logits, labels, offsets, ref=None, beta: float = 0.1, smooth
     flags = SK_LOSS_MEAN if mean else 0
     if out is not None:
         loss, reward, logp, d = out
+        d = d if grad else None
         dld = _check_gradient(d, logits)
         if loss is None or reward is None or logp is None:
             raise ValueError("out needs loss, reward and logp tensors")
@@ -291,6 +293,7 @@ def distill_loss(logits, index, teacher, teacher_lse=None, temperature: float = 
         raise ValueError(f"temperature must be positive, got {temperature}")
     if out is not None:
         loss, d = out
+        d = d if grad else None
         dld = _check_gradient(d, logits)
         if loss is None:
             raise ValueError("out needs a loss tensor")
@@ -326,6 +329,7 @@ def balance_loss(logits, index, offsets=None, balance: float = 1.0, z: float = 0
     flags = 0
     if out is not None:
         loss, zloss, counts, d = out
+        d = d if grad else None
         dld = _check_gradient(d, logits)
         if loss is None or zloss is None or counts is None:
             raise ValueError("out needs loss, zloss and counts tensors")

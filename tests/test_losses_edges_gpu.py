@@ -172,3 +172,25 @@ def test_a_weight_of_zero_takes_a_sequence_out(V, n, mean):
         assert torch.equal(loss, want[0]) and torch.equal(reward[2:], want[1][2:])
         assert torch.equal(reward[0], want[1][0]) and torch.equal(d, want[3])
         assert torch.equal(logp[out.cuda()], want[2][out.cuda()])
+
+
+def test_no_gradient_into_a_buffer_that_is_not_asked_for():
+    g = torch.Generator().manual_seed(1)
+    T, V = 6, 300
+    z = torch.randn(T, V, generator=g).cuda()
+    y = torch.randint(0, V, (T,), generator=g, dtype=torch.int32).cuda()
+    off = torch.tensor([0, 2, 6]).cuda()
+    x = torch.randn(T, generator=g).cuda()
+    new = lambda *s, dtype=torch.float32: torch.full(s, 7, dtype=dtype, device="cuda")  # noqa: E731
+    d = new(T, V)
+    calls = [(sk.policy_loss, (z, y, off, x, x), (new(2), new(2), new(T))),
+             (sk.preference_loss, (z, y, off), (new(1), new(2), new(T))),
+             (sk.distill_loss, (z, y[:, None], x[:, None]), (new(T),)),
+             (sk.balance_loss, (z, y[:, None], off),
+              (new(2), new(2), new(2, V, dtype=torch.int32)))]
+    for call, args, out in calls:
+        want = call(*args)
+        got = call(*args, out=(*out, d), grad=False)
+        assert got[-1] is None and (d == 7).all(), call
+        for a, b in zip(got[:-1], want[:-1]):
+            assert torch.equal(a, b), call
