@@ -14,8 +14,9 @@
  *     modulo 128 bytes as their logits are written fastest.
  *   - dlogits has the logits' dtype and rows `dld` apart.  It may be the logits
  *     themselves (the same address and row distance): the gradient is then
- *     written over them.  Any other overlap is refused.  NULL: no gradient.
- *     No other output may share memory with an input.
+ *     written over them.  NULL: no gradient.  Any other call in which outputs, the
+ *     gradient or the workspace share memory with each other or with an input is
+ *     refused; arrays between the rows of padded logits share none with them.
  *   - 0 <= T <= 2^24 rows and 1 <= V <= 2^24 values.  With T == 0 the pointers
  *     of row arrays may be NULL.
  *   - labels is [T] int32.  A negative label marks a row that is not scored (a

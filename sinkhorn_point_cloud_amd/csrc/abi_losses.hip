@@ -5,6 +5,7 @@
 #include "sinkhorn_losses.h"
 #include "token_loss.h"
 
+#include <initializer_list>
 #include <math.h>
 
 namespace sk {
@@ -141,6 +142,70 @@ int check_space(const void *ws, size_t ws_bytes, size_t need)
     return SK_OK;
 }
 
+// An array of a call (at == NULL: not given).
+struct Span {
+    const char *name;
+    const void *at;
+    size_t bytes;
+    uintptr_t first() const { return (uintptr_t)at; }
+    uintptr_t end() const { return first() + bytes; }
+};
+
+// Rows of a matrix, `distance` bytes from one to the next; what lies between them is
+// another's.
+struct Rows {
+    const char *name;
+    const void *at;
+    uint64_t rows, bytes, distance;
+};
+
+bool meet(const Span &a, const Span &b)
+{
+    return a.at && b.at && a.bytes && b.bytes && a.first() < b.end() && b.first() < a.end();
+}
+
+bool meet(const Span &a, const Rows &r)
+{
+    if (!a.at || !a.bytes || !r.at || !r.rows)
+        return false;
+    const uintptr_t first = (uintptr_t)r.at;
+    if (a.end() <= first || a.first() >= first + (r.rows - 1) * r.distance + r.bytes)
+        return false;
+    if (a.first() < first)
+        return true;
+    const uint64_t in = (a.first() - first) % r.distance;
+    return in < r.bytes || in + a.bytes > r.distance;
+}
+
+// Outputs, the workspace among them, lie apart from the inputs and from one another
+// (work-groups that share a row read what others would have overwritten), and the
+// gradient apart from all but the logits.
+int check_apart(const LogitRows &r, std::initializer_list<Span> inputs,
+                std::initializer_list<Span> outputs)
+{
+    const uint64_t size = elem(r.dtype), T = (uint64_t)r.T, bytes = (uint64_t)r.V * size;
+    const Rows logits{"logits", r.logits, T, bytes, (uint64_t)r.ld * size};
+    const Rows dlogits{"dlogits", r.dlogits, T, bytes, (uint64_t)r.dld * size};
+    auto refuse = [](const char *a, const char *b) {
+        return fail(SK_ERR_INVALID_ARG, "%s and %s overlap", a, b);
+    };
+    for (const Span *o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Span &i : inputs)
+            if (meet(*o, i))
+                return refuse(o->name, i.name);
+        for (const Span *q = outputs.begin(); q != o; ++q)
+            if (meet(*o, *q))
+                return refuse(o->name, q->name);
+        for (const Rows *m : {&logits, &dlogits})
+            if (meet(*o, *m))
+                return refuse(o->name, m->name);
+    }
+    for (const Span &i : inputs)
+        if (meet(i, dlogits))
+            return refuse(dlogits.name, i.name);
+    return SK_OK;
+}
+
 }  // namespace
 }  // namespace sk
 
@@ -170,9 +235,15 @@ int sinkhorn_token_logprobs(const void *logits, int dtype, int64_t ld, const int
         return rc;
     if (T == 0)
         return SK_OK;
+    const LogitRows r{logits, ld, dtype, T, V, scale, nullptr, 0};
+    const size_t rows = (size_t)T * 4;
+    if ((rc = check_apart(r, {{"labels", labels, rows}},
+                          {{"logp", logp, rows},
+                           {"lse", lse, rows},
+                           {"ws", ws, ws_bytes_of(SK_OP_TOKEN_LOGPROBS, T, V, 0, dtype)}})))
+        return rc;
     Carve c{(char *)ws};
     const Ws w = carve(c, SK_OP_TOKEN_LOGPROBS, T, V, 0, dtype);
-    const LogitRows r{logits, ld, dtype, T, V, scale, nullptr, 0};
     const hipError_t e = launch_logp(r, labels, Packed{nullptr, 0, 0}, w.token,
                                      LogpOut{logp, lse, nullptr}, (hipStream_t)stream);
     return e ? hip_fail(e, "token log-probabilities") : SK_OK;
@@ -194,9 +265,13 @@ int sinkhorn_token_logprobs_backward(const void *logits, int dtype, int64_t ld,
         return rc;
     if (T == 0)
         return SK_OK;
+    const LogitRows r{logits, ld, dtype, T, V, scale, dlogits, dld};
+    const size_t rows = (size_t)T * 4;
+    if ((rc = check_apart(r, {{"labels", labels, rows}, {"grad", grad, rows}},
+                          {{"ws", ws, ws_bytes_of(SK_OP_TOKEN_LOGPROBS, T, V, 0, dtype)}})))
+        return rc;
     Carve c{(char *)ws};
     const Ws w = carve(c, SK_OP_TOKEN_LOGPROBS, T, V, 0, dtype);
-    const LogitRows r{logits, ld, dtype, T, V, scale, dlogits, dld};
     const hipError_t e = launch_logp_backward(r, labels, grad, w.token, (hipStream_t)stream);
     return e ? hip_fail(e, "token log-probabilities backward") : SK_OK;
 }
@@ -225,9 +300,21 @@ int sinkhorn_policy_loss(const void *logits, int dtype, int64_t ld, const int32_
     if ((rc = check_grad(logits, ld, dlogits, dld, dtype, T, V)) ||
         (rc = check_space(ws, ws_bytes, ws_bytes_of(SK_OP_POLICY_LOSS, T, V, 0, dtype))))
         return rc;
+    const LogitRows r{logits, ld, dtype, T, V, scale, dlogits, dld};
+    const size_t rows = (size_t)T * 4, seqs = (size_t)n * 4;
+    if ((rc = check_apart(r, {{"labels", labels, rows},
+                              {"offsets", offsets, 2 * seqs + 8},
+                              {"old", old, rows},
+                              {"adv", adv, flags & SK_LOSS_ROW_ADVANTAGE ? rows : seqs},
+                              {"ref", ref, rows},
+                              {"weights", weights, seqs}},
+                          {{"loss", loss, seqs},
+                           {"kl", kl, seqs},
+                           {"logp", logp, rows},
+                           {"ws", ws, ws_bytes_of(SK_OP_POLICY_LOSS, T, V, 0, dtype)}})))
+        return rc;
     Carve c{(char *)ws};
     const Ws w = carve(c, SK_OP_POLICY_LOSS, T, V, 0, dtype);
-    const LogitRows r{logits, ld, dtype, T, V, scale, dlogits, dld};
     PolicyArgs a{};
     a.old = old;
     a.ref = ref;
@@ -273,9 +360,19 @@ int sinkhorn_preference_loss(const void *logits, int dtype, int64_t ld, const in
     if ((rc = check_grad(logits, ld, dlogits, dld, dtype, T, V)) ||
         (rc = check_space(ws, ws_bytes, ws_bytes_of(SK_OP_PREFERENCE_LOSS, T, V, 0, dtype))))
         return rc;
+    const LogitRows r{logits, ld, dtype, T, V, scale, dlogits, dld};
+    const size_t rows = (size_t)T * 4, each = (size_t)pairs * 4;
+    if ((rc = check_apart(r, {{"labels", labels, rows},
+                              {"offsets", offsets, 4 * each + 8},
+                              {"ref", ref, rows},
+                              {"weights", weights, each}},
+                          {{"loss", loss, each},
+                           {"reward", reward, 2 * each},
+                           {"logp", logp, rows},
+                           {"ws", ws, ws_bytes_of(SK_OP_PREFERENCE_LOSS, T, V, 0, dtype)}})))
+        return rc;
     Carve c{(char *)ws};
     const Ws w = carve(c, SK_OP_PREFERENCE_LOSS, T, V, 0, dtype);
-    const LogitRows r{logits, ld, dtype, T, V, scale, dlogits, dld};
     const PreferenceArgs a{ref,       weights, kind,   (flags & SK_LOSS_MEAN) != 0,
                            beta,      smoothing, w.coef, w.stat,
                            loss,      reward,  logp};
@@ -305,9 +402,17 @@ int sinkhorn_distill_loss(const void *logits, int dtype, int64_t ld, int T, int 
         return rc;
     if (T == 0)
         return SK_OK;
+    const LogitRows r{logits, ld, dtype, T, V, 1.0 / temperature, dlogits, dld};
+    const size_t rows = (size_t)T * 4;
+    if ((rc = check_apart(r, {{"index", index, rows * K},
+                              {"teacher", teacher, rows * K},
+                              {"teacher_lse", teacher_lse, rows},
+                              {"weights", weights, rows}},
+                          {{"loss", loss, rows},
+                           {"ws", ws, ws_bytes_of(SK_OP_DISTILL_LOSS, T, V, K, dtype)}})))
+        return rc;
     Carve c{(char *)ws};
     const Ws w = carve(c, SK_OP_DISTILL_LOSS, T, V, K, dtype);
-    const LogitRows r{logits, ld, dtype, T, V, 1.0 / temperature, dlogits, dld};
     const DistillArgs a{index, teacher, teacher_lse, weights, K, w.zk, loss};
     const hipError_t e = launch_distill(r, a, w.token, (hipStream_t)stream);
     return e ? hip_fail(e, "distillation loss") : SK_OK;
@@ -336,6 +441,15 @@ int sinkhorn_balance_loss(const void *logits, int dtype, int64_t ld, int T, int 
         return fail(SK_ERR_INVALID_ARG, "balance=%g and z=%g must be finite", balance, z);
     if ((rc = check_grad(logits, ld, dlogits, dld, dtype, T, E)) ||
         (rc = check_space(ws, ws_bytes, ws_bytes_of(SK_OP_BALANCE_LOSS, T, E, G, dtype))))
+        return rc;
+    const size_t groups = (size_t)G * 4;
+    if ((rc = check_apart(LogitRows{logits, ld, dtype, T, E, 1.0, dlogits, dld},
+                          {{"index", index, (size_t)T * K * 4},
+                           {"offsets", offsets, 2 * groups + 8}},
+                          {{"loss", loss, groups},
+                           {"zloss", zloss, groups},
+                           {"counts", counts, groups * E},
+                           {"ws", ws, ws_bytes_of(SK_OP_BALANCE_LOSS, T, E, G, dtype)}})))
         return rc;
     Carve c{(char *)ws};
     const Ws w = carve(c, SK_OP_BALANCE_LOSS, T, E, G, dtype);

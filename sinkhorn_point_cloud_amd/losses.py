@@ -11,7 +11,8 @@ logits' dtype and, where their rows are padded, their row distance; it is the
 gradient of the sum of the returned losses.  ``out`` reuses buffers, and its
 gradient may be the logits themselves; ``grad=False`` skips the gradient (None), also
 where ``out`` holds a buffer for it.  Rows outside every sequence get zeros in
-outputs that the call allocates and are left alone in the caller's.
+outputs that the call allocates and are left alone in the caller's.  Buffers that share
+memory with other arguments (but for that gradient) are refused.
 ``workspace`` is a uint8 tensor of at least ``losses_workspace_bytes``; calls
 that overlap, and graphs that are replayed, need one each.
 """

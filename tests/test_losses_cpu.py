@@ -144,7 +144,7 @@ import ctypes
 import sinkhorn_point_cloud_amd as sk
 lib, P = sk.load_library(), ctypes.c_void_p(4096)
 F = [ctypes.c_void_p(4096 * (k + 2)) for k in range(4)]
-tail = (P, 1 << 40, None)
+tail = (ctypes.c_void_p(1 << 32), 1 << 40, None)
 print(lib.sinkhorn_policy_loss(None, 0, 16, None, 0, 16, P, {n}, None, None, None, None, 1.0, 0.2,
                                0.2, 0.0, 0, F[0], F[1], None, F[2], 16, *tail),
       lib.sinkhorn_preference_loss(None, 0, 16, None, 0, 16, P, {n}, None, None, 1.0, 0, 0.1, 0.0, 0,
@@ -290,3 +290,83 @@ def test_logp_formula_against_torch():
     want = torch.log_softmax(z.double() * 0.7, 1).gather(1, y.long().clamp(min=0)[:, None])[:, 0]
     want[2] = 0
     assert (r.logp(y)[0] - want).abs().max() < 1e-12
+
+
+# --- outputs on top of inputs
+
+AT = {name: (k + 1) << 32 for k, name in enumerate(
+    "logits labels grad offsets old adv ref weights index teacher tlse loss klo reward zloss counts "
+    "logp lse dlogits ws".split())}
+T_, V_, N_, K_, LD_ = 10, 64, 3, 4, 80
+READS = {
+    "token_logprobs": "logits labels",
+    "token_logprobs_backward": "logits labels grad",
+    "policy_loss": "logits labels offsets old adv ref weights",
+    "preference_loss": "logits labels offsets ref weights",
+    "distill_loss": "logits index teacher tlse weights",
+    "balance_loss": "logits index offsets",
+}
+WRITES = {
+    "token_logprobs": "logp lse ws",
+    "token_logprobs_backward": "dlogits ws",
+    "policy_loss": "loss klo logp dlogits ws",
+    "preference_loss": "loss reward logp dlogits ws",
+    "distill_loss": "loss dlogits ws",
+    "balance_loss": "loss zloss counts dlogits ws",
+}
+PAIRS = [(n, o, i) for n in ALL for o in WRITES[n].split()
+         for i in READS[n].split() + WRITES[n].split() if o != i and (o, i) != ("dlogits", "logits")]
+
+
+def _sizes(name):
+    """Bytes of each array of the calls below; rows of logits and gradient are LD_ apart."""
+    seqs = 2 * N_ if name == "preference_loss" else N_
+    per = 4 * (N_ if name in ("policy_loss", "preference_loss") else T_)
+    op = {"token_logprobs": 0, "token_logprobs_backward": 0, "policy_loss": 1, "preference_loss": 2,
+          "distill_loss": 3, "balance_loss": 4}[name]
+    rows = ((T_ - 1) * LD_ + V_) * 4
+    loss = 4 * (T_ if name == "distill_loss" else N_)
+    return dict(logits=rows, dlogits=rows, labels=4 * T_, grad=4 * T_, offsets=8 * (seqs + 1),
+                old=4 * T_, adv=4 * N_, ref=4 * T_, weights=per, index=4 * T_ * K_,
+                teacher=4 * T_ * K_, tlse=4 * T_, loss=loss, klo=loss, reward=4 * seqs, zloss=loss,
+                counts=4 * N_ * V_, logp=4 * T_, lse=4 * T_,
+                ws=sk.losses_workspace_bytes(op, T_, V_, {3: K_, 4: N_}.get(op, 0), 0))
+
+
+def _placed(at):
+    p = {k: ctypes.c_void_p(v) for k, v in at.items()}
+    return dict(p, T=T_, V=V_, ld=LD_, dld=LD_, n=N_, G=N_, K=K_)
+
+
+@pytest.mark.parametrize("name,out,other", PAIRS)
+def test_outputs_over_other_arrays_are_refused(lib, name, out, other):
+    size = _sizes(name)
+    # the first and the last element of either array in the other
+    for at in (AT[other], AT[other] + size[other] - 4, AT[other] - size[out] + 4):
+        assert _call(lib, name, _placed(dict(AT, **{out: at}))) == sk.SK_ERR_INVALID_ARG
+        assert b"overlap" in lib.sinkhorn_last_error()
+
+
+def test_arrays_side_by_side_are_accepted():
+    """One array right behind another, and arrays in the gaps between padded rows: those calls reach
+    the launch, which fails without a device."""
+    program = f"""
+import sys
+sys.path[:0] = [{ROOT!r}, {os.path.join(ROOT, "tests")!r}]
+import test_losses_cpu as t
+lib = t.sk.load_library()
+for name, out, other in t.PAIRS:
+    size, at = t._sizes(name), dict(t.AT)
+    for place in (at[other] + size[other], at[other] - size[out]):
+        code = t._call(lib, name, t._placed(dict(at, **{{out: place}})))
+        assert code == 5, (name, out, other, code, lib.sinkhorn_last_error())
+    if size[out] <= 64 and other in ("logits", "dlogits"):
+        for gap, code in ((256, 5), (256 + 64 - size[out], 5), (252, 1), (256 + 68 - size[out], 1)):
+            place = at[other] + 3 * 320 + gap
+            got = t._call(lib, name, t._placed(dict(at, **{{out: place}})))
+            assert got == code, (name, out, other, gap, got, lib.sinkhorn_last_error())
+print("done")
+"""
+    run = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True,
+                         env=dict(os.environ, HIP_VISIBLE_DEVICES="-1"))
+    assert run.returncode == 0 and run.stdout.split() == ["done"], run
