@@ -13,7 +13,8 @@ namespace {
 
 constexpr int kMaxRows = 1 << 24;
 constexpr int kMaxSequences = 1 << 20;   // a work-group of 1024 threads each: 2^30 in a launch
-constexpr int64_t kMaxStride = 1ll << 38;   // rows x stride x 4 bytes stays below 2^64
+constexpr int64_t kMaxStride = 1ll << 38;
+constexpr int64_t kMaxSpan = 1ll << 58;      // elements: 2^60 bytes, beyond any address space
 
 size_t elem(int dtype) { return dtype == SK_BF16 ? 2 : 4; }
 
@@ -80,9 +81,9 @@ int check_rows(const void *logits, int dtype, int64_t ld, int T, int V, int max_
                     V, kMaxRows, max_V);
     if (T > 0 && !logits)
         return fail(SK_ERR_INVALID_ARG, "logits must be a non-NULL device pointer");
-    if (ld < V || ld > kMaxStride)
-        return fail(SK_ERR_INVALID_ARG, "rows of %d values cannot be %lld elements apart", V,
-                    (long long)ld);
+    if (ld < V || ld > kMaxStride || T * ld > kMaxSpan)
+        return fail(SK_ERR_INVALID_ARG, "%d rows of %d values cannot be %lld elements apart",
+                    T, V, (long long)ld);
     if ((uintptr_t)logits % elem(dtype))
         return fail(SK_ERR_INVALID_ARG, "logits are not aligned to their type");
     return SK_OK;
@@ -95,9 +96,9 @@ int check_grad(const void *logits, int64_t ld, const void *dlogits, int64_t dld,
     if (!dlogits || T == 0)
         return SK_OK;
     const int64_t size = (int64_t)elem(dtype);
-    if (dld < V || dld > kMaxStride)
-        return fail(SK_ERR_INVALID_ARG, "gradient rows of %d values cannot be %lld elements apart",
-                    V, (long long)dld);
+    if (dld < V || dld > kMaxStride || T * dld > kMaxSpan)
+        return fail(SK_ERR_INVALID_ARG, "%d gradient rows of %d values cannot be %lld elements apart",
+                    T, V, (long long)dld);
     if ((uintptr_t)dlogits % (uintptr_t)size)
         return fail(SK_ERR_INVALID_ARG, "dlogits are not aligned to their type");
     const int64_t a = (int64_t)(uintptr_t)logits, b = (int64_t)(uintptr_t)dlogits;

@@ -370,3 +370,12 @@ print("done")
     run = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True,
                          env=dict(os.environ, HIP_VISIBLE_DEVICES="-1"))
     assert run.returncode == 0 and run.stdout.split() == ["done"], run
+
+
+@pytest.mark.parametrize("name", GRADS)
+def test_matrices_beyond_the_address_space_are_refused(lib, name):
+    """2^24 rows 2^38 elements apart end where they begin, modulo 2^64 bytes."""
+    far = dict(_placed(dict(AT, logits=1 << 40, dlogits=(1 << 40) + 128)), T=1 << 24)
+    for changes in (dict(ld=1 << 38, dld=1 << 38), dict(dld=1 << 38)):
+        assert _call(lib, name, dict(far, **changes)) == sk.SK_ERR_INVALID_ARG
+        assert b"elements apart" in lib.sinkhorn_last_error(), lib.sinkhorn_last_error()
