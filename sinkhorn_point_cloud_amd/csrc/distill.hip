@@ -167,20 +167,26 @@ struct RowScalars {
 template <typename Src>
 __device__ __forceinline__ bool link(const List &l, const Src &src, int K)
 {
-    bool twice = false;
     for (int k = lane_id(); k < K; k += kWave) {
         // without probability: the dense value is the entry's own (a list padded with
         // one token and -inf is no list of duplicates)
         const int v = l.token[k];
         const int who = l.p[k] != 0.0 ? src.owner(v) : -1;
+        int before = -1;
         if (who >= 0) {
-            const int before = atomicExch(&l.head[who], k);
-            l.next[k] = before;
+            before = atomicExch(&l.head[who], k);
             atomicOr(&l.mark[who], 1 << (src.turn(v) & 31));
-            // every pair of a linked list's entries is met once
-            for (int j = before; j >= 0; j = l.next[j])
-                twice |= l.token[j] == v;
         }
+        l.next[k] = before;
+    }
+    // the walks below, and what follows them, read other lanes' entries
+    rows::wave_fence();
+    bool twice = false;
+    for (int k = lane_id(); k < K; k += kWave) {
+        const int v = l.token[k];
+        // every pair of a linked list's entries is met once
+        for (int j = l.next[k]; j >= 0; j = l.next[j])
+            twice |= l.token[j] == v;
     }
     return __any(twice);
 }

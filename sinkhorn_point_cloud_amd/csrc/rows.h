@@ -163,6 +163,14 @@ template <typename T, int NT> struct Slice {
     __device__ __forceinline__ int turn(int v) const { return ((v - cut.head) / n - c0) / NT; }
 };
 
+// What the lanes of a wave wrote to memory before it, all of them see behind it.  (A
+// wave's accesses to LDS stay in order; this keeps the compiler from moving them.)
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Reductions over a wave without LDS: over each row of 16 lanes by lane moves,
 // then the four rows through scalar registers, in a fixed order.  All lanes
 // active; every lane gets the result.

@@ -194,3 +194,25 @@ def test_no_gradient_into_a_buffer_that_is_not_asked_for():
         assert got[-1] is None and (d == 7).all(), call
         for a, b in zip(got[:-1], want[:-1]):
             assert torch.equal(a, b), call
+
+
+@pytest.mark.parametrize("V,K", [(40, 1024), (1500, 1024), (30011, 700), (70001, 129)])
+def test_lists_full_of_repeated_tokens(V, K):
+    """Entries of one token dealt to all lanes in turn, among others without probability: every one
+    of them is found, and each call finds the same."""
+    g = torch.Generator().manual_seed(V + K)
+    T = 9
+    z = torch.randn(T, V, generator=g)
+    few = torch.randint(0, V, (T, 7), generator=g)
+    idx = few.gather(1, torch.randint(0, 7, (T, K), generator=g)).int()
+    idx[1] = torch.randint(0, V, (K,), generator=g)
+    idx[2, ::5] = -1
+    u = torch.randn(T, K, generator=g)
+    u[3, ::3] = -math.inf
+    args = (z.cuda(), idx.cuda(), u.cuda())
+    got, want = sk.distill_loss(*args), F.distill(*args)
+    F.check(got[0], want[0], "loss")
+    F.check(got[1], want[1], "dlogits")
+    for _ in range(3):
+        again = sk.distill_loss(*args)
+        assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
