@@ -20,7 +20,8 @@ size_t elem(int dtype) { return dtype == SK_BF16 ? 2 : 4; }
 
 struct Ws {
     TokenWs token{};
-    float2 *info = nullptr, *term = nullptr;
+    PolicyRow *info = nullptr;
+    double2 *term = nullptr;
     RowStat *stat = nullptr;
     float *coef = nullptr, *zk = nullptr;
     BalanceWs balance{};
@@ -47,8 +48,8 @@ Ws carve(Carve &c, int op, int T, int V, int k, int dtype)
             w.token.zlab = c.take<float>(rows);
     }
     if (op == SK_OP_POLICY_LOSS) {
-        w.info = c.take<float2>(rows);
-        w.term = c.take<float2>(rows);
+        w.info = c.take<PolicyRow>(rows);
+        w.term = c.take<double2>(rows);
     } else if (op == SK_OP_PREFERENCE_LOSS) {
         w.stat = c.take<RowStat>(rows);
         w.coef = c.take<float>(rows);

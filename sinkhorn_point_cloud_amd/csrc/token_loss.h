@@ -58,12 +58,18 @@ hipError_t launch_logp(const LogitRows &r, const int32_t *labels, const Packed &
 // dlogits = G_t scale (1[v = label] - softmax), the softmax found on the way
 hipError_t launch_logp_backward(const LogitRows &r, const int32_t *labels, const float *G,
                                 const TokenWs &w, hipStream_t st);
+
+// What a row needs of its sequence: its weight there, and the advantage.
+struct PolicyRow {
+    double w;
+    float adv;
+};
 struct PolicyArgs {
     const float *old, *ref, *adv, *weights;
     int adv_per_token, mean;
     double lo, hi, log_lo, log_hi, kl;
-    float2 *info;   // [T] scratch: row weight and advantage, where they are found beforehand
-    float2 *term;   // [T] scratch: weighted loss and KL of a row
+    PolicyRow *info;   // [T] scratch, where it is found beforehand
+    double2 *term;     // [T] scratch: weighted loss and KL of a row
     float *loss, *kl_out, *logp;
 };
 hipError_t launch_policy(const LogitRows &r, const int32_t *labels, const Packed &p,

@@ -173,20 +173,11 @@ __device__ __forceinline__ KlTerm kl_term(double g)
     return KlTerm{over, over + g};
 }
 
-// e^x to fp32 precision in the range of fp64: a ratio beyond fp32's range times an
-// advantage of 0 is 0.
-__device__ __forceinline__ double exp_of(double x)
-{
-    double y = x * kLog2eD;
-    y = y > 1100.0 ? 1100.0 : y < -1100.0 ? -1100.0 : y;   // NaN stays
-    const double whole = __builtin_rint(y);
-    return __builtin_amdgcn_ldexp((double)ex2((float)(y - whole)), y == y ? (int)whole : 0);
-}
-
 struct PolicyMode {
     static constexpr bool kGradient = true;
     struct Row {
-        float w, adv, old, ref;   // row weight, advantage, given log-probabilities
+        double w;              // row weight
+        float adv, old, ref;   // advantage, given log-probabilities
     };
     // Every thread of the work-group, while the row's loads are in flight: what the
     // scalar phase needs is there when it begins.
@@ -196,8 +187,8 @@ struct PolicyMode {
         const PolicyArgs &q = a.pol;
         const float old = q.old[t], ref = q.ref ? q.ref[t] : 0.f;
         if (!a.fold) {
-            const float2 info = q.info[t];
-            return Row{info.x, info.y, old, ref};
+            const PolicyRow info = q.info[t];
+            return Row{info.w, info.adv, old, ref};
         }
         const int lane = lane_id(), i = seq_of(a.p, t);
         double w = q.weights ? (double)q.weights[i] : 1.0;
@@ -215,20 +206,20 @@ struct PolicyMode {
             }
             w = n ? w / (double)n : 0.0;
         }
-        return Row{(float)w, q.adv[q.adv_per_token ? t : i], old, ref};
+        return Row{w, q.adv[q.adv_per_token ? t : i], old, ref};
     }
     __device__ __forceinline__ static RowScalars row(const LabelArgs &a, long t, const Row &info,
                                                      float M, double R, float zy, bool writes)
     {
         const PolicyArgs &q = a.pol;
         // without a distribution, or weighted out: no part, whatever the row holds
-        const bool empty = row_empty(M, R), none = empty || info.w == 0.f;
-        const double s = a.r.scale, w = (double)info.w;
+        const bool empty = row_empty(M, R), none = empty || info.w == 0.0;
+        const double s = a.r.scale, w = info.w;
         const float adv = info.adv;
         const double logp = ((double)zy - (double)M) * s - row_ln(M, R);
         // the clipping decision is taken on the log-ratio, in fp64
         const double change = logp - (double)info.old;
-        const double ratio = exp_of(change);
+        const double ratio = exp2_fine(change * kLog2eD);
         const bool above = adv > 0.f && change > q.log_hi;
         const bool below = adv < 0.f && change < q.log_lo;
         const double gain = (above ? q.hi : below ? q.lo : ratio) * (double)adv;
@@ -245,9 +236,7 @@ struct PolicyMode {
         if (writes && lane_id() == 0) {
             if (q.logp)
                 q.logp[t] = empty ? 0.f : (float)logp;
-            q.term[t] = none ? make_float2(0.f, 0.f)
-                             : make_float2((float)(w * (cost - gain)),
-                                           (float)(w * kl));
+            q.term[t] = none ? make_double2(0.0, 0.0) : make_double2(w * (cost - gain), w * kl);
         }
         RowScalars k = coefficients(slope * w * s, logp, M, R);
         k.zero = none;
@@ -257,7 +246,7 @@ struct PolicyMode {
     {
         if (a.pol.logp)
             a.pol.logp[t] = 0.f;
-        a.pol.term[t] = make_float2(0.f, 0.f);
+        a.pol.term[t] = make_double2(0.0, 0.0);
     }
 };
 
@@ -414,7 +403,7 @@ __global__ __launch_bounds__(kSeqThreads) void policy_rows_kernel(const int32_t 
         w = n[0] > 0.0 ? w / n[0] : 0.0;
     }
     for (long t = r.first + threadIdx.x; t < r.last; t += kSeqThreads)
-        a.info[t] = make_float2((float)w, a.adv[a.adv_per_token ? t : i]);
+        a.info[t] = PolicyRow{w, a.adv[a.adv_per_token ? t : i]};
 }
 
 __global__ __launch_bounds__(kSeqThreads) void policy_sum_kernel(Packed p, long T, PolicyArgs a)
@@ -424,9 +413,9 @@ __global__ __launch_bounds__(kSeqThreads) void policy_sum_kernel(Packed p, long 
     const SeqRange r = seq_range(p, i, T);
     double v[2] = {0.0, 0.0};
     for (long t = r.first + threadIdx.x; t < r.last; t += kSeqThreads) {
-        const float2 k = a.term[t];
-        v[0] += (double)k.x;
-        v[1] += (double)k.y;
+        const double2 k = a.term[t];
+        v[0] += k.x;
+        v[1] += k.y;
     }
     group_sum<2>(v, room);
     if (threadIdx.x == 0) {

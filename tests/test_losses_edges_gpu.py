@@ -216,3 +216,24 @@ def test_lists_full_of_repeated_tokens(V, K):
     for _ in range(3):
         again = sk.distill_loss(*args)
         assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+
+
+@pytest.mark.parametrize("T,n,V", [(24, 1, 900), (24, 1, 20001), (24, 1, 70001), (2400, 70, 900),
+                                   (3001, 3, 4000)])
+def test_a_policy_loss_of_terms_that_cancel(T, n, V):
+    """Advantages of +1 and -1 over ratios that differ by 1e-6.  A ratio is off by 3e-10 of itself (its
+    exponential) and the log-probability's 2^-44, weights, terms and sums are fp64, and the loss is
+    rounded once."""
+    g = torch.Generator().manual_seed(T + V)
+    z, y = even(T, V)
+    half = -1.5 + 1.7 * torch.rand(T // 2 + 1, generator=g)
+    old = half.repeat_interleave(2)[:T] + torch.tensor([0.0, 1e-6]).repeat(T // 2 + 1)[:T]
+    adv = torch.tensor([1.0, -1.0]).repeat(T // 2 + 1)[:T]
+    off = torch.arange(n + 1) * T // n
+    w = 0.1 + torch.rand(n, generator=g)
+    kw = dict(clip=(0.99, math.inf), weights=w.cuda())
+    loss = sk.policy_loss(z, y, off.cuda(), old.cuda(), adv.cuda(), **kw)[0]
+    r = torch.exp(-math.log(2.0) - old.double())
+    sums = lambda v: torch.stack([v[a:b].mean() for a, b in F.ranges(off, T)]) * w.double()  # noqa: E731
+    want = sums(-r * adv.double())
+    F.check(loss, (want, sums(r) * (3e-10 + 2.0 ** -40) + U * want.abs()), "loss")
