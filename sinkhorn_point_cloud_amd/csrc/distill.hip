@@ -167,25 +167,25 @@ struct RowScalars {
 template <typename Src>
 __device__ __forceinline__ bool link(const List &l, const Src &src, int K)
 {
-    for (int k = lane_id(); k < K; k += kWave) {
-        // without probability: the dense value is the entry's own (a list padded with
-        // one token and -inf is no list of duplicates)
-        const int v = l.token[k];
-        const int who = l.p[k] != 0.0 ? src.owner(v) : -1;
-        int before = -1;
-        if (who >= 0) {
-            before = atomicExch(&l.head[who], k);
-            atomicOr(&l.mark[who], 1 << (src.turn(v) & 31));
-        }
-        l.next[k] = before;
-    }
-    // the walks below, and what follows them, read other lanes' entries
-    rows::wave_fence();
     bool twice = false;
-    for (int k = lane_id(); k < K; k += kWave) {
-        const int v = l.token[k];
+    for (int first = 0; first < K; first += kWave) {
+        const int k = first + lane_id();
+        int v = -1, before = -1;
+        if (k < K) {
+            v = l.token[k];
+            // without probability: the dense value is the entry's own (a list padded with
+            // one token and -inf is no list of duplicates)
+            const int who = l.p[k] != 0.0 ? src.owner(v) : -1;
+            if (who >= 0) {
+                before = atomicExch(&l.head[who], k);
+                l.next[k] = before;
+                atomicOr(&l.mark[who], 1 << (src.turn(v) & 31));
+            }
+        }
+        // the walk, and what follows it, reads other lanes' entries
+        rows::wave_fence();
         // every pair of a linked list's entries is met once
-        for (int j = l.next[k]; j >= 0; j = l.next[j])
+        for (int j = before; j >= 0; j = l.next[j])
             twice |= l.token[j] == v;
     }
     return __any(twice);
