@@ -145,32 +145,26 @@ struct BackwardMode {
     __device__ __forceinline__ static void unused(const LabelArgs &, long) {}
 };
 
-// The KL term e^g - 1 - g and its slope e^g - 1, in fp64 and its range: the term is a
-// multiple of e^g for a label that the reference finds likely, and after weights it
-// may be an ordinary number where e^g is beyond fp32.  Near 0 the series, where the
-// difference would cancel (|g| < 1: the first term left out, g^12/12!, is below
-// 2^-27 of the value).
+// The KL term e^g - 1 - g and its slope e^g - 1 from g and e = e^g, in fp64 and its
+// range: the term is a multiple of e^g for a label that the reference finds likely,
+// and after weights it may be an ordinary number where e^g is beyond fp32.  Near 0
+// the series, where the difference would cancel (|g| < 0.35: the first term left out,
+// 2 g^7/9!, is below 2^-27 of the value, as is beyond it what e, off by 3e-10, leaves).
 struct KlTerm {
     double over, slope;
 };
-__device__ __forceinline__ KlTerm kl_term(double g)
+__device__ __forceinline__ KlTerm kl_term(double g, double e)
 {
-    if (!(fabs(g) < 1.0)) {
-        const double e = exp2_fine(g * kLog2eD);
-        return KlTerm{e == (double)kInf ? e : e - 1.0 - g, e - 1.0};   // a label of probability 0
-    }
-    double r = 1.0 / 39916800.0;
-    r = fma(r, g, 1.0 / 3628800.0);
-    r = fma(r, g, 1.0 / 362880.0);
-    r = fma(r, g, 1.0 / 40320.0);
-    r = fma(r, g, 1.0 / 5040.0);
-    r = fma(r, g, 1.0 / 720.0);
-    r = fma(r, g, 1.0 / 120.0);
-    r = fma(r, g, 1.0 / 24.0);
-    r = fma(r, g, 1.0 / 6.0);
+    double r = 1.0 / 40320;
+    r = fma(r, g, 1.0 / 5040);
+    r = fma(r, g, 1.0 / 720);
+    r = fma(r, g, 1.0 / 120);
+    r = fma(r, g, 1.0 / 24);
+    r = fma(r, g, 1.0 / 6);
     r = fma(r, g, 0.5);
-    const double over = r * g * g;
-    return KlTerm{over, over + g};
+    const double near = r * g * g;
+    const double far = e == (double)kInf ? e : e - 1.0 - g;   // infinite: a label of probability 0
+    return fabs(g) < 0.35 ? KlTerm{near, near + g} : KlTerm{far, e - 1.0};
 }
 
 struct PolicyMode {
@@ -219,14 +213,17 @@ struct PolicyMode {
         const double logp = ((double)zy - (double)M) * s - row_ln(M, R);
         // the clipping decision is taken on the log-ratio, in fp64
         const double change = logp - (double)info.old;
-        const double ratio = exp2_fine(change * kLog2eD);
+        const double gap = (double)info.ref - logp;
+        // the ratio's exponential in one half of the lanes, the KL term's in the other
+        const double e = exp2_fine((lane_id() < kWave / 2 ? change : gap) * kLog2eD);
+        const double ratio = read_lane(e, 0);
         const bool above = adv > 0.f && change > q.log_hi;
         const bool below = adv < 0.f && change < q.log_lo;
         const double gain = (above ? q.hi : below ? q.lo : ratio) * (double)adv;
         double slope = above || below ? 0.0 : -ratio * (double)adv;   // d(-gain)/d logp
         double kl = 0.0, cost = 0.0;
         if (q.ref) {
-            const KlTerm k = kl_term((double)info.ref - logp);
+            const KlTerm k = kl_term(gap, read_lane(e, kWave - 1));
             kl = k.over;
             if (q.kl != 0.0) {   // only reported else, and it may be infinite
                 cost = q.kl * kl;
