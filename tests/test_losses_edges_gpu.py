@@ -237,3 +237,52 @@ def test_a_policy_loss_of_terms_that_cancel(T, n, V):
     sums = lambda v: torch.stack([v[a:b].mean() for a, b in F.ranges(off, T)]) * w.double()  # noqa: E731
     want = sums(-r * adv.double())
     F.check(loss, (want, sums(r) * (3e-10 + 2.0 ** -40) + U * want.abs()), "loss")
+
+
+@pytest.mark.parametrize("scale", [1.0, math.log(2.0) * (1 + 2.0 ** -24)])
+@pytest.mark.parametrize("T,V,dt", [(1000, 32000, torch.float32), (1000, 32000, torch.bfloat16),
+                                    (256, 131072, torch.bfloat16), (128, 70001, torch.float32)])
+def test_log_probabilities_to_their_own_precision(T, V, dt, scale):
+    """A pair's reward is logp - ref before it is rounded; with ref the fp32 value of logp it shows
+    each row's error to 1e-13.  Logits of deviation 2: at scale 1 a row's sum is shared by about
+    V e^-4 terms (580 at least) that lie 4.4 nats below its maximum in the mean.
+
+    Roundings, root mean square, relative to the sum: a term's exponential (2^-23 / sqrt 3) and
+    argument (two of half a unit at 6.3, 2^-22 / sqrt 3 ln 2 each) over the root of the number of
+    terms, 6e-9; a thread's 32 to 128 additions (2^-24 / sqrt 3 each, half of that on the mean of a
+    growing sum) over the root of 256 to 1024 threads, 6e-9; sums of 16 lanes, 4 additions each,
+    over the root of 64, 6e-9.  Together 1.1e-8; the exponential's mean error, of one sign, is given
+    1e-8 more.  So 2.1e-8 is allowed, for the mean error and the deviation alike.
+
+    At the scale that makes c = s log2 e = 1 + 2^-24 the arguments are not rounded at random: d, an
+    fp32 number of mantissa m in [1, 2), times c lies m / 2 of its unit beyond d and is always
+    rounded outwards, by 1 - m / 2 units: 2^-24 (2 / m - 1) of itself.  The mean of that over the
+    row's terms, each by its share of the sum, is of one sign and allowed too.
+
+    One fp32 number for the scale would be off by more: 1.3e-8 of each argument at scale 1, 2^-24 at
+    the other, with one sign.  The oracle with that mistake planted must be refused."""
+    g = torch.Generator().manual_seed(T + V)
+    z = (2 * torch.randn(T, V, generator=g)).to(dt)
+    y = torch.randint(0, V, (T,), generator=g, dtype=torch.int32)
+
+    def exact(s):
+        x = z.double() - z.double().amax(1, keepdim=True)
+        return scale * x.gather(1, y.long()[:, None])[:, 0] - torch.logsumexp(s * x, 1)
+
+    lp = exact(scale)
+    ref = lp.float()
+    reward = sk.preference_loss(z.cuda(), y.cuda(), torch.arange(T + 1).cuda(), ref.cuda(), beta=1.0,
+                                scale=scale, grad=False)[1]
+    wrong = reward.cpu().double() - (lp - ref.double())
+    allowed = 2.1e-8
+    if scale != 1.0:
+        x = z.double()
+        d = x.amax(1, keepdim=True) - x
+        m = 2 * torch.frexp(d).mantissa
+        outwards = torch.where(d > 0, 2.0 ** -24 * (2 / m - 1) * d * scale, 0.0)
+        allowed += (torch.softmax(x * scale, 1) * outwards).sum(1).mean().item()
+    print("allowed", allowed, "mean", wrong.mean().item(), "rms", wrong.square().mean().sqrt().item())
+    assert wrong.mean().abs() <= allowed and wrong.square().mean().sqrt() <= allowed
+    one_piece = float(torch.tensor(scale / math.log(2.0)).float()) * math.log(2.0)
+    planted = (exact(one_piece) - lp).mean().abs()
+    assert planted > allowed and (scale != 1.0 or planted > 2 * allowed)
