@@ -379,3 +379,75 @@ def test_matrices_beyond_the_address_space_are_refused(lib, name):
     for changes in (dict(ld=1 << 38, dld=1 << 38), dict(dld=1 << 38)):
         assert _call(lib, name, dict(far, **changes)) == sk.SK_ERR_INVALID_ARG
         assert b"elements apart" in lib.sinkhorn_last_error(), lib.sinkhorn_last_error()
+
+
+# --- offsets that the documentation does not allow
+
+def _bits(T):
+    """Chunk sizes of the balance loss, as powers of two (to count, for the gradient)."""
+    return (max(8, (T // 128 + 1).bit_length() - 1), max(4, (T // 1024 + 1).bit_length() - 1))
+
+
+def _place(off, T, chunk, bits, count_bits):
+    """A work-group's search for its chunk, as balance.hip does it with the 64 lanes of a wave;
+    every index it reads is checked.  (group, first, last, first counting chunk, how many)."""
+    G = len(off) - 1
+    row = lambda i: min(max(off[i], 0), T)  # noqa: E731
+    g, count = 0, G
+    while True:
+        step = (count + 63) // 64
+        at = [min(g + lane * step, G) for lane in range(64)]
+        begun = [g + lane * step < g + count and at[lane] + (row(at[lane]) >> bits) <= chunk
+                 for lane in range(64)]
+        lane = max(sum(begun) - 1, 0)
+        g += lane * step
+        assert 0 <= g < G
+        if step == 1:
+            b = row(at[lane])
+            e = max(row(at[lane + 1]) if lane + 1 < 64 else row(g + 1), b)
+            break
+        count = min(step, count - lane * step)
+        assert count >= 1
+    chunks = lambda rows, k: (rows + (1 << k) - 1) >> k  # noqa: E731
+    i = chunk - (g + (b >> bits))
+    if i < 0 or i >= chunks(e - b, bits):
+        return None
+    first = b + (i << bits)
+    return (g, first, min(first + (1 << bits), e), g + (b >> count_bits), chunks(e - b, count_bits))
+
+
+@pytest.mark.parametrize("seed", range(6))
+@pytest.mark.parametrize("ordered", [True, False])
+def test_balance_chunks_stay_in_bounds(seed, ordered):
+    """Whatever the offsets hold, no chunk lies outside the rows, the groups or the partial counts and
+    sums; in order, every row of every group is in one chunk of it, once."""
+    g = np.random.default_rng(seed)
+    T = int(g.integers(1025, 300000))
+    G = int(g.choice([1, 2, 63, 64, 65, 200, 5000]))
+    off = g.integers(-1000, T + 1000, G + 1)
+    if ordered:
+        off = np.sort(off.clip(0, T))
+    elif seed % 2:
+        off[g.integers(0, G + 1, 3)] = [2 ** 40, -2 ** 62, 2 ** 62]
+    off = [int(v) for v in off]
+    cb, gb = _bits(T)
+    for bits in (cb, gb):
+        total = (T >> bits) + G
+        seen = 0
+        for chunk in range(total):
+            place = _place(off, T, chunk, bits, cb)
+            if place is None:
+                continue
+            group, first, last, count0, counts = place
+            assert 0 <= group < G and 0 <= first < last <= T
+            assert 0 <= count0 < (T >> cb) + G
+            # the gradient's cap on what it reads of the partial counts
+            assert min(counts, (T >> cb) + G - count0) >= 1
+            if ordered:
+                assert off[group] <= first and last <= off[group + 1]
+                assert count0 + counts <= (T >> cb) + G
+                seen += last - first
+        if ordered:
+            assert seen == off[-1] - off[0]
+    for grp in range(G):    # the sums' launch
+        assert 0 <= grp + (min(max(off[grp], 0), T) >> gb) < (T >> gb) + G

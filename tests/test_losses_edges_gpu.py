@@ -286,3 +286,38 @@ def test_log_probabilities_to_their_own_precision(T, V, dt, scale):
     one_piece = float(torch.tensor(scale / math.log(2.0)).float()) * math.log(2.0)
     planted = (exact(one_piece) - lp).mean().abs()
     assert planted > allowed and (scale != 1.0 or planted > 2 * allowed)
+
+
+@pytest.mark.parametrize("T,V,n", [(40, 200, 4), (5000, 40, 130), (9000, 260, 300)])
+def test_offsets_out_of_order_write_nothing_outside(T, V, n):
+    """Not a call the documentation allows: outputs and workspace between guards, which stay."""
+    g = torch.Generator().manual_seed(T)
+    z = torch.randn(T, V, generator=g).cuda()
+    y = torch.randint(0, V, (T,), generator=g, dtype=torch.int32).cuda()
+    x = torch.zeros(T).cuda()
+    pad = 4096
+    kept = []
+
+    def guarded(*shape, dtype=torch.float32):
+        size = math.prod(shape)
+        buf = torch.full((size + 2 * pad,), 77, dtype=dtype, device="cuda")
+        kept.append((buf, size))
+        return buf[pad:pad + size].view(shape)
+
+    far = torch.randint(-T, 2 * T, (n + 1,), generator=g)
+    far[1], far[-1] = 2 ** 40, -2 ** 62
+    for off in (torch.randint(0, T + 1, (n + 1,), generator=g), far, torch.arange(n, -1, -1) * (T // n)):
+        off = off.cuda()
+        sizes = (sk.losses_workspace_bytes(1, T, V, 0, 0), sk.losses_workspace_bytes(2, T, V, 0, 0),
+                 sk.losses_workspace_bytes(4, T, V, n, 0))
+        ws = [guarded(s, dtype=torch.uint8) for s in sizes]
+        sk.policy_loss(z, y, off, x, x, out=(guarded(n), guarded(n), guarded(T), guarded(T, V)),
+                       workspace=ws[0])
+        sk.preference_loss(z, y, off, workspace=ws[1],
+                           out=(guarded(n // 2), guarded(n), guarded(T), guarded(T, V)))
+        sk.balance_loss(z, y[:, None], off, workspace=ws[2],
+                        out=(guarded(n), guarded(n), guarded(n, V, dtype=torch.int32), guarded(T, V)))
+        torch.cuda.synchronize()
+        for buf, size in kept:
+            assert (buf[:pad] == 77).all() and (buf[pad + size:] == 77).all()
+        kept.clear()
