@@ -36,10 +36,18 @@
  *     their sum.  A sequence, pair or row of weight 0 has loss (and KL) 0 and
  *     gradient 0, whatever its rows hold; the log-probabilities and rewards of a
  *     sequence or pair are reported all the same.
- *   - Exponentials are fp32, and so are a thread's sums of them; their joins,
- *     logarithms, ratios, clipping decisions and sums over rows are fp64.  Each output is rounded once.  Same inputs at the
- *     same addresses modulo 128 bytes, same bits: no result depends on an order
- *     of atomics.
+ *   - Precision.  The exponentials of a row of logits are fp32, and so are the
+ *     sums of a thread and of 16 lanes; the joins of those, logarithms,
+ *     log-probabilities, ratios and KL terms, clipping decisions, row weights and
+ *     sums over rows are fp64, and a loss is rounded once.  A log-probability is
+ *     off by about 1e-8 before it is rounded (up to 1e-7 where the scale puts
+ *     log2(e) scale right above a power of two).  A gradient value is an fp32
+ *     coefficient times an fp32 exponential, rounded to the logits' type.  A
+ *     teacher's probabilities come from fp32 exponentials.  The balance loss is fp32
+ *     within a row (softmax, f . p, log-sum-exp: off by 1e-7 of themselves) and
+ *     fp64 over rows.
+ *   - Same inputs at the same addresses modulo 128 bytes, same bits: no result
+ *     depends on an order of atomics.
  *   - Every call enqueues kernels only and returns without waiting; it can be
  *     captured in a graph.  Calls that overlap need workspaces of their own,
  *     and a captured call's workspace has to outlive its graph.

@@ -367,9 +367,9 @@ __device__ __forceinline__ double row_ln(float M, double R)
     return M == kInf ? __builtin_nan("") : ln_sum(R);
 }
 
-// ln(1 + R) to fp64 precision: 2 artanh(t), t = R / (2 + R), or for larger R the
+// ln(1 + R) to 2^-44 of itself: 2 artanh(t), t = R / (2 + R), or for larger R the
 // same for the sum's mantissa m between sqrt(1/2) and sqrt(2), t = (m - 1) /
-// (m + 1).  |t| <= 0.172: the first term left out, t^17/17, is below 2^-47 t.
+// (m + 1).  |t| <= 0.172: the first term left out, t^17/17, is below 2^-44 t.
 // (The library's logarithm, with its tables of extra precision, took several
 // times as long while the row's other waves waited.)
 __device__ __forceinline__ double ln_sum(double R)

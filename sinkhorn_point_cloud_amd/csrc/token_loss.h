@@ -41,7 +41,8 @@ struct TokenWs {
 };
 
 // What a row's statistics leave for a later pass: its maximum, the rest of its
-// sum and the label's log-probability before it is rounded.
+// sum (rounded to fp32, as the gradient's coefficient will be) and the label's
+// log-probability before it is rounded.
 struct RowStat {
     float M, R;
     double logp;
@@ -79,7 +80,7 @@ struct PreferenceArgs {
     const float *ref, *weights;
     int kind, mean;
     double beta, smoothing;
-    float *coef;    // [T] scratch: dloss/dlogp of a row
+    float *coef;    // [T] scratch: dloss/dlogp of a row, one rounding of the gradient's own
     RowStat *stat;  // [T] scratch
     float *loss, *reward, *logp;
 };

@@ -6,12 +6,13 @@
 //     logp = s (z_y - M) - ln(1 + R),        lse = s M + ln(1 + R),
 //     d logp / d z_v = -s q_v = -s e_v / (1 + R)  for v other than y,
 //                      -s expm1(logp)             for y.
-// Sums and maxima are fp32 over non-negative terms.  The log-probability is put
-// together in fp64 (off by about 1e-7) and so are its differences to given ones:
-// a ratio is clipped by the same decision as in 64 bits unless it is that near
-// the border.  Ratio and KL term are fp32 functions of those differences; a
-// double-precision exponential and logarithm, several hundred instructions in
-// one wave with the others waiting, cost 2 us a row.
+// Exponentials, maxima and a thread's sums are fp32, the sums' joins fp64.  The
+// log-probability is put together in fp64 (off by about 1e-8) and so are its
+// differences to given ones: a ratio is clipped by the same decision as in 64 bits
+// unless it is that near the border.  Ratio and KL term are short fp64 series of
+// those differences; the library's double-precision exponential and logarithm,
+// several hundred instructions in one wave with the others waiting, cost 2 us a row.
+// What the gradient pass takes up for every value (coefficient, maximum) is fp32.
 //
 // What bounds it: HBM.  A row is read once and its gradient written once.
 #include "rows.h"
