@@ -321,3 +321,20 @@ def test_offsets_out_of_order_write_nothing_outside(T, V, n):
         for buf, size in kept:
             assert (buf[:pad] == 77).all() and (buf[pad + size:] == 77).all()
         kept.clear()
+
+
+@pytest.mark.parametrize("T,E,K,G", [(40, 4, 2, 2), (500, 8, 2, 0), (3000, 8, 2, 3), (2000, 16, 2, 0),
+                                     (1500, 64, 6, 2), (1100, 256, 8, 2)])
+def test_balance_loss_within_its_own_additions(T, E, K, G, monkeypatch):
+    """The formulas' bound of a row's sum counts 100 additions, for rows of any length.  A router's row
+    is 16 lanes' of E / 16 values each, rounded up, and 4 additions between the lanes."""
+    monkeypatch.setattr(F, "eps_sum", lambda V: U * (2 + 2.1 * math.log2(V) + -(-V // 16) + 4))
+    g = torch.Generator().manual_seed(T + E)
+    z = 2 * torch.randn(T, E, generator=g)
+    idx = z.topk(K, dim=1).indices.int()
+    off = torch.arange(G + 1) * T // G if G else None
+    got = sk.balance_loss(z.cuda(), idx.cuda(), off.cuda() if G else None, balance=0.3, z=0.02)
+    want = F.balance(z, idx, off, balance=0.3, z=0.02)
+    assert torch.equal(got[2].cpu(), want[2])
+    for k, name in ((0, "loss"), (1, "zloss"), (3, "dlogits")):
+        F.check(got[k], want[k], name)
