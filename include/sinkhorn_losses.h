@@ -44,8 +44,8 @@
  *     log2(e) scale right above a power of two).  A gradient value is an fp32
  *     coefficient times an fp32 exponential, rounded to the logits' type.  A
  *     teacher's probabilities come from fp32 exponentials.  The balance loss is fp32
- *     within a row (softmax, f . p, log-sum-exp: off by 1e-7 of themselves) and
- *     fp64 over rows.
+ *     within a row (softmax and f . p off by 1 to 2e-7 of themselves, a
+ *     log-sum-exp by as much of the row's maximum) and fp64 over rows.
  *   - Same inputs at the same addresses modulo 128 bytes, same bits: no result
  *     depends on an order of atomics.
  *   - Every call enqueues kernels only and returns without waiting; it can be
