@@ -13,6 +13,9 @@ Entry points (same names as the C ABI):
 Losses over rows of logits (include/sinkhorn_losses.h, module ``losses``):
   token_logprobs, token_logprobs_backward, policy_loss, preference_loss,
   distill_loss, balance_loss
+The output end of a model (include/sinkhorn_head.h, module ``head``):
+  rms_norm, rms_norm_int8, rms_norm_backward, quantize_int8, int8_linear,
+  token_scores, token_scores_backward
 """
 from __future__ import annotations
 
@@ -25,6 +28,8 @@ __all__ = ["SinkhornError", "potentials", "potentials_noalloc", "plan_coo", "los
            "workspace_bytes",
            "token_logprobs", "token_logprobs_backward", "policy_loss", "preference_loss",
            "distill_loss", "balance_loss", "losses_workspace_bytes",
+           "rms_norm", "rms_norm_int8", "rms_norm_backward", "quantize_int8", "int8_linear",
+           "token_scores", "token_scores_backward", "head_workspace_bytes",
            "library_path", "load_library"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -101,6 +106,7 @@ def load_library():
     lib.sinkhorn_last_error.argtypes = []
     lib.sinkhorn_last_error.restype = ctypes.c_char_p
     losses.declare(lib)
+    head.declare(lib)
     _lib = lib
     return lib
 
@@ -518,3 +524,6 @@ def hvp(X, Y, a, b, f, g, eps: float, V, cg_iters: int = 100, workspace=None, ou
 from . import losses  # noqa: E402
 from .losses import (LOSS_EXPORTS, balance_loss, distill_loss, losses_workspace_bytes,  # noqa: E402
                      policy_loss, preference_loss, token_logprobs, token_logprobs_backward)
+from . import head  # noqa: E402
+from .head import (HEAD_EXPORTS, head_workspace_bytes, int8_linear, quantize_int8,  # noqa: E402
+                   rms_norm, rms_norm_backward, rms_norm_int8, token_scores, token_scores_backward)

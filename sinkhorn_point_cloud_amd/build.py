@@ -25,11 +25,13 @@ ARCH = os.environ.get("SK_OFFLOAD_ARCH", "gfx950")
 CFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++20", "-fPIC", "-Wall", "-Wno-unused-function",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # MFMA accumulators in ordinary VGPRs (gfx950 has one register file): no
-    # copies through the accumulation registers on every tile
-    "-mllvm", "-amdgpu-mfma-vgpr-form",
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
+# MFMA accumulators in ordinary VGPRs (gfx950 has one register file): no
+# copies through the accumulation registers on every tile
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+# 256 accumulators a lane are more than ordinary VGPRs beside anything else
+ACCUMULATION_FORM = {"int8_linear.hip"}
 
 
 def hipcc() -> str:
@@ -42,7 +44,8 @@ def hipcc() -> str:
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-    cmd = [hipcc(), *CFLAGS, "-c", src, "-o", obj]
+    form = [] if os.path.basename(src) in ACCUMULATION_FORM else VGPR_FORM
+    cmd = [hipcc(), *CFLAGS, *form, "-c", src, "-o", obj]
     proc = subprocess.run(cmd, capture_output=True, text=True)
     if proc.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{proc.stderr}")

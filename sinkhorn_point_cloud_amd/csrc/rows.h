@@ -417,8 +417,9 @@ __device__ __forceinline__ float expm1_of(float g)
     return fmaf(r * g, g, g);
 }
 
-// coefficient x exponential of one row, out_v = A 2^((x_v - M) c + up), but for the
-// elements that have a value of their own.  Those are a `Terms` with
+// coefficient x exponential of one row, out_v = A 2^((x_v - M) c + up) (or another
+// at(x) of a caller's), but for the elements that have a value of their own.  Those
+// are a `Terms` with
 //     chunk(i, first, x): sets them in a thread's i-th chunk, whose first element is `first`,
 //     edge(v, y):         the value of element v of the edge, y if it has none.
 // `up` is 0 but for a coefficient beyond fp32, of which A is then the mantissa: the
@@ -481,6 +482,35 @@ template <typename T, int NT> struct Streamed : Slice<T, NT> {
 
     __device__ __forceinline__ void load() {}
 
+    // f(this thread's i-th, chunk, values) for each chunk, read from memory
+    template <bool First, typename F> __device__ __forceinline__ void each(F &&f) const
+    {
+        int i = S::c0 + (int)threadIdx.x, k = 0;
+        for (; i + (kUnroll - 1) * NT < S::c1; i += kUnroll * NT, k += kUnroll) {
+            u32x4 v[kUnroll];
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j)
+                v[j] = *S::chunk(i + j * NT);
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j) {
+                float x[n];
+                Pack<T>::open(v[j], x);
+                f(k + j, i + j * NT, x);
+            }
+        }
+        for (; i < S::c1; i += NT, ++k) {
+            float x[n];
+            Pack<T>::open(*S::chunk(i), x);
+            f(k, i, x);
+        }
+    }
+    // the thread's value of the edge, -inf without one
+    __device__ __forceinline__ float edge_value() const
+    {
+        const int t = threadIdx.x;
+        return S::has_edge(t) ? Pack<T>::get(S::row + S::edge_at(t)) : -kInf;
+    }
+
     __device__ __forceinline__ void stats(const Scale &c, float &m, float &s) const
     {
         const int t = threadIdx.x;
@@ -508,8 +538,8 @@ template <typename T, int NT> struct Streamed : Slice<T, NT> {
         }
     }
 
-    template <typename Terms>
-    __device__ __forceinline__ void dense(T *out, const Dense &d, const Terms &terms) const
+    template <typename D, typename Terms>
+    __device__ __forceinline__ void dense(T *out, const D &d, const Terms &terms) const
     {
         const int t = threadIdx.x;
         const bool aligned = (((uintptr_t)(out + S::cut.head)) & 15) == 0;
@@ -594,6 +624,7 @@ template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
             }
         }
     }
+    __device__ __forceinline__ float edge_value() const { return e; }
     // f(this thread's i-th, chunk, values) for each held chunk, then for those beyond
     template <bool First, typename F> __device__ __forceinline__ void each(F &&f) const
     {
@@ -644,8 +675,8 @@ template <typename T, int NT, int N, int L = 0> struct Held : Slice<T, NT> {
         const float x[1] = {e};
         absorb<1>(x, c, m, s);
     }
-    template <typename Terms>
-    __device__ __forceinline__ void dense(T *out, const Dense &d, const Terms &terms) const
+    template <typename D, typename Terms>
+    __device__ __forceinline__ void dense(T *out, const D &d, const Terms &terms) const
     {
         const int t = threadIdx.x;
         const bool aligned = (((uintptr_t)(out + S::cut.head)) & 15) == 0;

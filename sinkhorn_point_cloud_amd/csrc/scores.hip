@@ -1,0 +1,655 @@
+// scores.hip -- log-probability of a row's label, entropy and top alternatives of
+// rows of logits, and the gradient of the first two.
+//
+// With M the row maximum, e_v = 2^-y_v, y_v = (M - z_v) c, c = s log2(e), R the sum
+// of e_v but for one maximum and W the sum of e_v y_v:
+//     lse = s M + ln(1 + R),   logp = s (z_y - M) - ln(1 + R),
+//     H = ln(1 + R) + D,       D = ln 2 W / (1 + R), the mean of s (M - z),
+//     dH/dz_v = s q_v (s (M - z_v) - D),   q_v = e_v / (1 + R).
+// W is a sum of terms that are not negative, carried with the running maximum: when
+// it rises by g / c, W becomes 2^-g (W + g (R + 1)).  Both parts of H keep their
+// relative precision where one token has nearly all of the probability.
+//
+// The alternatives: the `top`-th largest of the threads' own maxima is a lower bound
+// of the row's `top`-th largest value, and little more than `top` values lie at or
+// above it (in random order about top + top^2 / 2 NT).  They are listed in shared
+// memory and ranked there by value and index, so the order in which they were listed
+// does not matter.  A row of which more do not fit (many equal values, or the large
+// ones all in one thread's chunks) has its `top`-th value found by bisection first.
+//
+// What bounds it: HBM.  A row is read once and kept on the chip for the second look.
+#include "head.h"
+#include "rows.h"
+
+namespace sk {
+namespace {
+
+using namespace rows;
+
+constexpr int kSplit = 256;      // threads of a work-group that shares its row with others
+constexpr int kRoom = 1024;      // values that can be listed
+constexpr float kFar = 1000.f;   // 2^-kFar is 0: stands for the distance of what has no probability
+
+// --- maximum, rest and weighted distance
+
+struct Stats {
+    float m = -kInf, r = 0.f, w = 0.f;
+};
+
+// (d c, clipped) for a difference d <= 0, negated
+__device__ __forceinline__ float distance(float d, const Scale &c)
+{
+    return min_of(-fmaf(d, c.hi, d * c.lo), kFar);   // NaN stays
+}
+
+// Takes K values in; as absorb(), with the weighted distance.
+template <int K>
+__device__ __forceinline__ void absorb(const float (&x)[K], const Scale &c, Stats &s)
+{
+    float low[K], top = x[0];
+#pragma unroll
+    for (int i = 1; i < K; ++i) {
+        low[i] = min_of(top, x[i]);
+        top = max_of(top, x[i]);
+    }
+    const float mn = max_of(s.m, top), at = shift_of(mn);
+    const float g = distance(min_of(s.m, top) - at, c), f = ex2(-g);
+    float sum = f, far = f * g;
+#pragma unroll
+    for (int i = 1; i < K; ++i) {
+        const float y = distance(low[i] - at, c), e = ex2(-y);
+        sum += e;
+        far = fmaf(e, y, far);
+    }
+    const bool rises = top > s.m;
+    s.w = rises ? fmaf(f, fmaf(g, s.r, s.w), far) : s.w + far;
+    s.r = fmaf(s.r, rises ? f : 1.f, sum);
+    s.m = mn;
+}
+
+// A part's (r, w) from its own maximum to the common one `top`.
+template <typename F>
+__device__ __forceinline__ void shift(F &r, F &w, F f, F g, bool holds)
+{
+    // its own maximum becomes an ordinary term, but for the one that is left out
+    w = holds ? w : f * fma(g, r + (F)1, w);
+    r = holds ? r : fma(r, f, f);
+}
+
+__device__ __forceinline__ ScorePart merge_lanes(float m, double r, double w, const Scale &c)
+{
+    const float top = max_wave(m);
+    const float d = m - shift_of(top);
+    const double y = -(double)d * ((double)c.hi + (double)c.lo);
+    const bool far = y >= (double)kFar;   // its 2^-y counts as 0, as an fp32 one is
+    const double g = far ? (double)kFar : y;
+    const bool holds = __ffsll(__ballot(m == top)) - 1 == lane_id();
+    shift(r, w, far ? 0.0 : exp2_fine(-g), g, holds);
+    return ScorePart{sum_wave(r), sum_wave(w), top};
+}
+
+// Of the whole work-group, in its first wave.  `room`: one entry per wave.  One barrier.
+template <int NT>
+__device__ __forceinline__ ScorePart merge_group(const Stats &s, const Scale &c, ScorePart *room)
+{
+    const float top = max_wave(s.m);
+    const float g = distance(s.m - shift_of(top), c), f = ex2(-g);
+    const bool holds = __ffsll(__ballot(s.m == top)) - 1 == lane_id();
+    float r = s.r, w = s.w;
+    shift(r, w, f, g, holds);
+    ScorePart p{sum_wave((double)r), sum_wave((double)w), top};
+    if constexpr (NT > kWave) {
+        constexpr int waves = NT / kWave;
+        if (lane_id() == 0)
+            room[threadIdx.x / kWave] = p;
+        __syncthreads();
+        if (threadIdx.x < kWave) {
+            const ScorePart v = lane_id() < waves ? room[lane_id()] : ScorePart{0.0, 0.0, -kInf};
+            p = merge_lanes(v.m, v.r, v.w, c);
+        }
+    }
+    return p;
+}
+
+__device__ __forceinline__ ScorePart merge_parts(const ScorePart *part, int parts, const Scale &c)
+{
+    const ScorePart v = lane_id() < parts ? part[lane_id()] : ScorePart{0.0, 0.0, -kInf};
+    return merge_lanes(v.m, v.r, v.w, c);
+}
+
+// --- the alternatives
+
+// Keys in the order of the values: -0 as 0, NaN above +inf.
+__device__ __forceinline__ uint32_t key_of(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return x != x ? 0xFFFFFFFFu : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+constexpr uint32_t kNoKey = 0x007FFFFFu;   // of -inf, which is no alternative
+__device__ __forceinline__ float value_of(uint32_t key)
+{
+    return key == 0xFFFFFFFFu ? __builtin_nanf("")
+                              : __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+// Value and index in one: the order of alternatives.  0: none.
+constexpr int kIndexBits = 24;
+__device__ __forceinline__ uint64_t entry_of(uint32_t key, int v)
+{
+    return (uint64_t)key << kIndexBits | (uint64_t)((1 << kIndexBits) - 1 - v);
+}
+
+template <int NT> struct ListRoom {
+    uint32_t keys[NT];
+    uint64_t entry[kRoom];
+    int count, wave[NT / kWave];
+};
+
+// The lower 16 bits cleared of the `top`-th largest of the NT keys in room.keys (0 if
+// there are not as many): by bisection, in the first wave; every lane of it has the result.
+template <int NT> __device__ __forceinline__ uint32_t nth_key(const uint32_t *keys, int top)
+{
+    constexpr int per = NT / kWave;
+    uint32_t k[per], found = 0;
+#pragma unroll
+    for (int i = 0; i < per; ++i)
+        k[i] = keys[i * kWave + lane_id()];
+    for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t with = found | 1u << bit;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < per; ++i)
+            n += __popcll(__ballot(k[i] >= with));
+        found = n >= top ? with : found;
+    }
+    return found;
+}
+
+// Sum of a count over the work-group, in every thread.  Two barriers.
+template <int NT> __device__ __forceinline__ int group_count(int n, int *wave)
+{
+    n = wave_sum(n);
+    if constexpr (NT == kWave)
+        return n;
+    __syncthreads();
+    if (lane_id() == 0)
+        wave[threadIdx.x / kWave] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int i = 0; i < NT / kWave; ++i)
+        n += wave[i];
+    return n;
+}
+
+// Appends what is wanted to the list; returns without writing beyond its room.
+template <int NT>
+__device__ __forceinline__ void append(ListRoom<NT> &room, bool wanted, uint64_t entry)
+{
+    if (wanted) {
+        const int at = atomicAdd(&room.count, 1);
+        if (at < kRoom)
+            room.entry[at] = entry;
+    }
+}
+
+// Lists the alternatives of a source: `scan(f)` calls f(key, index) for each value of
+// this thread, `most` is this thread's largest key.  Leaves at most kRoom entries in
+// room.entry, `top` of which at least are the largest (fewer where there are fewer).
+// Returns how many; the list is there for every thread.  `again` is as scan, but reads
+// memory: keys of values in registers would be kept in more of them between its turns.
+template <int NT, typename Scan, typename Again>
+__device__ __forceinline__ int list_top(ListRoom<NT> &room, int top, uint32_t most, Scan &&scan,
+                                        Again &&again)
+{
+    room.keys[threadIdx.x] = most;
+    if (threadIdx.x == 0)
+        room.count = 0;
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+        const uint32_t k = top <= NT ? nth_key<NT>(room.keys, top) : 0u;
+        if (threadIdx.x == 0)
+            room.keys[0] = max(k, kNoKey + 1);
+    }
+    __syncthreads();
+    const uint32_t border = room.keys[0];
+    scan([&](uint32_t key, int v) { append(room, key >= border, entry_of(key, v)); });
+    __syncthreads();
+    const int n = room.count;
+    if (n <= kRoom)
+        return n;
+    // more than fit: the `top`-th entry itself, a bit at a time (entries differ)
+    uint64_t least = 0;
+    for (int bit = 31 + kIndexBits; bit >= 0; --bit) {
+        const uint64_t with = least | 1ull << bit;
+        int c = 0;
+        again([&](uint32_t key, int v) { c += entry_of(key, v) >= with; });
+        if (group_count<NT>(c, room.wave) >= top)
+            least = with;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        room.count = 0;
+    __syncthreads();
+    again([&](uint32_t key, int v) {
+        const uint64_t e = entry_of(key, v);
+        append(room, e >= least, e);
+    });
+    __syncthreads();
+    return room.count;
+}
+
+// Calls put(place, entry) for the largest `top` of the n listed ones, each by the
+// thread that has counted how many are larger.
+template <int NT, typename Put>
+__device__ __forceinline__ void rank_list(const ListRoom<NT> &room, int n, int top, Put &&put)
+{
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const uint64_t e = room.entry[i];
+        int place = 0;
+        for (int j = 0; j < n; ++j)
+            place += room.entry[j] > e;
+        if (place < top)
+            put(place, e);
+    }
+}
+
+// A row's values as a source of list_top.
+template <typename T, typename Src, typename F>
+__device__ __forceinline__ void scan_row(const Src &src, F &&f)
+{
+    constexpr int n = Pack<T>::n;
+    if (src.has_edge(threadIdx.x))
+        f(key_of(src.edge_value()), src.edge_at(threadIdx.x));
+    src.template each<false>([&](int, int at, const float (&x)[n]) {
+        if (at < src.c1) {
+#pragma unroll
+            for (int k = 0; k < n; ++k)
+                f(key_of(x[k]), src.cut.head + at * n + k);
+        }
+    });
+}
+
+// --- a row's outputs
+
+struct Args {
+    ScoreArgs a;
+    int parts;
+    Scale c;
+};
+
+__device__ __forceinline__ bool row_used(const ScoreArgs &a, long t)
+{
+    return !a.labels || a.labels[t] >= 0;
+}
+
+// Writes an alternative, or what marks an empty place.
+__device__ __forceinline__ void put_best(const ScoreArgs &a, long t, int place, uint64_t e, double lse)
+{
+    const int v = (1 << kIndexBits) - 1 - (int)(e & ((1 << kIndexBits) - 1));
+    const float x = value_of((uint32_t)(e >> kIndexBits));
+    a.index[t * a.top + place] = v;
+    a.best[t * a.top + place] = (float)((double)x * a.scale - lse);
+}
+template <int NT> __device__ __forceinline__ void put_empty(const ScoreArgs &a, long t, int from)
+{
+    for (int i = from + (int)threadIdx.x; i < a.top; i += NT) {
+        a.index[t * a.top + i] = -1;
+        a.best[t * a.top + i] = -kInf;
+    }
+}
+template <int NT> __device__ __forceinline__ void put_unused(const ScoreArgs &a, long t)
+{
+    if (threadIdx.x == 0) {
+        if (a.logp)
+            a.logp[t] = 0.f;
+        if (a.lse)
+            a.lse[t] = 0.f;
+        if (a.entropy)
+            a.entropy[t] = 0.f;
+    }
+    put_empty<NT>(a, t, 0);
+}
+
+// One wave, the same in every lane; returns the log-sum-exp.
+__device__ __forceinline__ double put_scores(const ScoreArgs &a, long t, const ScorePart &p, float zy)
+{
+    const bool none = row_empty(p.m, p.r);
+    const double ln = row_ln(p.m, p.r), s = a.scale;
+    const double lse = (double)p.m * s + ln;
+    if (lane_id() == 0) {
+        if (a.logp)
+            a.logp[t] = none ? 0.f : (float)(((double)zy - (double)p.m) * s - ln);
+        if (a.lse)
+            a.lse[t] = none ? -kInf : (float)lse;
+        if (a.entropy)
+            a.entropy[t] = none ? 0.f : (float)(ln + kLn2D * p.w / row_sum(p.m, p.r));
+    }
+    return lse;
+}
+
+template <typename T> __device__ __forceinline__ float logit_at(const ScoreArgs &a, const T *row, long t)
+{
+    if (!a.labels)
+        return 0.f;
+    const int y = a.labels[t];
+    return y < a.V ? Pack<T>::get(row + y) : __builtin_nanf("");
+}
+
+// A work-group per row.
+template <typename T, int NT, typename Src, bool Top>
+__global__ __launch_bounds__(NT, Src::waves) void score_kernel(Args g)
+{
+    extern __shared__ u32x4 chunks[];   // [Src::lds_chunks]
+    __shared__ ScorePart room[NT / kWave];
+    __shared__ double row_lse;
+    const ScoreArgs &a = g.a;
+    const long t = group_index();
+    if (t >= a.T)
+        return;
+    if (!row_used(a, t)) {
+        put_unused<NT>(a, t);
+        return;
+    }
+    const T *row = (const T *)a.logits + t * a.ld;
+    Src src(row, a.V, 0, 1, chunks);
+    const float zy = logit_at(a, row, t);
+    src.load();
+    Stats s;
+    const float edge[1] = {src.edge_value()};
+    src.template each<true>([&](int, int, const float (&x)[Pack<T>::n]) { absorb<Pack<T>::n>(x, g.c, s); });
+    absorb<1>(edge, g.c, s);
+    const ScorePart p = merge_group<NT>(s, g.c, room);
+    if (threadIdx.x < kWave) {
+        const double lse = put_scores(a, t, p, zy);
+        if (threadIdx.x == 0)
+            row_lse = lse;
+    }
+    if constexpr (Top) {
+        __shared__ ListRoom<NT> list;
+        const int n = list_top<NT>(list, a.top, key_of(s.m),
+                                   [&](auto &&f) { scan_row<T>(src, f); },
+                                   [&](auto &&f) {
+                                       scan_row<T>(Streamed<T, NT>(row, a.V, 0, 1), f);
+                                   });
+        const double lse = row_lse;   // written before list_top's barriers
+        rank_list<NT>(list, n, a.top, [&](int place, uint64_t e) { put_best(a, t, place, e, lse); });
+        put_empty<NT>(a, t, n);
+    }
+}
+
+// Few rows: each over `parts` work-groups.
+template <typename T, bool Top> __global__ __launch_bounds__(kSplit) void part_kernel(Args g)
+{
+    __shared__ ScorePart room[kSplit / kWave];
+    const ScoreArgs &a = g.a;
+    const long t = group_index() / g.parts;
+    const int part = (int)(group_index() % g.parts);
+    if (t >= a.T || !row_used(a, t))
+        return;
+    if (a.dlogits && !(a.grad && a.grad[t] != 0.f) && !(a.grad_entropy && a.grad_entropy[t] != 0.f))
+        return;
+    const T *row = (const T *)a.logits + t * a.ld;
+    const Streamed<T, kSplit> src(row, a.V, part, g.parts);
+    Stats s;
+    const float edge[1] = {src.edge_value()};
+    src.template each<true>([&](int, int, const float (&x)[Pack<T>::n]) { absorb<Pack<T>::n>(x, g.c, s); });
+    absorb<1>(edge, g.c, s);
+    const ScorePart p = merge_group<kSplit>(s, g.c, room);
+    if (threadIdx.x == 0) {
+        a.part[t * g.parts + part] = p;
+        if (part == 0)
+            a.zlab[t] = logit_at(a, row, t);
+    }
+    if constexpr (Top) {
+        __shared__ ListRoom<kSplit> list;
+        auto scan = [&](auto &&f) { scan_row<T>(src, f); };
+        const int n = list_top<kSplit>(list, a.top, key_of(s.m), scan, scan);
+        uint64_t *out = a.list + (t * g.parts + part) * a.top;
+        rank_list<kSplit>(list, n, a.top, [&](int place, uint64_t e) { out[place] = e; });
+        for (int i = n + (int)threadIdx.x; i < a.top; i += kSplit)
+            out[i] = 0;
+    }
+}
+
+// Second launch: outputs from the merged parts.
+template <bool Top> __global__ __launch_bounds__(kSplit) void join_kernel(Args g)
+{
+    __shared__ double row_lse;
+    const ScoreArgs &a = g.a;
+    const long t = group_index();
+    if (t >= a.T)
+        return;
+    if (!row_used(a, t)) {
+        put_unused<kSplit>(a, t);
+        return;
+    }
+    if (threadIdx.x < kWave) {
+        const double lse = put_scores(a, t, merge_parts(a.part + t * g.parts, g.parts, g.c), a.zlab[t]);
+        if (threadIdx.x == 0)
+            row_lse = lse;
+    }
+    if constexpr (Top) {
+        __shared__ ListRoom<kSplit> list;
+        const uint64_t *in = a.list + t * g.parts * a.top;
+        const int all = g.parts * a.top;
+        auto scan = [&](auto &&f) {
+            for (int i = threadIdx.x; i < all; i += kSplit) {
+                const uint64_t e = in[i];
+                f((uint32_t)(e >> kIndexBits), (1 << kIndexBits) - 1 - (int)(e & ((1 << kIndexBits) - 1)));
+            }
+        };
+        uint32_t most = 0;
+        scan([&](uint32_t key, int) { most = max(most, key); });
+        const int n = list_top<kSplit>(list, a.top, most, scan, scan);
+        const double lse = row_lse;
+        rank_list<kSplit>(list, n, a.top, [&](int place, uint64_t e) { put_best(a, t, place, e, lse); });
+        put_empty<kSplit>(a, t, n);
+    }
+}
+
+// --- the gradient
+
+// out_v = 2^(up - y_v) (A + B y_v): A = -s (grad + grad_entropy D) / (1 + R) and B =
+// s ln 2 grad_entropy / (1 + R), divided by 2^up where they come near fp32's end.
+struct DenseScores {
+    float A, B, M, c, up;
+    __device__ __forceinline__ float at(float x) const
+    {
+        const float y = fminf((M - x) * c, kFar);
+        return ex2(up - y) * fmaf(B, y, A);
+    }
+};
+struct GradScalars {
+    DenseScores d;
+    float own;   // the label's value
+    int zero;
+};
+
+__device__ __forceinline__ GradScalars grad_scalars(const Args &g, long t, const ScorePart &p, float zy)
+{
+    const ScoreArgs &a = g.a;
+    const double s = a.scale, S = row_sum(p.m, p.r), D = kLn2D * p.w / S;
+    const double gl = a.grad ? (double)a.grad[t] : 0.0;
+    const double ge = a.grad_entropy ? (double)a.grad_entropy[t] : 0.0;
+    const double away = ((double)p.m - (double)zy) * s;   // the label's distance
+    const double logp = -away - row_ln(p.m, p.r);
+    double A = -s * (gl + ge * D) / S, B = s * kLn2D * ge / S;
+    // a label beyond the row makes its gradient NaN, if there is one
+    double own = -s * gl * (double)expm1_of((float)logp);
+    if (gl != 0.0 && logp != logp)
+        A = __builtin_nan("");
+    if (ge != 0.0 && zy != -kInf)
+        own += s * ge * exp2_fine(logp * kLog2eD) * (away - D);
+    const double most = fmax(fabs(A), fabs(B));
+    float up = 0.f;
+    if (most > 0x1p64 && most < __builtin_inf()) {
+        // what is left stays finite times any distance, and 2^up while the value does
+        const int e = __builtin_amdgcn_frexp_exp(most) - 64;
+        A = __builtin_amdgcn_ldexp(A, -e);
+        B = __builtin_amdgcn_ldexp(B, -e);
+        up = (float)e;
+    }
+    return GradScalars{{(float)A, (float)B, p.m, g.c.near, up}, (float)own, row_empty(p.m, p.r)};
+}
+
+__device__ __forceinline__ bool grad_used(const ScoreArgs &a, long t)
+{
+    return row_used(a, t) &&
+           ((a.grad && a.grad[t] != 0.f) || (a.grad_entropy && a.grad_entropy[t] != 0.f));
+}
+// the label where it has a value of its own
+__device__ __forceinline__ OneTerm own_term(const ScoreArgs &a, long t, float own)
+{
+    return OneTerm{a.grad && a.grad[t] != 0.f ? a.labels[t] : -1, own};
+}
+
+template <typename T, int NT, typename Src>
+__global__ __launch_bounds__(NT, Src::waves) void score_grad_kernel(Args g)
+{
+    extern __shared__ u32x4 chunks[];   // [Src::lds_chunks]
+    __shared__ ScorePart room[NT / kWave];
+    __shared__ GradScalars scal;
+    const ScoreArgs &a = g.a;
+    const long t = group_index();
+    if (t >= a.T)
+        return;
+    T *out = (T *)a.dlogits + t * a.dld;
+    if (!grad_used(a, t)) {
+        zero_row<T, NT>(out, a.V, 0, 1);
+        return;
+    }
+    const T *row = (const T *)a.logits + t * a.ld;
+    Src src(row, a.V, 0, 1, chunks);
+    const float zy = logit_at(a, row, t);
+    src.load();
+    Stats s;
+    const float edge[1] = {src.edge_value()};
+    src.template each<true>([&](int, int, const float (&x)[Pack<T>::n]) { absorb<Pack<T>::n>(x, g.c, s); });
+    absorb<1>(edge, g.c, s);
+    const ScorePart p = merge_group<NT>(s, g.c, room);
+    if (threadIdx.x < kWave) {
+        const GradScalars k = grad_scalars(g, t, p, zy);
+        if (threadIdx.x == 0)
+            scal = k;
+    }
+    __syncthreads();
+    const GradScalars k = scal;
+    if (k.zero)
+        zero_row<T, NT>(out, a.V, 0, 1);
+    else
+        src.dense(out, k.d, own_term(a, t, k.own));
+}
+
+template <typename T> __global__ __launch_bounds__(kSplit) void grad_join_kernel(Args g)
+{
+    __shared__ GradScalars scal;
+    const ScoreArgs &a = g.a;
+    const long t = group_index() / g.parts;
+    const int part = (int)(group_index() % g.parts);
+    if (t >= a.T)
+        return;
+    T *out = (T *)a.dlogits + t * a.dld;
+    if (!grad_used(a, t)) {
+        zero_row<T, kSplit>(out, a.V, part, g.parts);
+        return;
+    }
+    if (threadIdx.x < kWave) {
+        const GradScalars k =
+            grad_scalars(g, t, merge_parts(a.part + t * g.parts, g.parts, g.c), a.zlab[t]);
+        if (threadIdx.x == 0)
+            scal = k;
+    }
+    __syncthreads();
+    const GradScalars k = scal;
+    if (k.zero) {
+        zero_row<T, kSplit>(out, a.V, part, g.parts);
+        return;
+    }
+    const Streamed<T, kSplit> src((const T *)a.logits + t * a.ld, a.V, part, g.parts);
+    src.dense(out, k.d, own_term(a, t, k.own));
+}
+
+// ------------------------------------------------------------------ launches
+
+template <typename T, bool Top> struct RunScores {
+    const Args &g;
+    hipStream_t st;
+    template <int NT, typename Src> void operator()() const
+    {
+        hipLaunchKernelGGL((score_kernel<T, NT, Src, Top>), grid_of(g.a.T), dim3(NT),
+                           (size_t)Src::lds_chunks * 16, st, g);
+    }
+};
+template <typename T> struct RunScoreGrad {
+    const Args &g;
+    hipStream_t st;
+    template <int NT, typename Src> void operator()() const
+    {
+        hipLaunchKernelGGL((score_grad_kernel<T, NT, Src>), grid_of(g.a.T), dim3(NT),
+                           (size_t)Src::lds_chunks * 16, st, g);
+    }
+};
+
+template <typename T> hipError_t run_scores(const Args &g, hipStream_t st)
+{
+    const ScoreArgs &a = g.a;
+    if (g.parts > 1) {
+        const dim3 all = grid_of((long)a.T * g.parts), rows = grid_of(a.T);
+        if (a.top) {
+            hipLaunchKernelGGL((part_kernel<T, true>), all, dim3(kSplit), 0, st, g);
+            hipLaunchKernelGGL((join_kernel<true>), rows, dim3(kSplit), 0, st, g);
+        } else {
+            hipLaunchKernelGGL((part_kernel<T, false>), all, dim3(kSplit), 0, st, g);
+            hipLaunchKernelGGL((join_kernel<false>), rows, dim3(kSplit), 0, st, g);
+        }
+    } else if (a.top) {
+        // the bound of the list needs several threads an alternative
+        const RunScores<T, true> run{g, st};
+        if (a.top > 32 && (long)a.V * (long)sizeof(T) <= 8 << 10)
+            run.template operator()<256, Held<T, 256, 4>>();
+        else
+            with_source<T>(a.V, sizeof(ListRoom<1024>), false, run);
+    } else {
+        with_stream<T>(a.V, a.T, RunScores<T, false>{g, st});
+    }
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t run_scores_backward(const Args &g, hipStream_t st)
+{
+    const ScoreArgs &a = g.a;
+    if (g.parts > 1) {
+        const dim3 all = grid_of((long)a.T * g.parts);
+        hipLaunchKernelGGL((part_kernel<T, false>), all, dim3(kSplit), 0, st, g);
+        hipLaunchKernelGGL((grad_join_kernel<T>), all, dim3(kSplit), 0, st, g);
+    } else {
+        with_source<T>(a.V, 0, false, RunScoreGrad<T>{g, st});
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// A row of up to 128 KB is one work-group's; longer ones are split while there are too
+// few rows to keep the compute units loading, as for the losses.
+int score_parts(int T, int V, int dtype)
+{
+    const long bytes = (long)V * (dtype == 1 ? 2 : 4), chunks = bytes / 16;
+    if (T < 1 || T > 128 || bytes <= 128 << 10)
+        return 1;
+    return (int)std::min({1024l / T, chunks / (2 * kSplit), 64l});
+}
+
+hipError_t launch_scores(const ScoreArgs &a, hipStream_t st)
+{
+    const Args g{a, score_parts(a.T, a.V, a.dtype), scale_of_row(a.scale)};
+    return a.dtype == 1 ? run_scores<uint16_t>(g, st) : run_scores<float>(g, st);
+}
+
+hipError_t launch_scores_backward(const ScoreArgs &a, hipStream_t st)
+{
+    const Args g{a, score_parts(a.T, a.V, a.dtype), scale_of_row(a.scale)};
+    return a.dtype == 1 ? run_scores_backward<uint16_t>(g, st) : run_scores_backward<float>(g, st);
+}
+
+}  // namespace sk
