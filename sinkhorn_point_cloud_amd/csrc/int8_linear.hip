@@ -6,21 +6,21 @@
 // lane.  Channels are the rows of an instruction's result and tokens its columns:
 // a lane then holds four channels of one token side by side.
 //
-// Two kernels.  Up to 64 tokens the weights are what is read: each wave streams its
-// own rows of them from memory to registers.  Beyond, tiles of both operands go
-// through shared memory, 64 bytes of K at a time, four stages deep.
+// Tiles of both operands go through shared memory, some stages of K ahead of the
+// products, also for a few tokens: the copies keep more bytes on their way than loads
+// to registers do (4 x 4096 to 131072: 106 us against 140 of a kernel that streams
+// weights to registers with a wave's 16 rows, 110 with 32 rows).  A few tokens and a
+// few channels leave too few tiles to fill the device; there four waves share 16
+// channels along K.
 #include "head.h"
 
 #include <algorithm>
-#include <type_traits>
 
 namespace sk {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 struct Args {
     ProductArgs a;
@@ -44,136 +44,63 @@ __device__ __forceinline__ i32x4 byte_mask(int live)
     return m;
 }
 
-// Four channels n .. n + 3 of token t, of which `live` are there.
-template <typename O>
-__device__ __forceinline__ void put4(const ProductArgs &a, long t, int n, i32x4 sum, float xs, bool whole)
-{
-    const int live = min(4, a.N - n);
-    if (live <= 0)
-        return;
-    O *out = (O *)a.out + t * a.ldo + n;
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = min(n + i, a.N - 1);
-        v[i] = (float)sum[i] * (xs * a.wscale[at]);
-        if (a.bias)
-            v[i] += a.bias[at];
-    }
-    if (whole && live == 4) {
-        if constexpr (sizeof(O) == 4)
-            *reinterpret_cast<f32x4 *>(out) = f32x4{v[0], v[1], v[2], v[3]};
-        else
-            *reinterpret_cast<bf16x4 *>(out) =
-                bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < live)
-            out[i] = (O)v[i];
-}
-// whether four channels are one aligned store
-template <typename O> __device__ __forceinline__ bool whole_stores(const ProductArgs &a)
-{
-    return (((uintptr_t)a.out | (uintptr_t)(a.ldo * (int64_t)sizeof(O))) & (4 * sizeof(O) - 1)) == 0;
-}
-
-// --- few tokens: weights from memory to registers
+// --- few tokens and channels: weights from memory to registers
 
 constexpr int kDeep = 4;   // steps of 64 bytes that are asked for together
 
-// RT x 16 channels and TT x 16 tokens a work-group; its 4 waves take every fourth
-// piece of kDeep steps along K and their sums are joined in shared memory.
-template <typename O, int RT, int TT>
-__global__ __launch_bounds__(256) void stream_kernel(Args g)
+// 16 channels and 16 tokens a work-group; its 4 waves take every fourth piece of kDeep
+// steps along K and their sums are joined in shared memory.
+template <typename O> __global__ __launch_bounds__(256) void stream_kernel(Args g)
 {
     const ProductArgs &a = g.a;
-    __shared__ i32x4 room[3][RT * TT][kWave];
+    __shared__ i32x4 room[3][kWave];
     const int lane = lane_id(), wave = wave_id_uniform(), row = lane & 15, quad = lane >> 4;
-    const int n0 = blockIdx.x * RT * 16, t0 = blockIdx.y * TT * 16;
-    const int8_t *w[RT], *x[TT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-        w[i] = a.w + (long)min(n0 + i * 16 + row, a.N - 1) * a.ldw + quad * 16;
-#pragma unroll
-    for (int i = 0; i < TT; ++i)
-        x[i] = a.x + (long)min(t0 + i * 16 + row, a.T - 1) * a.ldx + quad * 16;
-    i32x4 acc[RT][TT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < TT; ++j)
-            acc[i][j] = i32x4{0, 0, 0, 0};
+    const int n0 = blockIdx.x * 16;
+    const int8_t *w = a.w + (long)min(n0 + row, a.N - 1) * a.ldw + quad * 16;
+    const int8_t *x = a.x + (long)min(row, a.T - 1) * a.ldx + quad * 16;
+    i32x4 acc = {0, 0, 0, 0};
     const int whole = a.K / 64;   // steps without an end of a row
     int s = wave * kDeep;
     for (; s + kDeep <= whole; s += 4 * kDeep) {
-        i32x4 wv[kDeep][RT], xv[kDeep][TT];
+        i32x4 wv[kDeep], xv[kDeep];
 #pragma unroll
         for (int k = 0; k < kDeep; ++k) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-                wv[k][i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(w[i] + (long)(s + k) * 64));
-#pragma unroll
-            for (int j = 0; j < TT; ++j)
-                xv[k][j] = load16(x[j] + (long)(s + k) * 64);
+            wv[k] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(w + (long)(s + k) * 64));
+            xv[k] = load16(x + (long)(s + k) * 64);
         }
 #pragma unroll
         for (int k = 0; k < kDeep; ++k)
-#pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int j = 0; j < TT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[k][i], xv[k][j], acc[i][j], 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[k], xv[k], acc, 0, 0, 0);
     }
     // the wave whose piece holds the end: its steps one by one
     for (const int last = min(s + kDeep, (a.K + 63) / 64); s < last; ++s) {
         const int live = a.K - s * 64 - quad * 16;   // bytes of this lane's 16
-        const i32x4 mask = byte_mask(live);
-        i32x4 wv[RT], xv[TT];
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-            wv[i] = live > 0 ? load16(w[i] + (long)s * 64) : i32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < TT; ++j)
-            xv[j] = live > 0 ? load16(x[j] + (long)s * 64) & mask : i32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int j = 0; j < TT; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[i], xv[j], acc[i][j], 0, 0, 0);
+        const i32x4 none = {0, 0, 0, 0};
+        const i32x4 wv = live > 0 ? load16(w + (long)s * 64) : none;
+        const i32x4 xv = live > 0 ? load16(x + (long)s * 64) & byte_mask(live) : none;
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv, xv, acc, 0, 0, 0);
     }
-    if (wave > 0) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int j = 0; j < TT; ++j)
-                room[wave - 1][i * TT + j][lane] = acc[i][j];
-    }
-    __syncthreads();
     if (wave > 0)
+        room[wave - 1][lane] = acc;
+    __syncthreads();
+    if (wave > 0 || row >= a.T)
         return;
-    const bool even = whole_stores<O>(a);
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
-        const int t = t0 + j * 16 + row;
-        if (t >= a.T)
-            continue;
-        const float xs = a.xscale[t];
+    for (int k = 0; k < 3; ++k)
+        acc += room[k][lane];
+    O *out = (O *)a.out + row * a.ldo;
+    const float xs = a.xscale[row];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            i32x4 sum = acc[i][j];
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                sum += room[k][i * TT + j][lane];
-            put4<O>(a, t, n0 + i * 16 + quad * 4, sum, xs, even);
+    for (int k = 0; k < 4; ++k) {
+        const int n = n0 + quad * 4 + k;
+        if (n < a.N) {
+            const float y = (float)acc[k] * (xs * a.wscale[n]);
+            out[n] = (O)(a.bias ? y + a.bias[n] : y);
         }
     }
 }
 
-// --- many tokens: tiles in shared memory
-
-constexpr int kStages = 4, kBytes = 64;   // stages, and bytes of K in one
+// --- tiles in shared memory
 
 // 16 bytes a lane into shared memory, a wave's KB in a run from `to` on.  In asm, so
 // that reads of other stages do not wait for it; the waits are in wait_stage().  (A
@@ -202,46 +129,58 @@ template <typename O, int n> struct alignas(sizeof(O)) Run {
     O v[n];
 };
 
-// 32 tokens' sums of Cols channels from a wave's room, scaled, to the result.
-template <typename O, int Cols>
-__device__ __forceinline__ void put_rows(const ProductArgs &a, const int32_t *room, int pitch, int t0, int n0,
-                                         O *out, int64_t ldo)
-{
-    constexpr int n = 16 / (int)sizeof(O), lanes = Cols / n, rows = kWave / lanes;
-    const int at = lane_id() % lanes * n, live = a.N - n0 - at;
-    if (live <= 0)
-        return;
+// The channels of a run that a lane writes: n0 + at on, of `live`.
+template <typename O, int Cols> struct Channels {
+    static constexpr int n = 16 / (int)sizeof(O), lanes = Cols / n;
     float ws[n], bias[n];
+    int at, live;
+    __device__ __forceinline__ Channels(const ProductArgs &a, int n0)
+        : at(lane_id() % lanes * n), live(a.N - n0 - at)
+    {
 #pragma unroll
-    for (int k = 0; k < n; ++k) {
-        const int c = n0 + at + min(k, live - 1);
-        ws[k] = a.wscale[c];
-        bias[k] = a.bias ? a.bias[c] : 0.f;
-    }
-#pragma unroll
-    for (int r = lane_id() / lanes; r < 32; r += rows) {
-        const int t = t0 + r;
-        if (t >= a.T)
-            break;
-        const float xs = a.xscale[t];
-        Run<O, n> v;
-#pragma unroll
-        for (int k = 0; k < n; k += 4) {
-            const i32x4 sum = *reinterpret_cast<const i32x4 *>(room + r * pitch + at + k);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float y = (float)sum[e] * (xs * ws[k + e]);
-                v.v[k + e] = (O)(a.bias ? y + bias[k + e] : y);
-            }
+        for (int k = 0; k < n; ++k) {
+            const int c = min(n0 + at + k, a.N - 1);
+            ws[k] = a.wscale[c];
+            bias[k] = a.bias ? a.bias[c] : 0.f;
         }
-        O *p = out + t * ldo + n0 + at;
-        if (live >= n) {
-            *reinterpret_cast<Run<O, n> *>(p) = v;
-        } else {
+    }
+};
+
+// 32 tokens' sums from a wave's room, scaled, to the result; a token's scale lies behind
+// its sums.
+template <typename O, int Cols>
+__device__ __forceinline__ void put_rows(const ProductArgs &a, const Channels<O, Cols> &c, const int32_t *room,
+                                         int pitch, int t0, int n0)
+{
+    constexpr int n = Channels<O, Cols>::n, lanes = Channels<O, Cols>::lanes, rows = kWave / lanes;
+    if (c.live <= 0)
+        return;
+    O *out = (O *)a.out + n0 + c.at;
+    const bool bias = a.bias != nullptr;
 #pragma unroll
-            for (int k = 0; k < n; ++k)
-                if (k < live)
-                    p[k] = v.v[k];
+    for (int i = 0; i < 32 / rows; ++i) {
+        const int r = i * rows + lane_id() / lanes, t = t0 + r;
+        if (t < a.T) {
+            const float xs = __int_as_float(room[r * pitch + Cols]);
+            Run<O, n> v;
+#pragma unroll
+            for (int k = 0; k < n; k += 4) {
+                const i32x4 sum = *reinterpret_cast<const i32x4 *>(room + r * pitch + c.at + k);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y = (float)sum[e] * (xs * c.ws[k + e]);
+                    v.v[k + e] = (O)(bias ? y + c.bias[k + e] : y);
+                }
+            }
+            O *p = out + t * a.ldo;
+            if (c.live >= n) {
+                *reinterpret_cast<Run<O, n> *>(p) = v;
+            } else {
+#pragma unroll
+                for (int k = 0; k < n; ++k)
+                    if (k < c.live)
+                        p[k] = v.v[k];
+            }
         }
     }
 }
@@ -257,60 +196,67 @@ __device__ __forceinline__ void put_sums(const ProductArgs &a, const int32_t *ro
     }
 }
 
-template <typename O, int BT, int BN>
-__global__ __launch_bounds__(256, BT *BN >= 256 * 256 ? 1 : 2) void tile_kernel(Args g)
+// A tile of BT tokens and BN channels, a quarter for each wave; `Stages` stages of
+// `Bytes` bytes of K in shared memory.
+template <typename O, int BT, int BN, int Bytes, int Stages, int Occ>
+__global__ __launch_bounds__(256, Occ) void tile_kernel(Args g)
 {
-    // a row of a stage is 64 bytes; chunk c of 16 bytes lies at c ^ (row / 4 & 3), so
-    // that 16 rows' chunks c cover all 64 banks
-    constexpr int rows = BT + BN, stage = rows * kBytes, loads = rows / 64;
-    constexpr int TT = BT / 64, TN = BN / 64;   // 32 x 32 results of a wave (half of the tile each way)
-    extern __shared__ char lds[];               // [kStages][stage]
+    // a stage's rows are Bytes apart; chunk c of 16 bytes lies at c ^ turn(row), so that
+    // 16 rows' chunks c cover all 64 banks
+    constexpr int rows = BT + BN, stage = rows * Bytes, per_row = Bytes / 16;
+    constexpr int loads = rows * per_row / 256, subs = Bytes / 32;
+    constexpr int TT = BT / 64, TN = BN / 64;   // 32 x 32 results of a wave
+    auto turn = [](int row) { return Bytes == 64 ? row >> 2 & 3 : row >> 1 & 7; };
+    extern __shared__ char lds[];               // [Stages][stage]
     const ProductArgs &a = g.a;
     const int lane = lane_id(), wave = wave_id_uniform();
-    // tiles in bands of 8 along the tokens, channels across; a run of them to each XCD
+    // tiles in bands of 4 along the tokens, channels across; a run of them to each XCD.
+    // (4096 x 4096 to 131072: 2.31 ms, bands of 1, 2, 8 and 16 2.56, 2.35, 2.39, 2.53: work-groups
+    // that run at once share tiles of both operands, and write beside one another rather
+    // than below, in rows a power of two apart.)
     const int tiles_t = (a.T + BT - 1) / BT, tiles_n = (a.N + BN - 1) / BN;
     const long all = (long)tiles_t * tiles_n, per = (all + 7) / 8;
     const long b = blockIdx.x % 8 * per + blockIdx.x / 8;
     if (blockIdx.x / 8 >= per || b >= all)
         return;
-    const long band = b / (8l * tiles_n), in = b - band * 8l * tiles_n;
-    const int high = min(8, tiles_t - (int)band * 8);
-    const int t0 = ((int)band * 8 + (int)(in % high)) * BT, n0 = (int)(in / high) * BN;
+    constexpr int kBand = 4;
+    const long band = b / ((long)kBand * tiles_n), in = b - band * kBand * tiles_n;
+    const int high = min(kBand, tiles_t - (int)band * kBand);
+    const int t0 = ((int)band * kBand + (int)(in % high)) * BT, n0 = (int)(in / high) * BN;
     // this part's stages along K
-    const int chunks = (a.K + 15) / 16, steps = (a.K + kBytes - 1) / kBytes;
+    const int chunks = (a.K + 15) / 16, steps = (a.K + Bytes - 1) / Bytes;
     const int each = (steps + g.parts - 1) / g.parts;
     const int first = min((int)blockIdx.y * each, steps), count = min(each, steps - first);
 
     const int8_t *from[loads];
-    const int sub = lane >> 2, chunk = (lane & 3) ^ (lane >> 4 & 3);
+    const int sub = lane / per_row, chunk = lane % per_row ^ turn(sub);
+    static_assert(64 / per_row % (Bytes == 64 ? 16 : 8) == 0);   // turn(row) is that of sub, or
+    const int odd = Bytes == 64 ? 0 : 4;                          // of 8 rows more: ^ 4
 #pragma unroll
     for (int i = 0; i < loads; ++i) {
-        const int r = (i * 4 + wave) * 16 + sub;   // of the stage: tokens, then channels
+        const int r = (i * 4 + wave) * (64 / per_row) + sub;   // of the stage: tokens, then channels
         from[i] = r < BT ? a.x + (long)min(t0 + r, a.T - 1) * a.ldx
                          : a.w + (long)min(n0 + r - BT, a.N - 1) * a.ldw;
-        from[i] += (long)first * kBytes + chunk * 16;
+        from[i] += (long)first * Bytes + (chunk ^ (wave & 1 ? odd : 0)) * 16;
     }
+    const int mine = chunk ^ (wave & 1 ? odd : 0);
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-    // a stage of whole chunks, and any stage of this part
-    auto issue_whole = [&](int k) {
-        const uint32_t to = base + (k % kStages) * stage + wave * 1024;
-#pragma unroll
-        for (int i = 0; i < loads; ++i) {
-            copy16(from[i], to + i * 4096);
-            from[i] += kBytes;
-        }
+    // Piece p of `subs` of the copies of stage k: of whole chunks, or any stage's.
+    auto copy = [&](int k, int i) {
+        copy16(from[i], base + (k % Stages) * stage + wave * 1024 + i * 4096);
+        from[i] += Bytes;
     };
-    auto issue = [&](int k) {
-        if (first + k + 1 < steps || chunks % 4 == 0) {
-            issue_whole(k);
+    auto issue = [&](int k, int p0, int p1) {
+        if (k >= count)
             return;
-        }
-        // chunks behind the rows' end: zeros
-        const uint32_t to = base + (k % kStages) * stage + wave * 1024;
-        const bool there = (first + k) * 4 + chunk < chunks;
+        const bool there = (first + k) * per_row + mine < chunks;   // else behind the rows' end: zeros
 #pragma unroll
         for (int i = 0; i < loads; ++i)
-            copy16(there ? from[i] : (const int8_t *)kZeros, to + i * 4096);
+            if (i >= p0 * loads / subs && i < p1 * loads / subs) {
+                copy16(there ? from[i] : (const int8_t *)kZeros,
+                       base + (k % Stages) * stage + wave * 1024 + i * 4096);
+                from[i] += Bytes;
+            }
     };
     i32x16 acc[TN][TT];
 #pragma unroll
@@ -321,86 +267,122 @@ __global__ __launch_bounds__(256, BT *BN >= 256 * 256 ? 1 : 2) void tile_kernel(
             for (int k = 0; k < 16; ++k)
                 acc[i][j][k] = 0;
     const int wt = wave & 1, wn = wave >> 1, r32 = lane & 31, half = lane >> 5;
-    int at[2];   // of this lane's 16 bytes, for either half of a stage
+    int at[subs];   // of this lane's 16 bytes, for each 32 bytes of a stage
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-        at[s] = r32 * kBytes + ((2 * s + half) ^ (r32 >> 2 & 3)) * 16;
-    const int xrow = wt * (BT / 2) * kBytes, wrow = (BT + wn * (BN / 2)) * kBytes;
+    for (int s = 0; s < subs; ++s)
+        at[s] = r32 * Bytes + ((2 * s + half) ^ turn(r32)) * 16;
+    // the scales that the results will need
+    constexpr int cols = BN / 2, pitch = cols + 4;   // 16 tokens' stores cover all banks
+    const int nw = n0 + wn * cols;
+    const Channels<O, cols> channels(a, nw);
+    float xs[TT];
+#pragma unroll
+    for (int j = 0; j < TT; ++j)
+        xs[j] = a.xscale[min(t0 + wt * (BT / 2) + j * 32 + r32, a.T - 1)];
+    const int xrow = wt * (BT / 2) * Bytes, wrow = (BT + wn * (BN / 2)) * Bytes;
     i32x4 wf[2][TN], xf[2][TT];
-    auto fetch = [&](int k, int s) {
-        const char *p = lds + (k % kStages) * stage + at[s];
+    // Operand r of the TN + TT of piece s of stage k.
+    auto fetch = [&](int k, int s, int r) {
+        const char *p = lds + (k % Stages) * stage + at[s];
+        if (r < TN)
+            wf[s & 1][r] = *reinterpret_cast<const i32x4 *>(p + wrow + r * 32 * Bytes);
+        else
+            xf[s & 1][r - TN] = *reinterpret_cast<const i32x4 *>(p + xrow + (r - TN) * 32 * Bytes);
+    };
+    auto fetch_all = [&](int k, int s) {
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
-            wf[s][i] = *reinterpret_cast<const i32x4 *>(p + wrow + i * 32 * kBytes);
+        for (int r = 0; r < TN + TT; ++r)
+            fetch(k, s, r);
+    };
+    auto multiply = [&](int s, int m) {
+        const int i = m / TT, j = m % TT;
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[s & 1][i], xf[s & 1][j], acc[i][j], 0, 0, 0);
+    };
+    auto multiply_all = [&](int s) {
+#pragma unroll
+        for (int m = 0; m < TN * TT; ++m)
+            multiply(s, m);
+    };
+    // Piece s multiplied, with the reads of the next piece (n of stage kn) and piece p of
+    // the copies of stage kc between the products: the matrix cores never wait for the
+    // issue of either.
+    auto step = [&](int s, int kn, int n, int kc, int p) {
+        constexpr int M = TN * TT, R = TN + TT;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r * (M / 2) / R == m)
+                    fetch(kn, n, r);
+            const int c0 = p * loads / subs, c = (p + 1) * loads / subs - c0;
+#pragma unroll
+            for (int i = 0; i < loads; ++i)
+                if (i >= c0 && i < c0 + c && M / 2 + (i - c0) * (M / 2) / c == m)
+                    copy(kc, i);
+            multiply(s, m);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // what lies behind the rows' end in their last chunk counts as zeros
+    auto mask = [&](int s) {
+        const i32x4 m = byte_mask(a.K - (steps - 1) * Bytes - (2 * s + half) * 16);
 #pragma unroll
         for (int j = 0; j < TT; ++j)
-            xf[s][j] = *reinterpret_cast<const i32x4 *>(p + xrow + j * 32 * kBytes);
-    };
-    auto multiply = [&](int s) {
-#pragma unroll
-        for (int i = 0; i < TN; ++i)
-#pragma unroll
-            for (int j = 0; j < TT; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[s][i], xf[s][j], acc[i][j], 0, 0, 0);
+            xf[s & 1][j] &= m;
     };
     if (count > 0) {
+        // all stages but the last whole, of that the first piece
 #pragma unroll
-        for (int k = 0; k < kStages - 1; ++k)
-            if (k < count)
-                issue(k);
-        if (count > 2)
-            wait_stage<2 * loads>();
+        for (int k = 0; k < Stages; ++k)
+            issue(k, 0, k + 1 < Stages ? subs : 1);
+        if (count >= Stages)
+            wait_stage<(Stages - 2) * loads + loads / subs>();
         else
             wait_stage<0>();
-        fetch(0, 0);
-        // behind each wait, stage k + 1 is there for all and nobody reads stage k - 1 any more
+        fetch_all(0, 0);
         int k = 0;
-        for (; k + 4 < count; ++k) {
-            wait_stage<loads>();
-            issue_whole(k + 3);
-            fetch(k, 1);
-            multiply(0);
-            fetch(k + 1, 0);
-            multiply(1);
+        for (; k + Stages + 1 < count; ++k) {
+#pragma unroll
+            for (int s = 0; s + 1 < subs; ++s)
+                step(s, k, s + 1, k + Stages - 1, s + 1);
+            // stage k + 1 is there for all, and nobody reads stage k any more
+            wait_stage<(Stages - 2) * loads>();
+            step(subs - 1, k + 1, 0, k + Stages, 0);
         }
 #pragma unroll 1
-        for (; k + 1 < count; ++k) {
-            if (k + 2 < count)
-                wait_stage<loads>();
-            else
-                wait_stage<0>();
-            if (k + 3 < count)
-                issue(k + 3);
-            fetch(k, 1);
-            multiply(0);
-            fetch(k + 1, 0);
-            multiply(1);
-        }
-        // the last stage: what lies behind the rows' end counts as zeros
-        fetch(count - 1, 1);
-        if (a.K % 16 && first + count == steps) {
+        for (; k < count; ++k) {
+            const bool end = k + 1 == count && a.K % 16 && first + count == steps;
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const i32x4 mask = byte_mask(a.K - (steps - 1) * kBytes - (2 * s + half) * 16);
-#pragma unroll
-                for (int j = 0; j < TT; ++j)
-                    xf[s][j] &= mask;
+            for (int s = 0; s + 1 < subs; ++s) {
+                issue(k + Stages - 1, s + 1, s + 2);
+                fetch_all(k, s + 1);
+                if (end)
+                    mask(s);
+                multiply_all(s);
             }
+            if (end)
+                mask(subs - 1);
+            if (k + 1 < count) {
+                if (k + Stages <= count)
+                    wait_stage<(Stages - 2) * loads>();
+                else
+                    wait_stage<0>();
+            }
+            issue(k + Stages, 0, 1);
+            multiply_all(subs - 1);
+            fetch_all(k + 1, 0);   // behind the last stage: an older one, for nothing
         }
-        multiply(0);
-        multiply(1);
     }
     // A lane holds four channels of a token, and 32 tokens' rows of 16 bytes would be
     // written at once: the sums go through shared memory, 32 tokens at a time and each
     // wave in its own room, and leave in runs of a wave's BN / 2 channels.  (4096 x 4096
     // to 131072 in bf16: 3.69 ms without it.)
-    constexpr int cols = BN / 2, pitch = cols + 4;   // 16 tokens' stores cover all banks
-    static_assert(4 * 32 * pitch * 4 <= kStages * stage);
     __syncthreads();
     int32_t *room = reinterpret_cast<int32_t *>(lds) + wave * 32 * pitch;
-    const int nw = n0 + wn * cols;
 #pragma unroll
     for (int j = 0; j < TT; ++j) {
+        if (half == 0)
+            room[r32 * pitch + cols] = __float_as_int(xs[j]);
 #pragma unroll
         for (int i = 0; i < TN; ++i)
 #pragma unroll
@@ -410,7 +392,7 @@ __global__ __launch_bounds__(256, BT *BN >= 256 * 256 ? 1 : 2) void tile_kernel(
         wave_fence();
         const int tw = t0 + wt * (BT / 2) + j * 32;
         if (g.parts == 1)
-            put_rows<O, cols>(a, room, pitch, tw, nw, (O *)a.out, a.ldo);
+            put_rows<O, cols>(a, channels, room, pitch, tw, nw);
         else
             put_sums<cols>(a, room, pitch, tw, nw, a.part + (long)blockIdx.y * a.T * a.N);
         wave_fence();
@@ -436,43 +418,46 @@ template <typename O> __global__ __launch_bounds__(256) void join_kernel(Args g)
     }
 }
 
-constexpr int kStreamTokens = 64;
-
-template <typename O, int RT, int TT> void run_stream(const Args &g, hipStream_t st)
+// Which kernel, and the tile.  256 x 256 where such tiles fill the compute units and K is
+// long enough for what surrounds the products to be small: 8192 x 8192 to 8192 474 us
+// against 677 with 128 x 128, which hide it with three work-groups a compute unit (4096 x
+// 256 to 64000 251 us against 307, 333 x 1500 to 50001 56 against 71).  For up to 64
+// tokens, whose tiles are read for the weights' sake, 64 x 128, or 64 x 64 where the
+// channels are few (40 x 8192 to 32000 45 against 49 us, 64 x 14336 to 4096 45 against 36).
+enum Shape { kStream, kTiles64, kTiles64x128, kTiles128, kTiles256 };
+Shape shape_of(int T, int K, int N)
 {
-    const dim3 grid((g.a.N + RT * 16 - 1) / (RT * 16), (g.a.T + TT * 16 - 1) / (TT * 16));
-    hipLaunchKernelGGL((stream_kernel<O, RT, TT>), grid, dim3(256), 0, st, g);
+    if (T <= 16 && N <= 8192)
+        return kStream;
+    if (T <= 64)
+        return N < 32768 ? kTiles64 : kTiles64x128;
+    return T > 128 && K >= 2048 && ((long)T + 255) / 256 * (((long)N + 255) / 256) >= 192 ? kTiles256
+                                                                                           : kTiles128;
 }
-template <typename O, int BT, int BN> void run_tiles(const Args &g, hipStream_t st)
+
+template <typename O, int BT, int BN, int Bytes, int Stages, int Occ>
+void run_tiles(const Args &g, hipStream_t st)
 {
     const long all = ((long)g.a.T + BT - 1) / BT * (((long)g.a.N + BN - 1) / BN);
-    const size_t room = (size_t)kStages * (BT + BN) * kBytes;
-    hipLaunchKernelGGL((tile_kernel<O, BT, BN>), dim3((unsigned)((all + 7) / 8 * 8), g.parts), dim3(256),
-                       room, st, g);
+    const size_t stages = (size_t)Stages * (BT + BN) * Bytes, sums = (size_t)4 * 32 * (BN / 2 + 4) * 4;
+    hipLaunchKernelGGL((tile_kernel<O, BT, BN, Bytes, Stages, Occ>),
+                       dim3((unsigned)((all + 7) / 8 * 8), g.parts), dim3(256), std::max(stages, sums), st, g);
     if (g.parts > 1)
         hipLaunchKernelGGL((join_kernel<O>), dim3((g.a.N + 255) / 256, std::min(g.a.T, 32768)), dim3(256), 0,
                            st, g);
 }
 
-// Tiles of 256 x 256 where they fill the compute units, else of 128 x 128.
-bool large_tiles(int T, int N)
-{
-    return ((long)T + 255) / 256 * (((long)N + 255) / 256) >= 256;
-}
-
 template <typename O> void run_product(const Args &g, hipStream_t st)
 {
-    const int T = g.a.T;
-    if (T <= 16)
-        run_stream<O, 1, 1>(g, st);
-    else if (T <= 32)
-        run_stream<O, 2, 2>(g, st);
-    else if (T <= kStreamTokens)
-        run_stream<O, 2, 4>(g, st);
-    else if (large_tiles(T, g.a.N))
-        run_tiles<O, 256, 256>(g, st);
-    else
-        run_tiles<O, 128, 128>(g, st);
+    switch (shape_of(g.a.T, g.a.K, g.a.N)) {
+    case kStream:
+        hipLaunchKernelGGL((stream_kernel<O>), dim3((g.a.N + 15) / 16), dim3(256), 0, st, g);
+        break;
+    case kTiles64: run_tiles<O, 64, 64, 64, 4, 4>(g, st); break;
+    case kTiles64x128: run_tiles<O, 64, 128, 64, 4, 3>(g, st); break;
+    case kTiles128: run_tiles<O, 128, 128, 64, 3, 3>(g, st); break;
+    case kTiles256: run_tiles<O, 256, 256, 128, 2, 1>(g, st); break;
+    }
 }
 
 }  // namespace
@@ -481,10 +466,12 @@ template <typename O> void run_product(const Args &g, hipStream_t st)
 // compute units.
 int product_parts(int T, int K, int N)
 {
-    if (T <= kStreamTokens || large_tiles(T, N))
+    const Shape shape = shape_of(T, K, N);
+    if (shape != kTiles64 && shape != kTiles128)
         return 1;
-    const long tiles = ((long)T + 127) / 128 * (((long)N + 127) / 128);
-    return (int)std::max(1l, std::min({256 / tiles, (long)K / (8 * kBytes), 16l}));
+    const int side = shape == kTiles64 ? 64 : 128;
+    const long tiles = ((long)T + side - 1) / side * (((long)N + side - 1) / side);
+    return (int)std::max(1l, std::min({256 / std::max(tiles, 1l), (long)K / 512, 16l}));
 }
 
 hipError_t launch_product(const ProductArgs &a, hipStream_t st)
