@@ -14,10 +14,14 @@
 // of the row's `top`-th largest value, and little more than `top` values lie at or
 // above it (in random order about top + top^2 / 2 NT).  They are listed in shared
 // memory and ranked there by value and index, so the order in which they were listed
-// does not matter.  A row of which more do not fit (many equal values, or the large
-// ones all in one thread's chunks) has its `top`-th value found by bisection first.
+// does not matter.  Each thread keeps the maxima of up to 8 groups of its chunks, and
+// only groups that reach the bound are read again.  A row of which more do not fit
+// (many equal values, or the large ones all in one thread's chunks) has its `top`-th
+// value found by bisection first.
 //
-// What bounds it: HBM.  A row is read once and kept on the chip for the second look.
+// What bounds it: HBM.  (A row kept in registers for the second look leaves a compute
+// unit no other row to load meanwhile: 4096 rows of 131072 bf16 values with 64
+// alternatives took 477 us that way.)
 #include "head.h"
 #include "rows.h"
 
@@ -27,7 +31,6 @@ namespace {
 using namespace rows;
 
 constexpr int kSplit = 256;      // threads of a work-group that shares its row with others
-constexpr int kRoom = 1024;      // values that can be listed
 constexpr float kFar = 1000.f;   // 2^-kFar is 0: stands for the distance of what has no probability
 
 // --- maximum, rest and weighted distance
@@ -42,9 +45,10 @@ __device__ __forceinline__ float distance(float d, const Scale &c)
     return min_of(-fmaf(d, c.hi, d * c.lo), kFar);   // NaN stays
 }
 
-// Takes K values in; as absorb(), with the weighted distance.
+// Takes K values in, as absorb() of the losses, with the weighted distance.  Returns
+// the largest of them.
 template <int K>
-__device__ __forceinline__ void absorb(const float (&x)[K], const Scale &c, Stats &s)
+__device__ __forceinline__ float absorb(const float (&x)[K], const Scale &c, Stats &s)
 {
     float low[K], top = x[0];
 #pragma unroll
@@ -65,6 +69,7 @@ __device__ __forceinline__ void absorb(const float (&x)[K], const Scale &c, Stat
     s.w = rises ? fmaf(f, fmaf(g, s.r, s.w), far) : s.w + far;
     s.r = fmaf(s.r, rises ? f : 1.f, sum);
     s.m = mn;
+    return top;
 }
 
 // A part's (r, w) from its own maximum to the common one `top`.
@@ -139,27 +144,36 @@ __device__ __forceinline__ uint64_t entry_of(uint32_t key, int v)
 }
 
 template <int NT> struct ListRoom {
-    uint32_t keys[NT];
-    uint64_t entry[kRoom];
+    static constexpr int room = NT == kWave ? 256 : 1024;   // values that can be listed
+    uint32_t keys[NT], border;
+    uint64_t entry[room + 8];
     int count, wave[NT / kWave];
+    uint16_t flag[room];   // groups of values that reach the border
+    int flags;
 };
 
-// The lower 16 bits cleared of the `top`-th largest of the NT keys in room.keys (0 if
-// there are not as many): by bisection, in the first wave; every lane of it has the result.
-template <int NT> __device__ __forceinline__ uint32_t nth_key(const uint32_t *keys, int top)
+// The lower 16 bits cleared of the `top`-th largest of P x 64 maxima, each over some of
+// the NT threads' keys (0 if there are not as many): by bisection, two bits at a time, in
+// one wave; every lane of it has the result.
+template <int NT, int P> __device__ __forceinline__ uint32_t nth_key(const uint32_t *keys, int top)
 {
-    constexpr int per = NT / kWave;
-    uint32_t k[per], found = 0;
+    uint32_t k[P], found = 0;
 #pragma unroll
-    for (int i = 0; i < per; ++i)
+    for (int i = 0; i < P; ++i) {
         k[i] = keys[i * kWave + lane_id()];
-    for (int bit = 31; bit >= 16; --bit) {
-        const uint32_t with = found | 1u << bit;
-        int n = 0;
 #pragma unroll
-        for (int i = 0; i < per; ++i)
-            n += __popcll(__ballot(k[i] >= with));
-        found = n >= top ? with : found;
+        for (int j = P; j < NT / kWave; j += P)
+            k[i] = max(k[i], keys[(i + j) * kWave + lane_id()]);
+    }
+#pragma unroll
+    for (int bit = 30; bit >= 16; bit -= 2) {
+        int n[3] = {0, 0, 0};
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                n[q] += __popcll(__ballot(k[i] >= (found | (uint32_t)(q + 1) << bit)));
+        found |= (uint32_t)((n[0] >= top) + (n[1] >= top) + (n[2] >= top)) << bit;
     }
     return found;
 }
@@ -181,48 +195,73 @@ template <int NT> __device__ __forceinline__ int group_count(int n, int *wave)
     return n;
 }
 
-// Appends what is wanted to the list; returns without writing beyond its room.
+// Places in a list of `count` for the lanes of a wave that want one: one atomic a wave.
+// (One a lane, in a loop over the values of a group: 8192 rows of 8192 bf16 values with
+// 20 alternatives 53 us, of which the list 18.)
+__device__ __forceinline__ int take_place(int &count, bool wanted)
+{
+    const uint64_t mask = __ballot(wanted);
+    if (!mask)
+        return 0;
+    const int first = __builtin_ctzll(mask);
+    int at = 0;
+    if (lane_id() == first)
+        at = atomicAdd(&count, (int)__popcll(mask));
+    at = __builtin_amdgcn_readlane(at, first);
+    return at + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                               __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+// Appends what is wanted to the list; nothing is written beyond its room.
 template <int NT>
 __device__ __forceinline__ void append(ListRoom<NT> &room, bool wanted, uint64_t entry)
 {
-    if (wanted) {
-        const int at = atomicAdd(&room.count, 1);
-        if (at < kRoom)
-            room.entry[at] = entry;
-    }
+    const int at = take_place(room.count, wanted);
+    if (wanted && at < ListRoom<NT>::room)
+        room.entry[at] = entry;
 }
 
-// Lists the alternatives of a source: `scan(f)` calls f(key, index) for each value of
-// this thread, `most` is this thread's largest key.  Leaves at most kRoom entries in
-// room.entry, `top` of which at least are the largest (fewer where there are fewer).
-// Returns how many; the list is there for every thread.  `again` is as scan, but reads
-// memory: keys of values in registers would be kept in more of them between its turns.
-template <int NT, typename Scan, typename Again>
-__device__ __forceinline__ int list_top(ListRoom<NT> &room, int top, uint32_t most, Scan &&scan,
-                                        Again &&again)
+// This thread's largest key; then, behind a barrier, the border of the list, by one wave.
+// 64 maxima for up to 16 alternatives, 256 for more: little more is listed than with
+// a maximum of each thread, and the bisection is as much shorter.
+template <int NT> __device__ __forceinline__ void set_key(ListRoom<NT> &room, uint32_t most)
 {
     room.keys[threadIdx.x] = most;
     if (threadIdx.x == 0)
-        room.count = 0;
-    __syncthreads();
-    if (threadIdx.x < kWave) {
-        const uint32_t k = top <= NT ? nth_key<NT>(room.keys, top) : 0u;
-        if (threadIdx.x == 0)
-            room.keys[0] = max(k, kNoKey + 1);
-    }
-    __syncthreads();
-    const uint32_t border = room.keys[0];
-    scan([&](uint32_t key, int v) { append(room, key >= border, entry_of(key, v)); });
+        room.count = room.flags = 0;
+}
+template <int NT> __device__ __forceinline__ void set_border(ListRoom<NT> &room, int top)
+{
+    constexpr int P = NT < 256 ? NT / kWave : 4;
+    uint32_t k = 0;
+    if (top <= 16)
+        k = nth_key<NT, 1>(room.keys, top);
+    else if (top <= P * kWave)
+        k = nth_key<NT, P>(room.keys, top);
+    if (lane_id() == 0)
+        room.border = max(k, kNoKey + 1);
+}
+
+// Lists the alternatives of a source: `list(border)` appends the values of this thread at
+// or above the border, `scan(f)` calls f(key, index) for every value of this thread.
+// set_key() came before, a barrier, set_border() and another.  Leaves at most its room's
+// entries in room.entry, the `top` largest among them (fewer where there are fewer).
+// Returns how many; the list is there for every thread.
+template <int NT, typename List, typename Scan>
+__device__ __forceinline__ int list_top(ListRoom<NT> &room, int top, List &&list, Scan &&scan)
+{
+    const uint32_t border = room.border;
+    list(border);
     __syncthreads();
     const int n = room.count;
-    if (n <= kRoom)
+    if (n <= ListRoom<NT>::room)
         return n;
     // more than fit: the `top`-th entry itself, a bit at a time (entries differ)
     uint64_t least = 0;
+#pragma unroll 1
     for (int bit = 31 + kIndexBits; bit >= 0; --bit) {
         const uint64_t with = least | 1ull << bit;
         int c = 0;
-        again([&](uint32_t key, int v) { c += entry_of(key, v) >= with; });
+        scan([&](uint32_t key, int v) { c += entry_of(key, v) >= with; });
         if (group_count<NT>(c, room.wave) >= top)
             least = with;
     }
@@ -230,7 +269,7 @@ __device__ __forceinline__ int list_top(ListRoom<NT> &room, int top, uint32_t mo
     if (threadIdx.x == 0)
         room.count = 0;
     __syncthreads();
-    again([&](uint32_t key, int v) {
+    scan([&](uint32_t key, int v) {
         const uint64_t e = entry_of(key, v);
         append(room, e >= least, e);
     });
@@ -239,35 +278,138 @@ __device__ __forceinline__ int list_top(ListRoom<NT> &room, int top, uint32_t mo
 }
 
 // Calls put(place, entry) for the largest `top` of the n listed ones, each by the
-// thread that has counted how many are larger.
+// thread that has counted how many are larger.  One barrier.
 template <int NT, typename Put>
-__device__ __forceinline__ void rank_list(const ListRoom<NT> &room, int n, int top, Put &&put)
+__device__ __forceinline__ void rank_list(ListRoom<NT> &room, int n, int top, Put &&put)
 {
+    // zeros behind the list, which count for none: eight at a time
+    if (threadIdx.x < 8)
+        room.entry[n + threadIdx.x] = 0;
+    __syncthreads();
     for (int i = threadIdx.x; i < n; i += NT) {
         const uint64_t e = room.entry[i];
         int place = 0;
-        for (int j = 0; j < n; ++j)
-            place += room.entry[j] > e;
+        for (int j = 0; j < n; j += 8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                place += room.entry[j + k] > e;
+        }
         if (place < top)
             put(place, e);
     }
 }
 
-// A row's values as a source of list_top.
-template <typename T, typename Src, typename F>
-__device__ __forceinline__ void scan_row(const Src &src, F &&f)
-{
-    constexpr int n = Pack<T>::n;
-    if (src.has_edge(threadIdx.x))
-        f(key_of(src.edge_value()), src.edge_at(threadIdx.x));
-    src.template each<false>([&](int, int at, const float (&x)[n]) {
-        if (at < src.c1) {
+constexpr int kBatch = 4;    // chunks that a thread asks for together
+constexpr int kGroups = 8;   // of batches, a maximum of each
+
+// A row, or a part of one, read from memory: its statistics, and the maxima of groups
+// of each thread's chunks.
+template <typename T, int NT> struct Reader : Slice<T, NT> {
+    using S = Slice<T, NT>;
+    static constexpr int n = S::n;
+    int batches, per;    // of the longest thread, and in a group
+    int turns;           // chunks of a thread in a group: a short row's groups are chunks
+    float edge, most[kGroups];
+
+    __device__ __forceinline__ Reader(const T *p, int len, int part, int parts) : S(p, len, part, parts)
+    {
+        batches = (S::c1 - S::c0 + NT * kBatch - 1) / (NT * kBatch);
+        per = (batches + kGroups - 1) / kGroups;
+        turns = batches * kBatch <= kGroups ? 1 : per * kBatch;
+        edge = S::has_edge(threadIdx.x) ? Pack<T>::get(S::row + S::edge_at(threadIdx.x)) : -kInf;
+    }
+    // f(first element, values) for the chunks of batch b
+    template <typename F> __device__ __forceinline__ void batch(int b, F &&f) const
+    {
+        const int at = S::c0 + b * NT * kBatch + (int)threadIdx.x;
+        u32x4 v[kBatch];
+        if (S::c0 + (b + 1) * NT * kBatch <= S::c1) {
 #pragma unroll
-            for (int k = 0; k < n; ++k)
-                f(key_of(x[k]), src.cut.head + at * n + k);
+            for (int j = 0; j < kBatch; ++j)
+                v[j] = *S::chunk(at + j * NT);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                v[j] = u32x4{Pack<T>::kNone, Pack<T>::kNone, Pack<T>::kNone, Pack<T>::kNone};
+                if (at + j * NT < S::c1)
+                    v[j] = *S::chunk(at + j * NT);
+            }
         }
-    });
-}
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            float x[n];
+            Pack<T>::open(v[j], x);
+            f(S::cut.head + (at + j * NT) * n, x);
+        }
+    }
+    __device__ __forceinline__ void stats(const Scale &c, Stats &s)
+    {
+        if (turns == 1) {
+#pragma unroll
+            for (int b = 0; b < kGroups / kBatch; ++b) {
+                int j = b * kBatch;
+                if (b < batches) {
+                    batch(b, [&](int, const float (&x)[n]) { most[j++] = absorb<n>(x, c, s); });
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k)
+                        most[j++] = -kInf;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                float m = -kInf;
+                for (int b = g * per; b < min((g + 1) * per, batches); ++b)
+                    batch(b, [&](int, const float (&x)[n]) { m = max_of(m, absorb<n>(x, c, s)); });
+                most[g] = m;
+            }
+        }
+        const float x[1] = {edge};
+        absorb<1>(x, c, s);
+    }
+    // f(key, index) for every value of this thread; values of -inf, or none, among them
+    template <typename F> __device__ __forceinline__ void scan(F &&f) const
+    {
+        f(key_of(edge), S::edge_at(threadIdx.x));
+#pragma unroll 1
+        for (int b = 0; b < batches; ++b)
+            batch(b, [&](int first, const float (&x)[n]) {
+#pragma unroll
+                for (int k = 0; k < n; ++k)
+                    f(key_of(x[k]), first + k);
+            });
+    }
+    // Appends the values at or above the border: first the groups that have any, then
+    // their values, dealt to all threads.  More groups than fit count as more values than
+    // fit.  For the whole work-group; one barrier.
+    __device__ __forceinline__ void list(uint32_t border, ListRoom<NT> &room) const
+    {
+        append(room, key_of(edge) >= border, entry_of(key_of(edge), S::edge_at(threadIdx.x)));
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+            if (g * turns < batches * kBatch) {
+                const bool has = key_of(most[g]) >= border;
+                const int at = take_place(room.flags, has);
+                if (has && at < ListRoom<NT>::room)
+                    room.flag[at] = (uint16_t)(g << 10 | threadIdx.x);
+            }
+        __syncthreads();
+        const int flags = room.flags;
+        if (flags > ListRoom<NT>::room) {
+            if (threadIdx.x == 0)
+                room.count = ListRoom<NT>::room + 1;
+            return;
+        }
+        for (int turn = 0; turn < turns; ++turn)
+            for (int i = threadIdx.x; i < flags * n; i += NT) {
+                const int f = room.flag[i / n], chunk = S::c0 + ((f >> 10) * turns + turn) * NT + (f & 1023);
+                const int v = S::cut.head + chunk * n + i % n;
+                const uint32_t key = chunk < S::c1 ? key_of(Pack<T>::get(S::row + v)) : 0u;
+                append(room, key >= border, entry_of(key, v));
+            }
+    }
+};
 
 // --- a row's outputs
 
@@ -336,10 +478,8 @@ template <typename T> __device__ __forceinline__ float logit_at(const ScoreArgs 
 }
 
 // A work-group per row.
-template <typename T, int NT, typename Src, bool Top>
-__global__ __launch_bounds__(NT, Src::waves) void score_kernel(Args g)
+template <typename T, int NT, bool Top> __global__ __launch_bounds__(NT, 8) void score_kernel(Args g)
 {
-    extern __shared__ u32x4 chunks[];   // [Src::lds_chunks]
     __shared__ ScorePart room[NT / kWave];
     __shared__ double row_lse;
     const ScoreArgs &a = g.a;
@@ -351,34 +491,35 @@ __global__ __launch_bounds__(NT, Src::waves) void score_kernel(Args g)
         return;
     }
     const T *row = (const T *)a.logits + t * a.ld;
-    Src src(row, a.V, 0, 1, chunks);
+    Reader<T, NT> src(row, a.V, 0, 1);
     const float zy = logit_at(a, row, t);
-    src.load();
     Stats s;
-    const float edge[1] = {src.edge_value()};
-    src.template each<true>([&](int, int, const float (&x)[Pack<T>::n]) { absorb<Pack<T>::n>(x, g.c, s); });
-    absorb<1>(edge, g.c, s);
-    const ScorePart p = merge_group<NT>(s, g.c, room);
+    src.stats(g.c, s);
+    __shared__ typename std::conditional<Top, ListRoom<NT>, int>::type list;
+    if constexpr (Top)
+        set_key<NT>(list, key_of(s.m));
+    const ScorePart p = merge_group<NT>(s, g.c, room);   // a barrier, of more than a wave
     if (threadIdx.x < kWave) {
         const double lse = put_scores(a, t, p, zy);
         if (threadIdx.x == 0)
             row_lse = lse;
     }
     if constexpr (Top) {
-        __shared__ ListRoom<NT> list;
-        const int n = list_top<NT>(list, a.top, key_of(s.m),
-                                   [&](auto &&f) { scan_row<T>(src, f); },
-                                   [&](auto &&f) {
-                                       scan_row<T>(Streamed<T, NT>(row, a.V, 0, 1), f);
-                                   });
-        const double lse = row_lse;   // written before list_top's barriers
+        // by the second wave, while the first has the row's statistics to do
+        if (NT == kWave || threadIdx.x / kWave == 1)
+            set_border<NT>(list, a.top);
+        __syncthreads();
+        const int n = list_top<NT>(
+            list, a.top, [&](uint32_t border) { src.list(border, list); },
+            [&](auto &&f) { src.scan(f); });
+        const double lse = row_lse;
         rank_list<NT>(list, n, a.top, [&](int place, uint64_t e) { put_best(a, t, place, e, lse); });
         put_empty<NT>(a, t, n);
     }
 }
 
 // Few rows: each over `parts` work-groups.
-template <typename T, bool Top> __global__ __launch_bounds__(kSplit) void part_kernel(Args g)
+template <typename T, bool Top> __global__ __launch_bounds__(kSplit, 8) void part_kernel(Args g)
 {
     __shared__ ScorePart room[kSplit / kWave];
     const ScoreArgs &a = g.a;
@@ -389,11 +530,12 @@ template <typename T, bool Top> __global__ __launch_bounds__(kSplit) void part_k
     if (a.dlogits && !(a.grad && a.grad[t] != 0.f) && !(a.grad_entropy && a.grad_entropy[t] != 0.f))
         return;
     const T *row = (const T *)a.logits + t * a.ld;
-    const Streamed<T, kSplit> src(row, a.V, part, g.parts);
+    Reader<T, kSplit> src(row, a.V, part, g.parts);
     Stats s;
-    const float edge[1] = {src.edge_value()};
-    src.template each<true>([&](int, int, const float (&x)[Pack<T>::n]) { absorb<Pack<T>::n>(x, g.c, s); });
-    absorb<1>(edge, g.c, s);
+    src.stats(g.c, s);
+    __shared__ typename std::conditional<Top, ListRoom<kSplit>, int>::type list;
+    if constexpr (Top)
+        set_key<kSplit>(list, key_of(s.m));
     const ScorePart p = merge_group<kSplit>(s, g.c, room);
     if (threadIdx.x == 0) {
         a.part[t * g.parts + part] = p;
@@ -401,9 +543,12 @@ template <typename T, bool Top> __global__ __launch_bounds__(kSplit) void part_k
             a.zlab[t] = logit_at(a, row, t);
     }
     if constexpr (Top) {
-        __shared__ ListRoom<kSplit> list;
-        auto scan = [&](auto &&f) { scan_row<T>(src, f); };
-        const int n = list_top<kSplit>(list, a.top, key_of(s.m), scan, scan);
+        if (threadIdx.x / kWave == 1)
+            set_border<kSplit>(list, a.top);
+        __syncthreads();
+        const int n = list_top<kSplit>(
+            list, a.top, [&](uint32_t border) { src.list(border, list); },
+            [&](auto &&f) { src.scan(f); });
         uint64_t *out = a.list + (t * g.parts + part) * a.top;
         rank_list<kSplit>(list, n, a.top, [&](int place, uint64_t e) { out[place] = e; });
         for (int i = n + (int)threadIdx.x; i < a.top; i += kSplit)
@@ -423,24 +568,37 @@ template <bool Top> __global__ __launch_bounds__(kSplit) void join_kernel(Args g
         put_unused<kSplit>(a, t);
         return;
     }
+    __shared__ typename std::conditional<Top, ListRoom<kSplit>, int>::type list;
+    // the parts' alternatives, in the form of values and indices
+    const uint64_t *in = Top ? a.list + t * g.parts * a.top : nullptr;
+    const int all = g.parts * a.top;
+    auto scan = [&](auto &&f) {
+        for (int i = threadIdx.x; i < all; i += kSplit) {
+            const uint64_t e = in[i];
+            f((uint32_t)(e >> kIndexBits), (1 << kIndexBits) - 1 - (int)(e & ((1 << kIndexBits) - 1)));
+        }
+    };
+    if constexpr (Top) {
+        uint32_t most = 0;
+        scan([&](uint32_t key, int) { most = max(most, key); });
+        set_key<kSplit>(list, most);
+        __syncthreads();
+        if (threadIdx.x / kWave == 1)
+            set_border<kSplit>(list, a.top);
+    }
     if (threadIdx.x < kWave) {
         const double lse = put_scores(a, t, merge_parts(a.part + t * g.parts, g.parts, g.c), a.zlab[t]);
         if (threadIdx.x == 0)
             row_lse = lse;
     }
     if constexpr (Top) {
-        __shared__ ListRoom<kSplit> list;
-        const uint64_t *in = a.list + t * g.parts * a.top;
-        const int all = g.parts * a.top;
-        auto scan = [&](auto &&f) {
-            for (int i = threadIdx.x; i < all; i += kSplit) {
-                const uint64_t e = in[i];
-                f((uint32_t)(e >> kIndexBits), (1 << kIndexBits) - 1 - (int)(e & ((1 << kIndexBits) - 1)));
-            }
-        };
-        uint32_t most = 0;
-        scan([&](uint32_t key, int) { most = max(most, key); });
-        const int n = list_top<kSplit>(list, a.top, most, scan, scan);
+        __syncthreads();
+        const int n = list_top<kSplit>(
+            list, a.top,
+            [&](uint32_t border) {
+                scan([&](uint32_t key, int v) { append(list, key >= border, entry_of(key, v)); });
+            },
+            scan);
         const double lse = row_lse;
         rank_list<kSplit>(list, n, a.top, [&](int place, uint64_t e) { put_best(a, t, place, e, lse); });
         put_empty<kSplit>(a, t, n);
@@ -571,15 +729,13 @@ template <typename T> __global__ __launch_bounds__(kSplit) void grad_join_kernel
 
 // ------------------------------------------------------------------ launches
 
-template <typename T, bool Top> struct RunScores {
-    const Args &g;
-    hipStream_t st;
-    template <int NT, typename Src> void operator()() const
-    {
-        hipLaunchKernelGGL((score_kernel<T, NT, Src, Top>), grid_of(g.a.T), dim3(NT),
-                           (size_t)Src::lds_chunks * 16, st, g);
-    }
-};
+template <typename T, int NT> void run_rows(const Args &g, hipStream_t st)
+{
+    if (g.a.top)
+        hipLaunchKernelGGL((score_kernel<T, NT, true>), grid_of(g.a.T), dim3(NT), 0, st, g);
+    else
+        hipLaunchKernelGGL((score_kernel<T, NT, false>), grid_of(g.a.T), dim3(NT), 0, st, g);
+}
 template <typename T> struct RunScoreGrad {
     const Args &g;
     hipStream_t st;
@@ -602,15 +758,20 @@ template <typename T> hipError_t run_scores(const Args &g, hipStream_t st)
             hipLaunchKernelGGL((part_kernel<T, false>), all, dim3(kSplit), 0, st, g);
             hipLaunchKernelGGL((join_kernel<false>), rows, dim3(kSplit), 0, st, g);
         }
-    } else if (a.top) {
-        // the bound of the list needs several threads an alternative
-        const RunScores<T, true> run{g, st};
-        if (a.top > 32 && (long)a.V * (long)sizeof(T) <= 8 << 10)
-            run.template operator()<256, Held<T, 256, 4>>();
-        else
-            with_source<T>(a.V, sizeof(ListRoom<1024>), false, run);
     } else {
-        with_stream<T>(a.V, a.T, RunScores<T, false>{g, st});
+        // Few rows take more threads each; up to 256 KB, more rows at once on a compute unit
+        // load more evenly (8192 rows of 131072 bf16 values with 20 alternatives: 256, 512
+        // and 1024 threads 412, 429 and 444 us; longer ones less so: 3000 of 100003 fp32
+        // 233, 218 and 203).  Many alternatives need threads for their bound.
+        const long bytes = (long)a.V * (long)sizeof(T), few = a.T <= 256 ? 4 : 1;
+        if (few * bytes <= 8 << 10 && a.top <= 32)
+            run_rows<T, 64>(g, st);
+        else if (few * bytes <= 64 << 10)
+            run_rows<T, 256>(g, st);
+        else if (few * bytes <= 256 << 10)
+            run_rows<T, 512>(g, st);
+        else
+            run_rows<T, 1024>(g, st);
     }
     return hipGetLastError();
 }
