@@ -121,7 +121,9 @@ def _sixteen(n):
 
 def _new_eight(T, d, device):
     """int8 [T, d], each row at a multiple of 16 bytes, as the product takes it."""
-    return torch.empty((T, _sixteen(d)), dtype=torch.int8, device=device)[:, :d]
+    wide = _sixteen(d)
+    q = torch.empty((T, wide), dtype=torch.int8, device=device)
+    return q if wide == d else q[:, :d]
 
 
 def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out=None):
