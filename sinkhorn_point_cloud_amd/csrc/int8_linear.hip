@@ -20,6 +20,8 @@ namespace sk {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef i32x4 __attribute__((aligned(2))) i32x4_a2;
+typedef i32x4 __attribute__((aligned(4))) i32x4_a4;
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 struct Args {
@@ -124,10 +126,21 @@ __device__ __forceinline__ void wave_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
-// 16 bytes at any address that suits the type.
-template <typename O, int n> struct alignas(sizeof(O)) Run {
+// 16 bytes of results.
+template <typename O, int n> struct Run {
     O v[n];
 };
+// To any address that suits their type, past the caches that hold the operands (333 x
+// 1500 to 50001 fp32 77 us through them, 51 past them; 4096 x 256 to 64000 bf16 251 and
+// 191).
+__device__ __forceinline__ void put_run(float *p, i32x4 v)
+{
+    __builtin_nontemporal_store(v, reinterpret_cast<i32x4_a4 *>(p));
+}
+__device__ __forceinline__ void put_run(__bf16 *p, i32x4 v)
+{
+    __builtin_nontemporal_store(v, reinterpret_cast<i32x4_a2 *>(p));
+}
 
 // The channels of a run that a lane writes: n0 + at on, of `live`.
 template <typename O, int Cols> struct Channels {
@@ -174,7 +187,7 @@ __device__ __forceinline__ void put_rows(const ProductArgs &a, const Channels<O,
             }
             O *p = out + t * a.ldo;
             if (c.live >= n) {
-                *reinterpret_cast<Run<O, n> *>(p) = v;
+                put_run(p, __builtin_bit_cast(i32x4, v));
             } else {
 #pragma unroll
                 for (int k = 0; k < n; ++k)
@@ -419,26 +432,31 @@ template <typename O> __global__ __launch_bounds__(256) void join_kernel(Args g)
 }
 
 // Which kernel, and the tile.  256 x 256 where such tiles fill the compute units and K is
-// long enough for what surrounds the products to be small: 8192 x 8192 to 8192 474 us
-// against 677 with 128 x 128, which hide it with three work-groups a compute unit (4096 x
-// 256 to 64000 251 us against 307, 333 x 1500 to 50001 56 against 71).  For up to 64
+// long enough for what surrounds the products to be small: 8192 x 8192 to 8192 475 us
+// against 677 with 128 x 128.  Else work-groups that share a compute unit hide it: 256 x
+// 128, two of them, where the tokens fill such tiles (4096 x 1024 to 131072 844 us against
+// 937 with 128 x 128 and 892 with 256 x 256, 1000 x 1000 to 30000 52 against 59 and 55), or
+// 128 x 128, three of them (333 x 1500 to 50001 51 us against 64 and 67).  For up to 64
 // tokens, whose tiles are read for the weights' sake, 64 x 128, or 64 x 64 where the
 // channels are few (40 x 8192 to 32000 45 against 49 us, 64 x 14336 to 4096 45 against 36).
-enum Shape { kStream, kTiles64, kTiles64x128, kTiles128, kTiles256 };
+enum Shape { kStream, kTiles64, kTiles64x128, kTiles128, kTiles256x128, kTiles256 };
+long tiles_of(int T, int N, int BT, int BN) { return ((long)T + BT - 1) / BT * (((long)N + BN - 1) / BN); }
 Shape shape_of(int T, int K, int N)
 {
     if (T <= 16 && N <= 8192)
         return kStream;
     if (T <= 64)
         return N < 32768 ? kTiles64 : kTiles64x128;
-    return T > 128 && K >= 2048 && ((long)T + 255) / 256 * (((long)N + 255) / 256) >= 192 ? kTiles256
-                                                                                           : kTiles128;
+    if (T > 128 && K >= 2048 && tiles_of(T, N, 256, 256) >= 192)
+        return kTiles256;
+    const long padded = ((long)T + 255) / 256 * 256;
+    return K < 2048 && padded <= T * 1.15 && tiles_of(T, N, 256, 128) >= 384 ? kTiles256x128 : kTiles128;
 }
 
 template <typename O, int BT, int BN, int Bytes, int Stages, int Occ>
 void run_tiles(const Args &g, hipStream_t st)
 {
-    const long all = ((long)g.a.T + BT - 1) / BT * (((long)g.a.N + BN - 1) / BN);
+    const long all = tiles_of(g.a.T, g.a.N, BT, BN);
     const size_t stages = (size_t)Stages * (BT + BN) * Bytes, sums = (size_t)4 * 32 * (BN / 2 + 4) * 4;
     hipLaunchKernelGGL((tile_kernel<O, BT, BN, Bytes, Stages, Occ>),
                        dim3((unsigned)((all + 7) / 8 * 8), g.parts), dim3(256), std::max(stages, sums), st, g);
@@ -456,6 +474,7 @@ template <typename O> void run_product(const Args &g, hipStream_t st)
     case kTiles64: run_tiles<O, 64, 64, 64, 4, 4>(g, st); break;
     case kTiles64x128: run_tiles<O, 64, 128, 64, 4, 3>(g, st); break;
     case kTiles128: run_tiles<O, 128, 128, 64, 3, 3>(g, st); break;
+    case kTiles256x128: run_tiles<O, 256, 128, 64, 3, 2>(g, st); break;
     case kTiles256: run_tiles<O, 256, 256, 128, 2, 1>(g, st); break;
     }
 }
@@ -470,7 +489,7 @@ int product_parts(int T, int K, int N)
     if (shape != kTiles64 && shape != kTiles128)
         return 1;
     const int side = shape == kTiles64 ? 64 : 128;
-    const long tiles = ((long)T + side - 1) / side * (((long)N + side - 1) / side);
+    const long tiles = tiles_of(T, N, side, side);
     return (int)std::max(1l, std::min({256 / std::max(tiles, 1l), (long)K / 512, 16l}));
 }
 

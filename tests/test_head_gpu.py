@@ -195,7 +195,8 @@ PRODUCTS = [(1, 1, 1), (1, 16, 5), (3, 15, 17), (16, 64, 16), (2, 4096, 300), (1
             (128, 192, 256), (129, 255, 257), (200, 1500, 500), (65, 5000, 40), (300, 128, 4100),
             (500, 333, 9000), (4097, 200, 4200), (2, 131071, 20), (66, 131071, 20), (5, 200, 8200),
             (16, 4001, 16000), (33, 8000, 90), (64, 777, 33000), (3, 40, 32768), (3000, 2049, 4500),
-            (257, 2311, 49152), (256, 2048, 49153)]
+            (257, 2311, 49152), (256, 2048, 49153),
+            (250, 1999, 25000), (1023, 17, 20001)]
 
 
 def eight_rows(rows, K, g, pad=0):
