@@ -72,7 +72,8 @@ int sinkhorn_rms_norm(const void *x, int dtype, int64_t ldx, const void *residua
  *     q = 127 p / a, rounded to the nearest (ties to even),
  *     scale = a / (127 sqrt(sum h^2 / d + eps)),       y ~ scale q.
  * The norm's factor cancels in q, which is exact.  A row of zeros has q 0 and
- * scale 0; a row with NaN or an infinity has q 0 and scale NaN.
+ * scale 0; a row with NaN or an infinity, or a bf16 one with products beyond fp32, has
+ * q 0 and scale NaN.  Rows at multiples of 128 bytes are read fastest by the product.
  */
 int sinkhorn_rms_norm_int8(const void *x, int dtype, int64_t ldx, const void *residual,
                            int64_t ldr, const void *weight, int T, int d, double eps, int8_t *q,
@@ -104,7 +105,7 @@ int sinkhorn_rms_norm_backward(const void *dy, int dtype, int64_t lddy, const vo
  * Product in 8-bit integers, a scale for each token and each channel:
  *     out[t][n] = xscale[t] wscale[n] sum_k x[t][k] w[n][k] + bias[n],
  * x [T][K], w [N][K] (1 <= K <= 131071, so that sums stay within 32 bits;
- * 1 <= N <= 2^24), out [T][N] in `dtype`, bias [N] fp32 or NULL.  Rows of x and w
+ * 1 <= N <= 2^24, T N <= 2^37), out [T][N] in `dtype`, bias [N] fp32 or NULL.  Rows of x and w
  * start at multiples of 16 bytes (addresses and ldx, ldw): a row's last 16 bytes
  * are read whole, and what lies behind the row in them has no effect.
  * The sum is exact; the scales' product, its product with the sum and the bias's

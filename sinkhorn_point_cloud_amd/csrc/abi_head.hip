@@ -13,7 +13,7 @@ namespace {
 constexpr int kMaxRows = 1 << 24;
 constexpr int64_t kMaxStride = 1ll << 38;
 constexpr int64_t kMaxSpan = 1ll << 58;
-constexpr int64_t kMaxResults = 1ll << 39;   // 2^23 tiles
+constexpr int64_t kMaxResults = 1ll << 37;   // 2^23 tiles of 128 x 128
 
 size_t elem(int dtype) { return dtype == SK_BF16 ? 2 : 4; }
 
