@@ -17,11 +17,11 @@
 // does not matter.  Each thread keeps the maxima of up to 8 groups of its chunks, and
 // only groups that reach the bound are read again.  A row of which more do not fit
 // (many equal values, or the large ones all in one thread's chunks) has its `top`-th
-// value found by bisection first.
+// value found by bisection first (rows of one value: 940 us).
 //
 // What bounds it: HBM.  (A row kept in registers for the second look leaves a compute
 // unit no other row to load meanwhile: 4096 rows of 131072 bf16 values with 64
-// alternatives took 477 us that way.)
+// alternatives took 477 us that way, 201 to 216 this way, 4.6 TB/s.)
 #include "head.h"
 #include "rows.h"
 
@@ -136,11 +136,18 @@ __device__ __forceinline__ float value_of(uint32_t key)
     return key == 0xFFFFFFFFu ? __builtin_nanf("")
                               : __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
-// Value and index in one: the order of alternatives.  0: none.
+// Value and index in one: the order of alternatives.  0: none.  (Values that stand for
+// none, behind a row's end, may come with an index beyond its bits.)
 constexpr int kIndexBits = 24;
+constexpr uint32_t kIndexMask = (1u << kIndexBits) - 1;
 __device__ __forceinline__ uint64_t entry_of(uint32_t key, int v)
 {
-    return (uint64_t)key << kIndexBits | (uint64_t)((1 << kIndexBits) - 1 - v);
+    return (uint64_t)key << kIndexBits | ((kIndexMask - (uint32_t)v) & kIndexMask);
+}
+__device__ __forceinline__ uint32_t key_in(uint64_t entry) { return (uint32_t)(entry >> kIndexBits); }
+__device__ __forceinline__ int index_in(uint64_t entry)
+{
+    return (int)(kIndexMask - ((uint32_t)entry & kIndexMask));
 }
 
 template <int NT> struct ListRoom {
@@ -148,6 +155,7 @@ template <int NT> struct ListRoom {
     uint32_t keys[NT], border;
     uint64_t entry[room + 8];
     int count, wave[NT / kWave];
+    unsigned long long any, all;
     uint16_t flag[room];   // groups of values that reach the border
     int flags;
 };
@@ -242,12 +250,12 @@ template <int NT> __device__ __forceinline__ void set_border(ListRoom<NT> &room,
 }
 
 // Lists the alternatives of a source: `list(border)` appends the values of this thread at
-// or above the border, `scan(f)` calls f(key, index) for every value of this thread.
-// set_key() came before, a barrier, set_border() and another.  Leaves at most its room's
+// or above the border, `scan(most, f)` calls f(key, index) for every value of this thread
+// in the first `most` of `batches` pieces, which come in the order of indices.  set_key() came before, a barrier, set_border() and another.  Leaves at most its room's
 // entries in room.entry, the `top` largest among them (fewer where there are fewer).
 // Returns how many; the list is there for every thread.
 template <int NT, typename List, typename Scan>
-__device__ __forceinline__ int list_top(ListRoom<NT> &room, int top, List &&list, Scan &&scan)
+__device__ __forceinline__ int list_top(ListRoom<NT> &room, int top, int batches, List &&list, Scan &&scan)
 {
     const uint32_t border = room.border;
     list(border);
@@ -255,13 +263,41 @@ __device__ __forceinline__ int list_top(ListRoom<NT> &room, int top, List &&list
     const int n = room.count;
     if (n <= ListRoom<NT>::room)
         return n;
-    // more than fit: the `top`-th entry itself, a bit at a time (entries differ)
-    uint64_t least = 0;
+    // more than fit: the `top`-th entry itself, a bit at a time (entries differ), from the
+    // first bit on in which any two at or above the border do
+    if (threadIdx.x == 0) {
+        room.any = 0;
+        room.all = ~0ull;
+    }
+    __syncthreads();
+    unsigned long long any = 0, all = ~0ull;
+    scan(batches, [&](uint32_t key, int v) {
+        if (key >= border) {
+            any |= entry_of(key, v);
+            all &= entry_of(key, v);
+        }
+    });
+    atomicOr(&room.any, any);
+    atomicAnd(&room.all, all);
+    __syncthreads();
+    const uint64_t differ = room.any ^ room.all;
+    const int first = differ ? 63 - __builtin_clzll(differ) : -1;
+    // where all have one value, the first `top` of them will do
+    int most = batches;
+    if (first < kIndexBits)
+        for (most = 1; most < batches; most *= 2) {
+            int c = 0;
+            scan(most, [&](uint32_t key, int) { c += key >= border; });
+            if (group_count<NT>(c, room.wave) >= top)
+                break;
+        }
+    most = min(most, batches);
+    uint64_t least = first < 0 ? room.all : room.all >> first >> 1 << first << 1;
 #pragma unroll 1
-    for (int bit = 31 + kIndexBits; bit >= 0; --bit) {
+    for (int bit = first; bit >= 0; --bit) {
         const uint64_t with = least | 1ull << bit;
         int c = 0;
-        scan([&](uint32_t key, int v) { c += entry_of(key, v) >= with; });
+        scan(most, [&](uint32_t key, int v) { c += entry_of(key, v) >= with; });
         if (group_count<NT>(c, room.wave) >= top)
             least = with;
     }
@@ -269,7 +305,7 @@ __device__ __forceinline__ int list_top(ListRoom<NT> &room, int top, List &&list
     if (threadIdx.x == 0)
         room.count = 0;
     __syncthreads();
-    scan([&](uint32_t key, int v) {
+    scan(most, [&](uint32_t key, int v) {
         const uint64_t e = entry_of(key, v);
         append(room, e >= least, e);
     });
@@ -368,17 +404,21 @@ template <typename T, int NT> struct Reader : Slice<T, NT> {
         const float x[1] = {edge};
         absorb<1>(x, c, s);
     }
-    // f(key, index) for every value of this thread; values of -inf, or none, among them
-    template <typename F> __device__ __forceinline__ void scan(F &&f) const
+    // f(key, index) for every value of this thread in the first `most` batches, which come
+    // in the order of their indices; values of -inf, or none, among them
+    template <typename F> __device__ __forceinline__ void scan(int most, F &&f) const
     {
-        f(key_of(edge), S::edge_at(threadIdx.x));
+        if (most >= batches || (int)threadIdx.x < S::cut.head)
+            f(key_of(edge), S::edge_at(threadIdx.x));
+        const int end = (int)min((long)S::c1, S::c0 + (long)most * (NT * kBatch));
 #pragma unroll 1
-        for (int b = 0; b < batches; ++b)
-            batch(b, [&](int first, const float (&x)[n]) {
+        for (int i = S::c0 + (int)threadIdx.x; i < end; i += NT) {
+            float x[n];
+            Pack<T>::open(*S::chunk(i), x);
 #pragma unroll
-                for (int k = 0; k < n; ++k)
-                    f(key_of(x[k]), first + k);
-            });
+            for (int k = 0; k < n; ++k)
+                f(key_of(x[k]), S::cut.head + i * n + k);
+        }
     }
     // Appends the values at or above the border: first the groups that have any, then
     // their values, dealt to all threads.  More groups than fit count as more values than
@@ -427,8 +467,8 @@ __device__ __forceinline__ bool row_used(const ScoreArgs &a, long t)
 // Writes an alternative, or what marks an empty place.
 __device__ __forceinline__ void put_best(const ScoreArgs &a, long t, int place, uint64_t e, double lse)
 {
-    const int v = (1 << kIndexBits) - 1 - (int)(e & ((1 << kIndexBits) - 1));
-    const float x = value_of((uint32_t)(e >> kIndexBits));
+    const int v = index_in(e);
+    const float x = value_of(key_in(e));
     a.index[t * a.top + place] = v;
     a.best[t * a.top + place] = (float)((double)x * a.scale - lse);
 }
@@ -510,8 +550,8 @@ template <typename T, int NT, bool Top> __global__ __launch_bounds__(NT, 8) void
             set_border<NT>(list, a.top);
         __syncthreads();
         const int n = list_top<NT>(
-            list, a.top, [&](uint32_t border) { src.list(border, list); },
-            [&](auto &&f) { src.scan(f); });
+            list, a.top, src.batches, [&](uint32_t border) { src.list(border, list); },
+            [&](int most, auto &&f) { src.scan(most, f); });
         const double lse = row_lse;
         rank_list<NT>(list, n, a.top, [&](int place, uint64_t e) { put_best(a, t, place, e, lse); });
         put_empty<NT>(a, t, n);
@@ -547,8 +587,8 @@ template <typename T, bool Top> __global__ __launch_bounds__(kSplit, 8) void par
             set_border<kSplit>(list, a.top);
         __syncthreads();
         const int n = list_top<kSplit>(
-            list, a.top, [&](uint32_t border) { src.list(border, list); },
-            [&](auto &&f) { src.scan(f); });
+            list, a.top, src.batches, [&](uint32_t border) { src.list(border, list); },
+            [&](int most, auto &&f) { src.scan(most, f); });
         uint64_t *out = a.list + (t * g.parts + part) * a.top;
         rank_list<kSplit>(list, n, a.top, [&](int place, uint64_t e) { out[place] = e; });
         for (int i = n + (int)threadIdx.x; i < a.top; i += kSplit)
@@ -572,15 +612,15 @@ template <bool Top> __global__ __launch_bounds__(kSplit) void join_kernel(Args g
     // the parts' alternatives, in the form of values and indices
     const uint64_t *in = Top ? a.list + t * g.parts * a.top : nullptr;
     const int all = g.parts * a.top;
-    auto scan = [&](auto &&f) {
+    auto scan = [&](int, auto &&f) {   // one piece
         for (int i = threadIdx.x; i < all; i += kSplit) {
             const uint64_t e = in[i];
-            f((uint32_t)(e >> kIndexBits), (1 << kIndexBits) - 1 - (int)(e & ((1 << kIndexBits) - 1)));
+            f(key_in(e), index_in(e));
         }
     };
     if constexpr (Top) {
         uint32_t most = 0;
-        scan([&](uint32_t key, int) { most = max(most, key); });
+        scan(1, [&](uint32_t key, int) { most = max(most, key); });
         set_key<kSplit>(list, most);
         __syncthreads();
         if (threadIdx.x / kWave == 1)
@@ -594,9 +634,9 @@ template <bool Top> __global__ __launch_bounds__(kSplit) void join_kernel(Args g
     if constexpr (Top) {
         __syncthreads();
         const int n = list_top<kSplit>(
-            list, a.top,
+            list, a.top, 1,
             [&](uint32_t border) {
-                scan([&](uint32_t key, int v) { append(list, key >= border, entry_of(key, v)); });
+                scan(1, [&](uint32_t key, int v) { append(list, key >= border, entry_of(key, v)); });
             },
             scan);
         const double lse = row_lse;

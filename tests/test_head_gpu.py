@@ -337,6 +337,9 @@ def test_alternatives_of_ties_and_crowds(T, V, dt):
         z[4] = torch.arange(V).float() / 8
         z[4, ::64] += 1e5
     z = z.to(TYPES[dt]).cuda()
+    # the lowest finite value but for a few larger ones, the last of them behind all chunks
+    z[-1] = torch.finfo(z.dtype).min
+    z[-1, V - 1] = z[-1, V // 2] = 3.0
     for top in (1, 40, 128):
         got = sk.token_scores(z, None, top=top)
         keep = list(range(min(T, 5))) + [T - 1]
@@ -344,6 +347,21 @@ def test_alternatives_of_ties_and_crowds(T, V, dt):
         assert torch.equal(got[3][keep].cpu(), index)
         tol = (2 * H.U + L.U) * (best.abs().nan_to_num(posinf=0.0) + got[1][keep].cpu().double().abs()[:, None])
         H.check(got[4][keep], (best, tol + H.TINY), "best")
+
+
+def test_ties_of_the_longest_rows():
+    """Equal values throughout rows that end at the last index there is, where what stands for none
+    behind the row's end has an index beyond it."""
+    for V in ((1 << 24) - 5, 1 << 24):
+        z = torch.zeros(2, V, device="cuda")
+        z[1, V - 3:] = 1.0
+        _, lse, ent, index, best = sk.token_scores(z, top=40)
+        assert index[0].tolist() == list(range(40))
+        assert index[1].tolist() == [V - 3, V - 2, V - 1] + list(range(37))
+        # S = V, exact sums of ones; lse and entropy are log V
+        H.check(lse[:1], (torch.tensor([math.log(V)]).double(), 2 * H.U * math.log(V)), "lse")
+        H.check(ent[:1], (torch.tensor([math.log(V)]).double(), 2 * H.U * math.log(V)), "entropy")
+        H.check(best[0], (torch.full((40,), -math.log(V)).double(), 2 * H.U * math.log(V)), "best")
 
 
 @pytest.mark.parametrize("T,V", [(5, 300), (5, 9000), (6, 70001), (200, 500)])
