@@ -95,8 +95,16 @@ def _beside(x, like, what):
     if not isinstance(x, torch.Tensor) or x.dtype != like.dtype or x.shape != like.shape \
             or x.device != like.device:
         raise ValueError(f"{what} must be {like.dtype} {tuple(like.shape)} on {like.device}")
+    if x.is_contiguous():
+        return x, like.shape[1]
     x, _, _, _, ld = _matrix(x, what)
     return x, ld
+
+
+def _new_like(x):
+    """An output of the shape and type of x, its rows side by side (for a contiguous x the call that
+    takes least time)."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 def _out_matrix(x, shape, dtype, device, what):
@@ -143,8 +151,8 @@ def rms_norm(x, weight=None, residual=None, eps: float = 1e-6, out=None):
         ldh = 0 if h is None else _out_matrix(h, (T, d), x.dtype, dev, "h")
         kept = h
     else:
-        y, ldy = torch.empty((T, d), dtype=x.dtype, device=dev), d
-        h = x if residual is None else torch.empty((T, d), dtype=x.dtype, device=dev)
+        y, ldy = _new_like(x), d
+        h = x if residual is None else _new_like(x)
         kept, ldh = (None, 0) if residual is None else (h, d)
     _run(lib.sinkhorn_rms_norm, dev, _at(x), dt, ldx, _at(residual), ldr, _at(weight), T, d, eps,
          _at(y), ldy, _at(kept), ldh)
@@ -171,7 +179,7 @@ def rms_norm_int8(x, weight=None, residual=None, eps: float = 1e-6, out=None):
         q = _new_eight(T, d, dev)
         ldq = q.stride(0)
         scale = torch.empty(T, dtype=torch.float32, device=dev)
-        h = x if residual is None else torch.empty((T, d), dtype=x.dtype, device=dev)
+        h = x if residual is None else _new_like(x)
         kept, ldh = (None, 0) if residual is None else (h, d)
     _run(lib.sinkhorn_rms_norm_int8, dev, _at(x), dt, ldx, _at(residual), ldr, _at(weight), T, d,
          eps, _at(q), ldq, _at(scale), _at(kept), ldh)
@@ -223,7 +231,7 @@ def rms_norm_backward(dy, h, weight=None, dh=None, eps: float = 1e-6, out=None, 
         lddx = _out_matrix(dx, (T, d), h.dtype, dev, "dx")
         _check_out(((dw, (d,)),), torch.float32, dev, "out")
     else:
-        dx, lddx = torch.empty((T, d), dtype=h.dtype, device=dev), d
+        dx, lddx = _new_like(h), d
         dw = None if weight is None else torch.empty(d, dtype=torch.float32, device=dev)
     ws = _space(SK_OP_RMS_NORM_BACKWARD, T, d, 0, dt, dev, workspace)
     _run(lib.sinkhorn_rms_norm_backward, dev, _at(dy), dt, lddy, _at(h), ldh, _at(weight), _at(dh),
@@ -299,8 +307,9 @@ def token_scores(logits, labels=None, top: int = 0, scale: float = 1.0, out=None
                    dev, "out")
         _check_out(((index, (T, top)),), torch.int32, dev, "out")
     else:
-        logp, lse, entropy = (torch.empty(T, dtype=torch.float32, device=dev) for _ in range(3))
-        logp = None if labels is None else logp
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        entropy = torch.empty_like(lse)
+        logp = None if labels is None else torch.empty_like(lse)
         index = torch.empty((T, top), dtype=torch.int32, device=dev) if top else None
         best = torch.empty((T, top), dtype=torch.float32, device=dev) if top else None
     ws = _space(SK_OP_TOKEN_SCORES, T, V, top, dt, dev, workspace)
