@@ -73,7 +73,7 @@ int sinkhorn_rms_norm(const void *x, int dtype, int64_t ldx, const void *residua
  *     scale = a / (127 sqrt(sum h^2 / d + eps)),       y ~ scale q.
  * The norm's factor cancels in q, which is exact.  A row of zeros has q 0 and
  * scale 0; a row with NaN or an infinity, or a bf16 one with products beyond fp32, has
- * q 0 and scale NaN.  Rows at multiples of 128 bytes are read fastest by the product.
+ * q 0 and scale NaN (bf16 products below fp32's normal range lose bits).  Rows at multiples of 128 bytes are read fastest by the product.
  */
 int sinkhorn_rms_norm_int8(const void *x, int dtype, int64_t ldx, const void *residual,
                            int64_t ldr, const void *weight, int T, int d, double eps, int8_t *q,
@@ -94,7 +94,8 @@ int sinkhorn_quantize_int8(const void *x, int dtype, int64_t ldx, int T, int d, 
  *     dx = r (u - h r^2 (sum u h) / d) + dh            (x's and the residual's),
  *     dweight_j = sum over rows of dy_j h_j r           (fp32 [d]; NULL: none).
  * dx may be dy, dh or h itself.  Sums within a row are fp64; those of dweight
- * are fp32 over up to T / 1024 + 1 rows (rounded up to whole work-groups) and fp64 beyond.
+ * are fp32 over up to T / 1024 + 1 rows (rounded up to whole work-groups) and fp64 beyond;
+ * r and r^3 (sum u h) / d have to lie within fp32.
  */
 int sinkhorn_rms_norm_backward(const void *dy, int dtype, int64_t lddy, const void *h,
                                int64_t ldh, const void *weight, const void *dh, int64_t lddh,

@@ -481,33 +481,35 @@ norm_grad_kernel(NormGradArgs a, int G)
 }
 #undef SK_PLACE
 
-// dweight from the workers' shares: 64 columns a work-group, 16 threads a column, eight
-// shares asked for together.
+// dweight from the workers' shares: C columns a work-group, 1024 / C threads a column,
+// eight shares asked for together.
+template <int C>
 __global__ __launch_bounds__(1024) void norm_join_kernel(const float *part, int G, int d, float *dweight)
 {
-    __shared__ double room[16][kWave];
-    const int at = blockIdx.x * kWave + lane_id(), slice = threadIdx.x / kWave;
+    constexpr int slices = 1024 / C;
+    __shared__ double room[slices][C];
+    const int column = threadIdx.x % C, at = blockIdx.x * C + column, slice = threadIdx.x / C;
     double v = 0.0;
     if (at < d) {
         int g = slice;
-        for (; g + 7 * 16 < G; g += 8 * 16) {
+        for (; g + 7 * slices < G; g += 8 * slices) {
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                x[i] = part[(long)(g + i * 16) * d + at];
+                x[i] = part[(long)(g + i * slices) * d + at];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v += (double)x[i];
         }
-        for (; g < G; g += 16)
+        for (; g < G; g += slices)
             v += (double)part[(long)g * d + at];
     }
-    room[slice][lane_id()] = v;
+    room[slice][column] = v;
     __syncthreads();
     if (slice == 0 && at < d) {
 #pragma unroll
-        for (int i = 1; i < 16; ++i)
-            v += room[i][lane_id()];
+        for (int i = 1; i < slices; ++i)
+            v += room[i][column];
         dweight[at] = (float)v;
     }
 }
@@ -582,8 +584,11 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t st)
 
 int norm_groups(int T, int d, int dtype)
 {
+    // workers of a wave are more, where they still have eight rows each (65536 x 512 bf16: with
+    // 1024, 2048 and 4096 of them 69, 50 and 44 us, the join 5, 6 and 10)
     const int per = rows_per_group(chunks_of(d, dtype));
-    return std::min((T + per - 1) / per * per, 1024);
+    const int most = per > 1 ? std::clamp(T / 8 / per * per, 1024, 2048) : 1024;
+    return std::min((T + per - 1) / per * per, most);
 }
 
 hipError_t launch_norm_backward(const NormGradArgs &a, hipStream_t st)
@@ -595,9 +600,12 @@ hipError_t launch_norm_backward(const NormGradArgs &a, hipStream_t st)
         else
             with_shape<float>(chunks, RunGrad<float>{a, G, st});
     }
-    if (a.dweight)
-        hipLaunchKernelGGL(norm_join_kernel, dim3((a.d + kWave - 1) / kWave), dim3(1024), 0, st,
-                           a.part, G, a.d, a.dweight);
+    if (a.dweight && a.d <= 1024)
+        hipLaunchKernelGGL((norm_join_kernel<16>), dim3((a.d + 15) / 16), dim3(1024), 0, st, a.part, G, a.d,
+                           a.dweight);
+    else if (a.dweight)
+        hipLaunchKernelGGL((norm_join_kernel<64>), dim3((a.d + 63) / 64), dim3(1024), 0, st, a.part, G, a.d,
+                           a.dweight);
     return hipGetLastError();
 }
 
