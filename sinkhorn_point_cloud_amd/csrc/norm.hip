@@ -12,8 +12,8 @@
 // counts as zeros; so do the chunks of threads beyond the row, which read its last one
 // again.  The loads are then the same for all threads and asked for together.  (With a
 // path for the end of its own, value by value, 777 rows of 2501 fp32 values took 9.8 us,
-// the gradient 16.3.)  A thread writes only what it alone has read, so an output may be
-// an input itself.
+// the gradient 16.3.)  A thread writes only values that no other counts, behind its own
+// reads of them, so an output may be an input itself.
 // Sums within a row are fp64: squares of any finite input stay in range, and the
 // row's factor is off by no more than its own rounding.
 #include "head.h"

@@ -251,8 +251,9 @@ template <int NT> __device__ __forceinline__ void set_border(ListRoom<NT> &room,
 
 // Lists the alternatives of a source: `list(border)` appends the values of this thread at
 // or above the border, `scan(most, f)` calls f(key, index) for every value of this thread
-// in the first `most` of `batches` pieces, which come in the order of indices.  set_key() came before, a barrier, set_border() and another.  Leaves at most its room's
-// entries in room.entry, the `top` largest among them (fewer where there are fewer).
+// in the first `most` of `batches` pieces, which come in the order of indices.  set_key()
+// came before, a barrier, set_border() and another.  Leaves at most its room's entries in
+// room.entry, the `top` largest among them (fewer where there are fewer).
 // Returns how many; the list is there for every thread.
 template <int NT, typename List, typename Scan>
 __device__ __forceinline__ int list_top(ListRoom<NT> &room, int top, int batches, List &&list, Scan &&scan)
