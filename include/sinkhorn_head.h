@@ -89,13 +89,14 @@ int sinkhorn_quantize_int8(const void *x, int dtype, int64_t ldx, int T, int d, 
 
 /*
  * Gradient of sinkhorn_rms_norm from dy = dL/dy and dh, what reaches h along
- * the residual stream (NULL: nothing).  With r = 1 / sqrt(sum h^2 / d + eps)
- * and u = dy weight,
- *     dx = r (u - h r^2 (sum u h) / d) + dh            (x's and the residual's),
- *     dweight_j = sum over rows of dy_j h_j r           (fp32 [d]; NULL: none).
+ * the residual stream (NULL: nothing).  With r = 1 / sqrt(sum h^2 / d + eps),
+ * n = h r and u = dy weight,
+ *     dx = r (u - n (r sum u h) / d) + dh               (x's and the residual's),
+ *     dweight_j = sum over rows of dy_j n_j             (fp32 [d]; NULL: none).
  * dx may be dy, dh or h itself.  Sums within a row are fp64; those of dweight
- * are fp32 over up to T / 1024 + 1 rows (rounded up to whole work-groups) and fp64 beyond;
- * r and r^3 (sum u h) / d have to lie within fp32.
+ * are fp32 over up to T / 1024 + 1 rows (rounded up to whole work-groups) and fp64 beyond.
+ * u is fp32: where it lies below 1e36 and within fp32's normal range, any row of finite h has
+ * its gradient.
  */
 int sinkhorn_rms_norm_backward(const void *dy, int dtype, int64_t lddy, const void *h,
                                int64_t ldh, const void *weight, const void *dh, int64_t lddh,

@@ -3,8 +3,8 @@
 //
 //     h = round(x + residual),  r = 1 / sqrt(sum h^2 / d + eps),  y = h w r;
 //     8 bits: p = h w, a = max |p|,  q = rint(127 p / a),  scale = a r / 127;
-//     backward, u = dy w:  dx = r (u - h r^2 (sum u h) / d) + dh,
-//                          dweight_j = sum over rows of dy_j h_j r.
+//     backward, u = dy w, n = h r:  dx = r (u - n (r sum u h) / d) + dh,
+//                                   dweight_j = sum over rows of dy_j n_j.
 // What bounds it: HBM.  A row is read once and kept in registers as 16-byte chunks,
 // chunk i + j NT with thread i of the row's NT.  Rows at any address: the hardware loads
 // and stores 16 bytes at any multiple of the type's size.  A row that ends inside a
@@ -448,8 +448,10 @@ norm_grad_kernel(NormGradArgs a, int G)
             packed(gv[j]);
             packed(wv[j]);
         }
+        // n is at most sqrt(d) and the mean of u n at most u's: factors that leave fp32 in no row
+        // whose gradient does not (r^3 (sum u h) / d and dy r are 0 for rows of 1e20 and small dy)
         const double r = 1.0 / sqrt(ss / d + a.eps);
-        const float rf = (float)r, c = (float)(r * r * r * (uh / d));
+        const float rf = (float)r, mean = (float)(r * (uh / d));
         T *dx = (T *)a.dx + t * a.lddx;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -461,9 +463,9 @@ norm_grad_kernel(NormGradArgs a, int G)
             Pack<T>::open(NV <= 2 ? ev[j] : beside(j), e);
 #pragma unroll
             for (int k = 0; k < n; ++k) {
-                const float yr = y[k] * rf;
-                acc[j][k] = fmaf(yr, x[k], acc[j][k]);
-                y[k] = fmaf(-c, x[k], yr * w[k]) + e[k];
+                const float norm = x[k] * rf;
+                acc[j][k] = fmaf(y[k], norm, acc[j][k]);
+                y[k] = fmaf(rf, fmaf(-norm, mean, y[k] * w[k]), e[k]);
             }
             put_chunk(dx, at, d, Pack<T>::close(y));
         }
