@@ -71,9 +71,10 @@ int sinkhorn_rms_norm(const void *x, int dtype, int64_t ldx, const void *residua
  * a = max |p| over the row,
  *     q = 127 p / a, rounded to the nearest (ties to even),
  *     scale = a / (127 sqrt(sum h^2 / d + eps)),       y ~ scale q.
- * The norm's factor cancels in q, which is exact.  A row of zeros has q 0 and
+ * The norm's factor cancels in q, which is exact to the last tie (but for bf16
+ * products below fp32's normal range, which lose bits).  A row of zeros has q 0 and
  * scale 0; a row with NaN or an infinity, or a bf16 one with products beyond fp32, has
- * q 0 and scale NaN (bf16 products below fp32's normal range lose bits).  Rows at multiples of 128 bytes are read fastest by the product.
+ * q 0 and scale NaN.  Rows at multiples of 128 bytes are read fastest by the product.
  */
 int sinkhorn_rms_norm_int8(const void *x, int dtype, int64_t ldx, const void *residual,
                            int64_t ldr, const void *weight, int T, int d, double eps, int8_t *q,

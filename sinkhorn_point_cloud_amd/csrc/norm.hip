@@ -171,8 +171,9 @@ template <bool Alone, typename P> __device__ __forceinline__ P row_most(P v, P *
 
 // 127 p / a to the nearest whole number, ties to even, where a = m 2^e with m in
 // [1/2, 1): from the fp32 quotient, off by less than 1e-4, unless that is nearer to
-// the middle of two; there the sign of 127 p - (k + 1/2) a decides, which is exact
-// in fp64 for bf16 products (and off by 2^-53 for fp32 ones).
+// the middle of two; there the sign of 127 p - (k + 1/2) a decides.  127 p of a fp32
+// product (48 bits) has up to 55 bits: its rounding and what that left out.  Both, and
+// the difference so near the middle (of at most 43 bits), are exact in fp64.
 __device__ __forceinline__ float quotient(double p, int e, float inv)
 {
     return (float)__builtin_amdgcn_ldexp(p, -e) * inv;
@@ -188,7 +189,8 @@ __device__ __forceinline__ bool near_middle(float t)
 __device__ __forceinline__ int step_exact(double p, double a, float t)
 {
     const double k = __builtin_floor((double)t);
-    const double gap = fma(-(k + 0.5), a, 127.0 * p);
+    const double much = 127.0 * p, rest = fma(127.0, p, -much);
+    const double gap = fma(-(k + 0.5), a, much) + rest;
     const int low = (int)k;
     return gap > 0.0 || (gap == 0.0 && (low & 1)) ? low + 1 : low;
 }
