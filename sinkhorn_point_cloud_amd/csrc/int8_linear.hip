@@ -106,11 +106,11 @@ template <typename O> __global__ __launch_bounds__(256) void stream_kernel(Args 
 
 // 16 bytes a lane into shared memory, a wave's KB in a run from `to` on.  In asm, so
 // that reads of other stages do not wait for it; the waits are in wait_stage().  (A
-// write of m0 needs a wait state before the load that reads it; nothing else here uses m0.)
+// write of m0 needs a wait state before the load that reads it.)
 __device__ __forceinline__ void copy16(const int8_t *from, uint32_t to)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from)
-                 : "memory");
+                 : "memory", "m0");
 }
 // Waits until all but `Left` of this wave's copies are there and its reads of shared
 // memory are done, then for the other waves.
