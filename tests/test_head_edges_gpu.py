@@ -109,3 +109,105 @@ def test_eight_bits_of_weighted_fp32_rows_beside_ties():
             want[t, 2 * t], want[t, 2 * t + 1] = 127, sign * nearest(hp * wp, ha * wa)
         q, _, _ = sk.rms_norm_int8((h * scale).cuda(), w.cuda())
         assert torch.equal(q.cpu(), want), (sign, scale)
+
+
+# --- gradients against differences
+
+def score_directions(dt):
+    """Few, peaked logits on a grid of 2^-5 (7 bits and a sign below 4, exact also one step away), a
+    label that is not the likeliest, and weights of logp and entropy."""
+    g = rng(41)
+    T, V = 5, 12
+    z = torch.randint(-90, 91, (T, V), generator=g).float() / 32
+    y = z.argsort(1)[:, V // 2].int()
+    return (z.to(TYPES[dt]), y, 0.5 + torch.rand(T, generator=g), -0.5 - torch.rand(T, generator=g))
+
+
+def slack_of(z, wl, we, grad, h):
+    """What a central difference of step h along +-1 may be off from grad's part in that direction.
+    With x the direction and Z the logits (range R) under the row's q, logp''' = -k3(x) and
+    H''' = -(k(Z, x, x, x) + 2 k3(x)), joint cumulants: |k3| <= 0.77 for |x| <= 1, and
+    |k(Z, x, x, x)| <= E|Z - EZ||x - Ex|^3 + 3 |cov(Z, x)| var(x) <= 2 R + 3 R / 2, since |x - Ex| <= 2,
+    var(x) <= 1, |cov(Z, x)| <= R / 2.  The central difference is off by h^2 / 6 times that.  Outputs of
+    at most 16 are off by less than 16 U + 2e-7, twice, over 2 h; gradient entries by half a step of
+    their type and 2e-6 of fp32 arithmetic."""
+    R = (z.double().amax(1) - z.double().amin(1)).max() + 2 * h
+    wl, we = wl.abs().double().sum(), we.abs().double().sum()
+    return h * h / 6 * (wl * 0.77 + we * (3.5 * R + 1.54)) + (wl + we) * (16 * H.U + 2e-7) / h \
+        + (H.HALF[z.dtype] + 2e-6) * grad.double().abs().sum()
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_score_gradients_against_differences(dt):
+    """Along the signs of the gradient, where the difference is the sum of its magnitudes: logp and
+    entropy alone and together.  A gradient of zeros and one of the entropy's sign reversed are far
+    outside of the slack."""
+    z, y, wl, we = score_directions(dt)
+    h = 2.0 ** -5
+    yd, wld, wed = y.cuda(), wl.cuda(), we.cuda()
+
+    def grad(a, b):
+        return sk.token_scores_backward(z.cuda(), yd, a, b).cpu().double()
+
+    def difference(a, b, x):
+        def total(s):
+            moved = (z.float() + s * x).to(z.dtype)
+            assert torch.equal(moved.double(), z.double() + s * x.double())
+            o = sk.token_scores(moved.cuda(), yd)
+            return (a.double() * o[0].cpu().double() + b.double() * o[2].cpu().double()).sum()
+        return (total(h) - total(-h)) / (2 * h)
+    zero = torch.zeros_like(wl)
+    dl, de, both = grad(wld, None), grad(None, wed), grad(wld, wed)
+    for d, a, b in ((dl, wl, zero), (de, zero, we), (both, wl, we)):
+        x = d.sign().float()
+        diff, slack = difference(a, b, x), slack_of(z, a, b, d, h)
+        assert abs(diff - (d * x).sum()) < slack
+        assert abs(diff) > 8 * slack                                   # zeros
+    x = both.sign().float()
+    # the slack of both, and how far the entropy's part reversed or left out would be off
+    assert abs((de * x).sum()) > 2 * slack_of(z, wl, we, both, h)
+    for d, x in ((dl, dl.sign().float()), (de, de.sign().float())):
+        assert abs((both * x).sum() - (d * x).sum()) > 2 * slack_of(z, wl, we, both, h)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("weighted", [False, True])
+def test_norm_gradients_against_differences(weighted, dt):
+    """dx along its own signs, dweight along its own: sums of magnitudes.  The difference's own error
+    is that of the formula in fp64; y is off by half a step and 3 U, its sums with dy are fp64."""
+    g = rng(42)
+    T, d, h, eps = 4, 48, 2.0 ** -3, 0.5
+    x = (torch.randint(-12, 13, (T, d), generator=g).float() / 8).to(TYPES[dt])
+    w = ((torch.randint(4, 13, (d,), generator=g).float() / 8) if weighted else torch.ones(d)).to(x.dtype)
+    # half of dy follows x, so that the projection is a large part
+    dy = (torch.randint(-4, 5, (T, d), generator=g).float() / 8 + x.float()).to(x.dtype)
+    dh = (torch.randint(-4, 5, (T, d), generator=g).float() / 8).to(x.dtype)
+    dx, dw = sk.rms_norm_backward(dy.cuda(), x.cuda(), w.cuda(), dh=dh.cuda(), eps=eps)
+    dx, dw = dx.cpu().double(), dw.cpu().double()
+
+    def total(x_, w_, here):
+        y = sk.rms_norm(x_.cuda(), w_.cuda(), eps=eps)[0].cpu().double() if here \
+            else H.norm(x_, w_, eps, torch.float64)[0]
+        return (y * dy.double()).sum() + (x_.double() * dh.double()).sum()
+
+    def moved(a, s, way):
+        b = (a.float() + s * way.float()).to(a.dtype)
+        assert torch.equal(b.double(), a.double() + s * way.double())
+        return b
+
+    way = dx.sign()
+    here, there = ((total(moved(x, h, way), w, k) - total(moved(x, -h, way), w, k)) / (2 * h)
+                   for k in (True, False))
+    size = H.norm(x, w, eps, torch.float64)[0].abs() + h * w.double()
+    rounding = ((H.HALF[x.dtype] + 4 * H.U) * size * dy.double().abs()).sum() / h
+    (ref, tol), _ = H.norm_backward(dy, x, w, dh, eps)
+    slack = rounding + abs(there - (ref * way).sum()) + tol.sum()
+    assert abs(here - dx.abs().sum()) < slack and dx.abs().sum() > 4 * slack
+    # without its projection on h it would be seen
+    u = dy.double() * w.double()
+    bare = H.factor(x, eps) * u + dh.double()
+    assert abs((bare * way).sum() - dx.abs().sum()) > 2 * slack
+    way = dw.sign()
+    here = (total(x, moved(w, h, way), True) - total(x, moved(w, -h, way), True)) / (2 * h)
+    assert abs(here - dw.abs().sum()) < rounding + 1e-5 * dw.abs().sum()
+    assert dw.abs().sum() > 4 * rounding
