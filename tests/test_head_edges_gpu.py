@@ -211,3 +211,68 @@ def test_norm_gradients_against_differences(weighted, dt):
     here = (total(x, moved(w, h, way), True) - total(x, moved(w, -h, way), True)) / (2 * h)
     assert abs(here - dw.abs().sum()) < rounding + 1e-5 * dw.abs().sum()
     assert dw.abs().sum() > 4 * rounding
+
+
+# --- outputs over inputs
+
+# lengths that end inside a chunk (of 8 bf16 or 4 fp32 values), of each launch shape
+OVER = [(9, 61), (5, 515), (4, 1029), (3, 4099), (3, 16389), (2, 32765)]
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("T,d", OVER)
+def test_norm_outputs_over_inputs(T, d, dt):
+    """y and h over x and the residual, either way, and h over either with y in 8 bits: the bits of
+    outputs of their own."""
+    g = rng(T + d)
+    x, r, w = norm_case(T, d, dt, g)
+    wd = w.cuda()
+
+    def inputs():
+        return padded(x, 3, 1)[0], padded(r, 3, 1)[0]
+    xd, rd = inputs()
+    y, h = sk.rms_norm(xd, wd, rd)
+    q, scale, _ = sk.rms_norm_int8(xd, wd, rd)
+    assert torch.equal(h.cpu(), H.stream(x, r))
+    for swap in (False, True):
+        xd, rd = inputs()
+        to = (rd, xd) if swap else (xd, rd)
+        got = sk.rms_norm(xd, wd, rd, out=to)
+        assert torch.equal(to[0], y) and torch.equal(to[1], h) and got[0] is to[0]
+        xd, rd = inputs()
+        over, other, kept = (rd, xd, x) if swap else (xd, rd, r)
+        got = sk.rms_norm_int8(xd, wd, rd, out=(torch.empty_like(q), torch.empty_like(scale), over))
+        assert torch.equal(got[0], q) and torch.equal(got[1], scale) and torch.equal(over, h)
+        assert torch.equal(other.cpu(), kept)
+        xd, rd = inputs()
+        over = rd if swap else xd
+        sk.rms_norm(xd, wd, rd, out=(over, None))
+        assert torch.equal(over, y)
+    xd, _ = inputs()
+    y, _ = sk.rms_norm(xd, wd)
+    q, scale, _ = sk.rms_norm_int8(xd, wd)
+    got = sk.rms_norm_int8(xd, wd, out=(torch.empty_like(q), torch.empty_like(scale), xd))
+    assert torch.equal(got[0], q) and torch.equal(xd.cpu(), x)
+    # y in 8 bits where x was is no input itself
+    with pytest.raises(sk.SinkhornError):
+        sk.rms_norm_int8(xd, wd, out=(xd.view(torch.int8)[:, :d], scale, None))
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("T,d", OVER)
+def test_norm_gradient_over_inputs(T, d, dt):
+    g = rng(T * 3 + d)
+    h, dh, w = norm_case(T, d, dt, g)
+    dy = torch.randn(T, d, generator=g).to(h.dtype)
+    wd = w.cuda()
+
+    def inputs():
+        return [padded(a, 5, 1)[0] for a in (dy, h, dh)]
+    a, b, c = inputs()
+    dx, dw = sk.rms_norm_backward(a, b, wd, dh=c)
+    H.check(dx, H.norm_backward(dy, h, w, dh, 1e-6)[0], "dx")
+    for k in range(3):
+        a, b, c = inputs()
+        over = (a, b, c)[k]
+        got, dw2 = sk.rms_norm_backward(a, b, wd, dh=c, out=(over, torch.empty_like(dw)))
+        assert torch.equal(over, dx) and torch.equal(dw2, dw)
