@@ -276,3 +276,21 @@ def test_norm_gradient_over_inputs(T, d, dt):
         over = (a, b, c)[k]
         got, dw2 = sk.rms_norm_backward(a, b, wd, dh=c, out=(over, torch.empty_like(dw)))
         assert torch.equal(over, dx) and torch.equal(dw2, dw)
+
+
+# --- many rows
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("T,d", [(2500, 96), (1023, 300), (1025, 2056), (9001, 40), (70001, 24),
+                                 (131072, 8), (20000, 1100), (300001, 3)])
+def test_weight_gradient_of_many_rows(T, d, dt):
+    """No worker of the T rows adds up more than T / 1024 + 1 of them in fp32."""
+    g = rng(T + d)
+    h = torch.randn(T, d, generator=g).to(TYPES[dt])
+    dy = torch.randn(T, d, generator=g).to(TYPES[dt])
+    dy += 0.5           # sums that grow with T
+    w = (1 + 0.3 * torch.randn(d, generator=g)).to(TYPES[dt])
+    dx, dw = sk.rms_norm_backward(dy.cuda(), h.cuda(), w.cuda())
+    wx, ww = H.norm_backward(dy, h, w, None, 1e-6, workers=min(T, 1024))
+    H.check(dw, ww, "dweight")
+    H.check(dx, wx, "dx")
