@@ -294,3 +294,41 @@ def test_weight_gradient_of_many_rows(T, d, dt):
     wx, ww = H.norm_backward(dy, h, w, None, 1e-6, workers=min(T, 1024))
     H.check(dw, ww, "dweight")
     H.check(dx, wx, "dx")
+
+
+# --- rows far into their matrices
+
+def test_gradients_of_rows_beyond_32_bit_offsets():
+    """The last of rows that lie 2^33 bytes into their matrices, in the norm with its residual and in
+    both gradients; gradients over their inputs."""
+    T, d, V = 131073, 32768, 70001
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    g = rng(10)
+    a = torch.zeros(T, d, dtype=torch.bfloat16, device="cuda")
+    b = torch.zeros_like(a)
+    x, r, dy = (torch.randn(3, d, generator=g).bfloat16() for _ in range(3))
+    w = (1 + 0.3 * torch.randn(d, generator=g)).bfloat16()
+    a[-3:], b[-3:] = x.cuda(), r.cuda()
+    h = H.stream(x, r)
+    y, hd = sk.rms_norm(a, w.cuda(), b, out=(a, b))
+    H.check(y[-3:], H.norm(h, w, 1e-6, torch.bfloat16), "y")
+    assert torch.equal(hd[-3:].cpu(), h) and (y[:-3] == 0).all()
+    a[-3:] = dy.cuda()
+    dx, dw = sk.rms_norm_backward(a, b, w.cuda(), out=(a, torch.empty(d, device="cuda")))
+    wx, ww = H.norm_backward(dy, h, w, None, 1e-6)
+    H.check(dx[-3:], wx, "dx")
+    H.check(dw, ww, "dweight")
+    assert (dx[:-3] == 0).all()
+    del b, hd, y, dx
+    z = a.view(-1)[: T * d // V * V].view(-1, V)
+    rows = z.shape[0]
+    z[-2:] = torch.randn(2, V, generator=g).bfloat16().cuda()
+    last = z[-2:].clone()
+    labels = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    labels[-2:] = torch.tensor([5, V - 1], dtype=torch.int32)
+    gl, ge = torch.randn(2, rows, generator=g)
+    dz = sk.token_scores_backward(z, labels, gl.cuda(), ge.cuda(), out=z)
+    S = H.Scores(last, labels[-2:], 1.0)
+    H.check(dz[-2:], S.backward(labels[-2:], gl[-2:], ge[-2:]), "dlogits")
+    assert (dz[:-2] == 0).all()
