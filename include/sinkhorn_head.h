@@ -16,7 +16,14 @@
  *   - 0 <= T <= 2^24 rows.  With T == 0 the pointers of row arrays may be NULL.
  *   - Outputs and the workspace share no memory with one another or with inputs,
  *     but where an entry point says that an output may be an input itself: the
- *     same address and row distance.  Any other overlap is refused.
+ *     same address and row distance.  Any other overlap is refused, and so are
+ *     matrices of different row distances (in bytes) that lie between one another's rows.
+ *   - Precision.  Sums of squares and of products within a row of the norm are
+ *     fp64, the factor and the products with it fp32.  A row's exponentials and
+ *     the sums of a thread over them are fp32; the joins of those, logarithms
+ *     and log-probabilities are fp64 and rounded once.  A gradient value is an
+ *     fp32 exponential times fp32 coefficients: off, relative, by a few 2^-24 and
+ *     by 3 2^-24 of its distance s (M - z) from the row's maximum M, then rounded.
  *   - Same inputs at the same addresses modulo 128 bytes, same bits: no result
  *     depends on an order of atomics.
  *   - Every call enqueues kernels only and returns without waiting; it can be
@@ -60,7 +67,10 @@ size_t sinkhorn_head_workspace_bytes(int op, int T, int V, int k, int dtype);
  * alone, is its gradient.  h may be NULL (not written); without a residual it
  * is a copy of x.  eps in [1e-30, 1e30].
  * y or h may be x or the residual themselves (not both the same one).  Sums of
- * squares are fp64; y is rounded once.
+ * squares are fp64; the factor, its product with h and that with the weight are fp32,
+ * and y is rounded to the type behind them.  (Of rows whose root mean square is beyond
+ * 2^126 the factor lies below fp32's normal range: another 2^-22 of y, and of
+ * the parts of the gradient.)
  */
 int sinkhorn_rms_norm(const void *x, int dtype, int64_t ldx, const void *residual, int64_t ldr,
                       const void *weight, int T, int d, double eps, void *y, int64_t ldy,
@@ -97,7 +107,7 @@ int sinkhorn_quantize_int8(const void *x, int dtype, int64_t ldx, int T, int d, 
  * dx may be dy, dh or h itself.  Sums within a row are fp64; those of dweight
  * are fp32 over up to T / 1024 + 1 rows (rounded up to whole work-groups) and fp64 beyond.
  * u is fp32: where it lies below 1e36 and within fp32's normal range, any row of finite h has
- * its gradient.
+ * its gradient.  (The workspace is asked for without dweight, too.)
  */
 int sinkhorn_rms_norm_backward(const void *dy, int dtype, int64_t lddy, const void *h,
                                int64_t ldh, const void *weight, const void *dh, int64_t lddh,
@@ -111,8 +121,8 @@ int sinkhorn_rms_norm_backward(const void *dy, int dtype, int64_t lddy, const vo
  * 1 <= N <= 2^24, T N <= 2^37), out [T][N] in `dtype`, bias [N] fp32 or NULL.  Rows of x and w
  * start at multiples of 16 bytes (addresses and ldx, ldw): a row's last 16 bytes
  * are read whole, and what lies behind the row in them has no effect.
- * The sum is exact; the scales' product, its product with the sum and the bias's
- * addition are fp32, rounded once to the type.
+ * The sum is exact; its conversion (beyond 2^24 a rounding), the scales' product, their
+ * product with it and the bias's addition are fp32, rounded once to the type.
  */
 int sinkhorn_int8_linear(const int8_t *x, int64_t ldx, const float *xscale, const int8_t *w,
                          int64_t ldw, const float *wscale, const float *bias, int T, int K, int N,
@@ -133,7 +143,7 @@ int sinkhorn_int8_linear(const int8_t *x, int64_t ldx, const float *xscale, cons
  * entropy are 0 and its alternatives are empty.  A label of V or more gives a
  * logp of NaN alone.  A logit of -inf has no probability and is no alternative; an
  * empty place holds index -1 and best -inf, which sinkhorn_distill_loss takes as no
- * entry.  A row of nothing but -inf has logp 0, lse -inf, entropy 0.  A row with
+ * entry.  A row of nothing but -inf has logp 0 whatever its label, lse -inf, entropy 0.  A row with
  * NaN or +inf has logp, lse, entropy and best NaN; index then names the NaN
  * first, the infinities next.
  */

@@ -70,6 +70,28 @@ def test_weight_gradient_of_extreme_rows(size, grad, dt):
     H.check(dw, H.norm_backward(dy, h, w, None, 1e-30)[1], "dweight")
 
 
+@pytest.mark.parametrize("dt", TYPES)
+def test_norm_of_rows_whose_factor_is_subnormal(dt):
+    """Root mean squares beyond 2^126, whose inverse has fewer bits in fp32: off by 2^-150, at most
+    2^-22 of itself, once in y, and in the gradient in both factors of the projection and in one of u."""
+    g = rng(33)
+    top = torch.finfo(TYPES[dt]).max
+    h = torch.randn(9, 700, generator=g).sign() * (0.98 + 0.02 * torch.rand(9, 700, generator=g))
+    h = (h.double() * (torch.linspace(0.26, 1, 9)[:, None] * top)).to(TYPES[dt])
+    assert h.isfinite().all() and (h.double().square().mean(1).sqrt() > 2.0 ** 126).all()
+    dy = (h.sign() * (0.5 + torch.rand(9, 700, generator=g)) * 1e6).to(h.dtype)
+    w = torch.ones(700, dtype=h.dtype)
+    y, _ = sk.rms_norm(h.cuda(), w.cuda())
+    ref, tol = H.norm(h, w, 1e-6, h.dtype)
+    H.check(y, (ref, tol + 2.0 ** -22 * ref.abs()), "y")
+    dx, dw = sk.rms_norm_backward(dy.cuda(), h.cuda(), w.cuda())
+    (ref, tol), (wref, wtol) = H.norm_backward(dy, h, w, None, 1e-6, workers=9)
+    away = H.factor(h, 1e-6) * dy.double() - ref        # the projection
+    H.check(dx, (ref, tol + 2.0 ** -22 * (ref.abs() + away.abs()) * 1.01), "dx")
+    n = dy.double() * h.double() * H.factor(h, 1e-6)
+    H.check(dw, (wref, wtol + 2.0 ** -22 * n.abs().sum(0)), "dweight")
+
+
 # --- 8 bits to the last bit
 
 def nearest(p, a):
@@ -332,3 +354,16 @@ def test_gradients_of_rows_beyond_32_bit_offsets():
     S = H.Scores(last, labels[-2:], 1.0)
     H.check(dz[-2:], S.backward(labels[-2:], gl[-2:], ge[-2:]), "dlogits")
     assert (dz[:-2] == 0).all()
+
+
+def test_labels_of_rows_without_a_distribution():
+    """A row of nothing but -inf drops out whatever its label: logp 0, gradient 0, no alternatives."""
+    for T, V in ((4, 300), (4, 9000), (4, 70000)):
+        for dtype in TYPES.values():
+            z = torch.full((T, V), -math.inf, dtype=dtype, device="cuda")
+            y = torch.tensor([0, V - 1, V, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+            logp, lse, ent, index, best = sk.token_scores(z, y, top=3)
+            assert (logp == 0).all() and (lse == -math.inf).all() and (ent == 0).all()
+            assert (index == -1).all() and (best == -math.inf).all()
+            one = torch.ones(T, device="cuda")
+            assert (sk.token_scores_backward(z, y, one, one) == 0).all()
