@@ -437,8 +437,9 @@ template <typename O> __global__ __launch_bounds__(256) void join_kernel(Args g)
 // 128, two of them, where the tokens fill such tiles (4096 x 1024 to 131072 844 us against
 // 937 with 128 x 128 and 892 with 256 x 256, 1000 x 1000 to 30000 52 against 59 and 55), or
 // 128 x 128, three of them (333 x 1500 to 50001 51 us against 64 and 67).  For up to 64
-// tokens, whose tiles are read for the weights' sake, 64 x 128, or 64 x 64 where the
-// channels are few (40 x 8192 to 32000 45 against 49 us, 64 x 14336 to 4096 45 against 36).
+// tokens, whose tiles are read for the weights' sake, 64 x 128, or 64 x 64 split along K
+// where the channels are few (with weights that no cache holds, 64 x 64 and 64 x 128:
+// 64 x 14336 to 4096 26 and 75 us, 40 x 8192 to 32000 64 and 61, to 50000 116 and 97).
 enum Shape { kStream, kTiles64, kTiles64x128, kTiles128, kTiles256x128, kTiles256 };
 long tiles_of(int T, int N, int BT, int BN) { return ((long)T + BT - 1) / BT * (((long)N + BN - 1) / BN); }
 Shape shape_of(int T, int K, int N)

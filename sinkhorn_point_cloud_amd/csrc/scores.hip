@@ -10,14 +10,16 @@
 // it rises by g / c, W becomes 2^-g (W + g (R + 1)).  Both parts of H keep their
 // relative precision where one token has nearly all of the probability.
 //
-// The alternatives: the `top`-th largest of the threads' own maxima is a lower bound
-// of the row's `top`-th largest value, and little more than `top` values lie at or
-// above it (in random order about top + top^2 / 2 NT).  They are listed in shared
-// memory and ranked there by value and index, so the order in which they were listed
-// does not matter.  Each thread keeps the maxima of up to 8 groups of its chunks, and
-// only groups that reach the bound are read again.  A row of which more do not fit
-// (many equal values, or the large ones all in one thread's chunks) has its `top`-th
-// value found by bisection first (rows of one value: 940 us).
+// The alternatives: of the threads' own maxima, joined to G = 64 for up to 16
+// alternatives and to 256 for more, the `top`-th largest is a lower bound of the row's
+// `top`-th largest value.  In random order about -G ln(1 - top / G) values lie above
+// it: 18 for 16 alternatives, 177 for 128 (and those that differ from it in the lower 16
+// bits of their keys alone).  They are listed in shared memory and ranked there by value
+// and index, so the order in which they were listed does not matter.  Each thread keeps
+// the maxima of up to 8 groups of its chunks, and only groups that reach the bound are
+// read again.  A row of which more do not fit (many equal values, or the large ones all
+// in one thread's chunks) has its `top`-th entry found by bisection first (4096 rows of
+// 131072 bf16 values, each of one value: 940 us).
 //
 // What bounds it: HBM.  (A row kept in registers for the second look leaves a compute
 // unit no other row to load meanwhile: 4096 rows of 131072 bf16 values with 64
@@ -229,8 +231,9 @@ __device__ __forceinline__ void append(ListRoom<NT> &room, bool wanted, uint64_t
 }
 
 // This thread's largest key; then, behind a barrier, the border of the list, by one wave.
-// 64 maxima for up to 16 alternatives, 256 for more: little more is listed than with
-// a maximum of each thread, and the bisection is as much shorter.
+// 64 maxima for up to 16 alternatives, 256 for more: at 128 alternatives some 177 values
+// are listed, with the maxima of 1024 threads it would be 137, and the bisection is as
+// much shorter.
 template <int NT> __device__ __forceinline__ void set_key(ListRoom<NT> &room, uint32_t most)
 {
     room.keys[threadIdx.x] = most;
