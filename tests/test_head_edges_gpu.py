@@ -44,6 +44,10 @@ def extreme_case(dt, d, g):
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("d", [37, 515, 2501, 20000])
 def test_norm_gradient_of_extreme_rows(d, dt):
+    """dx = r (u - n m) + dh in fp32: u is off by U, n by 2 U (r and its product), m by U and what u's
+    roundings bring to its sum, the inner difference and r by U of it each, the whole by U.  That is
+    U |r u| + 3 U |r n m| + 2 U |v| + U |dx| beside the sum's part, against the formula's 3 U |r u| + 2 U
+    |r n m| + 2 U |v| + 2 U |dx|: within it, since |r n m| <= |r u| + |dx| without dh."""
     h, dy, w = extreme_case(dt, d, rng(d))
     for weight in (w, None):
         wd = None if weight is None else weight.cuda()
